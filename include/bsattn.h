@@ -17,6 +17,10 @@
  *                             memory into a GPU block cache (the offload path)
  *   bs_cpu_sparse_attn,       attention of a block subset on the host cores, and the
  *   bs_lse_merge              GPU merge of two partial results (CPU/GPU split)
+ *   bs_quant_append           new tokens' K and V quantised into the pages of an 8-bit
+ *                             cache (BS_E4M3 or BS_INT8 codes, one scale per page)
+ *   bs_pages_reserve, _fork,  pages of a cache handed out, shared between sequences,
+ *   _free, _compact, _copy    taken back, and moved together, all on the device
  *
  * Method sources: "Technisches Resümee: NOSA: Native und Offloadable Sparse
  * Attention" (section Methodik: "1. Algorithmus: NOSA" and "2. System: NOSI") and
@@ -49,6 +53,9 @@
  * Data layout (dims below are the fields of bs_dims)
  * ----------------------------------------------------
  *   K, V pools     [n_pages][page_size=16][head_dim], kv_dtype; 16-byte aligned base.
+ *   K, V scales    float32 [n_pages], 8-bit caches only: a page belongs to one unit, so
+ *                  this is a scale for each block of 16 tokens and KV head. The value of
+ *                  a code c of page p is c * scale[p] (finite, >= 0).
  *   page_table     int32 [units][max_pages_per_unit]; entry p of unit u is the
  *                  physical page holding tokens [16p, 16p+16) of that unit.
  *   seq_lens       int32 [batch]; T = tokens in the cache including the current
@@ -88,7 +95,10 @@ typedef enum {
   BS_ERR_TIMEOUT = 7        /* (device) a bounded wait ran out */
 } bs_status;
 
-typedef enum { BS_BF16 = 0, BS_FP32 = 1 } bs_dtype;
+/* BS_E4M3 (float8 e4m3fn: 4 exponent bits, 3 mantissa bits, largest value 448, no
+ * infinities) and BS_INT8 (signed, -127..127) are storage types of the K and V pools
+ * only (bs_dims.kv_dtype), each with one scale per page; queries are BS_BF16 or BS_FP32. */
+typedef enum { BS_BF16 = 0, BS_FP32 = 1, BS_E4M3 = 2, BS_INT8 = 3 } bs_dtype;
 
 /* Head classes (Fluxion, Kerninzichten item 2: streaming vs retrieval heads;
  * NOSA, Dual-Selection-Mechanismus: query-aware plus query-agnostic selection). */
@@ -113,11 +123,14 @@ typedef struct {
   bs_dtype kv_dtype, q_dtype;
 } bs_dims;
 
-/* Paged KV cache: device pointers. */
+/* Paged KV cache: device pointers. k_scale and v_scale are the page scales of an 8-bit
+ * cache (kv_dtype BS_E4M3 or BS_INT8; required there, v_scale not by
+ * bs_build_block_summaries) and not looked at otherwise. */
 typedef struct {
   const void *k_pool, *v_pool;
   const int32_t *page_table;
   const int32_t *seq_lens;
+  const float *k_scale, *v_scale;   /* [n_pages] */
 } bs_kv;
 
 /* Per-unit head properties, struct of arrays of length batch * n_kv_heads, device
@@ -154,7 +167,10 @@ bs_status bs_check_head_cfg(const bs_dims *dims, const bs_head_cfg *cfg_host,
  * [tok_begin[b], seq_lens[b]): kbar_j = (1/n_j) sum of K[t] over the n_j tokens of
  * [j*s, min((j+1)*s, T)), summed in token order in fp32. A decode step passes
  * tok_begin = T-1 (one sub-block per unit); a prefill passes 0. The result does not
- * depend on how the range was split across calls.
+ * depend on how the range was split across calls. 8-bit caches: K[t] is its code times
+ * its page's scale, and because an append may round the codes of the page it starts in
+ * again (bs_quant_append), every sub-block with a token of the page that holds
+ * tok_begin[b] is recomputed too.
  * tok_begin: device int32 [batch]. max_new_tokens (host): an upper bound on
  * seq_lens[b] - tok_begin[b], used only to size the grid. */
 bs_status bs_build_block_summaries(const bs_dims *dims, const bs_kv *kv, const bs_head_cfg *cfg,
@@ -217,6 +233,10 @@ bs_status bs_select_topk(const bs_dims *dims, const bs_head_cfg *cfg, const int3
  *     others leave at once; the merge is the same, as their records were empty).
  * A unit's plan depends on its own sizes only, so a sub-batch launched with the same S
  * gives bitwise the same per-unit results as the full batch.
+ * 8-bit caches: K[t] and V[t] are codes times their page's scale. The products are
+ * accurate to fp32 (codes are exact in fp16; each query row is scaled by a power of two
+ * and, like the probabilities, enters as fp16 parts hi + lo), whatever the scales. A
+ * page whose block logit is -inf is not read; NaN codes in tokens past T do not count.
  * workspace: device scratch of at least bs_workspace_size(dims) bytes, 16-byte
  * aligned. It starts with four int32 words per unit (padded to 16 bytes): the fused
  * step's selection tickets, the attention's arrival tickets, the fused step's published
@@ -359,7 +379,8 @@ typedef struct {
   int32_t pages_per_slot;       /* >= g/16 of every unit */
 } bs_block_cache;
 
-/* One step's swap for every unit: first every block of `removed` leaves the cache
+/* (Not for 8-bit caches: BS_ERR_INVALID_ARG.)
+ * One step's swap for every unit: first every block of `removed` leaves the cache
  * (its slot is freed, its page-table entries become -1); then the blocks of `added`
  * (ascending) take the free slots in ascending slot order, their page-table entries
  * are set, and the pages of each added block that hold tokens (< T) are copied, K and
@@ -397,7 +418,8 @@ typedef struct {
   int32_t max_blocks_per_unit;  /* row length of evict_bias (used only when it is set) */
 } bs_host_tables;
 
-/* Attention of each unit's listed blocks (tokens clipped to T) on the host cores,
+/* (Not for 8-bit caches: BS_ERR_INVALID_ARG.)
+ * Attention of each unit's listed blocks (tokens clipped to T) on the host cores,
  * fp32 arithmetic, units spread over n_threads threads; synchronous. Everything is
  * HOST memory: q ([batch][n_q_heads][head_dim], q_dtype), the pools of `kv` (its
  * page_table field is not used; `tables` gives the host page table), sel_idx
@@ -416,6 +438,132 @@ bs_status bs_cpu_sparse_attn(const bs_dims *dims, const void *q, const bs_host_k
  * empty sides give a zero row and -inf. out / lse may be out_a / lse_a (in place). */
 bs_status bs_lse_merge(const bs_dims *dims, const float *out_a, const float *lse_a, const float *out_b,
                        const float *lse_b, float *out, float *lse, bs_stream_t stream);
+
+/* ------------------------------------------------------------------------------
+ * Writing an 8-bit cache. ("Technisches Resümee: NOSA", 2. System: NOSI keeps the cache
+ * in minimal block units and works on it as tokens are written; the storage type is not
+ * the page's.)
+ * ------------------------------------------------------------------------------ */
+
+/* K and V pools that a call writes, with the page scales of an 8-bit cache (NULL and
+ * unused otherwise). Device pointers. */
+typedef struct {
+  void *k_pool, *v_pool;        /* [n_pages][16][head_dim], kv_dtype, 16-byte aligned */
+  float *k_scale, *v_scale;     /* [n_pages] */
+} bs_pools;
+
+/* Quantises new tokens into the pages of an 8-bit cache (kv_dtype BS_E4M3 or BS_INT8).
+ * Token t of sequence b, tok_begin[b] <= t < seq_lens[b], is row row_begin[b] + t -
+ * tok_begin[b] of k_new and v_new: n_rows rows of row_stride elements (q_dtype: BS_BF16
+ * or BS_FP32), KV head h at [h * head_dim, (h + 1) * head_dim), so that K and V may be
+ * columns of one fused projection's output. It goes to slot t % 16 of the page that
+ * page_table names for t / 16; that page must be no other unit's (see bs_pages_fork).
+ * For each page, K and V apart, with x the new values of the page:
+ *   a = the largest |x| that is finite;  f(a) = 0 when a = 0, else
+ *     BS_E4M3: the smallest power of two with a / f(a) <= 448,
+ *     BS_INT8: a / 127 rounded to fp32;   both at least 2^-126;
+ *   s = f(a) when the page held no token of the sequence before, else max(old scale, f(a));
+ *   code of x = Q(x / s), the fp32 quotient rounded to the nearest code, ties to even,
+ *     and cut to the largest magnitude (448, 127); NaN gives NaN (BS_E4M3) or 0 (BS_INT8);
+ *     0 when s = 0;
+ *   when s grew, the codes c already there become Q(c * old scale / s) (in fp32).
+ * Slots of the page past seq_lens[b] keep what they hold. With BS_E4M3 the scales are
+ * powers of two: rounding a page again changes only codes that become subnormal.
+ * page_table int32 [units][max_pages_per_unit]; seq_lens, tok_begin, row_begin int32
+ * [batch]; tok_begin[b] = seq_lens[b] appends nothing for b (row_begin[b] is not read).
+ * max_new_tokens (host): an upper bound on seq_lens[b] - tok_begin[b]; sizes the grid
+ * only. k_new and v_new 16-byte aligned, row_stride >= n_kv_heads * head_dim and a
+ * multiple of 16 bytes. A sequence whose rows or lengths do not fit (tok_begin < 0 or
+ * above seq_lens: BS_ERR_INVALID_ARG; more pages than a row: BS_ERR_CAPACITY; rows
+ * outside [0, n_rows): BS_ERR_DEVICE_BOUNDS) is skipped, and so is a page outside the
+ * pool (BS_ERR_DEVICE_BOUNDS). One launch; bitwise reproducible. */
+bs_status bs_quant_append(const bs_dims *dims, const bs_pools *pools, const int32_t *page_table,
+                          const int32_t *seq_lens, const int32_t *tok_begin, const int32_t *row_begin,
+                          const void *k_new, const void *v_new, int64_t row_stride, int64_t n_rows,
+                          int32_t max_new_tokens, int32_t *dev_status, bs_stream_t stream);
+
+/* ------------------------------------------------------------------------------
+ * Pages of a cache, handed out and taken back on the device. A page is free when no
+ * page-table entry holds it (ref_count 0). Nothing waits for the GPU, so these calls
+ * stand between decode steps, in a captured graph too. Calls on one map, and other
+ * calls that read or write what it points to, must be ordered (one stream). The calls
+ * work on the table only; bs_pages_copy then moves the data, once for each layer that
+ * shares the table. They use batch, n_kv_heads, max_pages_per_unit and n_pages of the
+ * dims (which must be valid as a whole); any kv_dtype.
+ * Which free page is taken is fixed: the k-th page asked for (ascending unit, then
+ * ascending logical page) gets the k-th lowest free page.
+ * reserve and fork do all of their work or none: a call that reports an error leaves the
+ * map as it was (and *count = 0).
+ * ------------------------------------------------------------------------------ */
+
+/* Device pointers; all in/out. */
+typedef struct {
+  int32_t *page_table;  /* [units][max_pages_per_unit]: page of each logical page, -1 none */
+  int32_t *ref_count;   /* [n_pages]: page-table entries that hold the page, >= 0 */
+  int32_t *seq_lens;    /* [batch]: tokens of each sequence (0: an empty slot) */
+} bs_page_map;
+
+/* Pages to copy (device memory, written by fork and compact): *count pairs (source page,
+ * destination page). Within one list no page is a destination twice or a source and a
+ * destination. */
+typedef struct {
+  int32_t *pairs;       /* [capacity][2], 8-byte aligned */
+  int32_t *count;
+  int32_t capacity;     /* host value: pairs that fit */
+} bs_page_copies;
+
+/* Scratch of reserve, fork and compact for these dims (0 on bad dims): 16-byte aligned,
+ * overwritten by every call, needs no clearing. Calls that share it must be ordered. */
+size_t bs_pages_workspace_size(const bs_dims *dims);
+
+/* Every entry of a unit of sequence b below ceil(new_lens[b] / 16) that holds no page
+ * gets a free one (ref_count 1). new_lens (device int32 [batch]) may be map->seq_lens;
+ * <= 0 asks for nothing; the lengths themselves are not written. Too few free pages, or
+ * a length beyond the row: BS_ERR_CAPACITY, nothing changes. Two launches. */
+bs_status bs_pages_reserve(const bs_dims *dims, const bs_page_map *map, const int32_t *new_lens, void *workspace,
+                           size_t workspace_bytes, int32_t *dev_status, bs_stream_t stream);
+
+/* Sequence slot dst[i] becomes a copy of sequence src[i], for i < n (device int32 [n]; a
+ * negative src[i] or dst[i] skips i): its length is src's, its units share src's full
+ * pages (their counts grow), and the partial last page, where tokens will be appended,
+ * gets a free page of its own with a pair (src's page, the free page) in `copies`, in
+ * order of i, then KV head. Logical pages of src past its length are not shared; an
+ * entry of src that holds no page (-1) stays -1.
+ * One src may have many dst. Every dst must be an empty slot (no page in its rows), named
+ * once, and be no src of the same call; both in [0, batch): else BS_ERR_INVALID_ARG.
+ * BS_ERR_CAPACITY for too few free pages or a src length beyond its row (src length < 0:
+ * BS_ERR_INVALID_ARG), BS_ERR_DEVICE_BOUNDS for a shared entry outside the pool or a
+ * free page (count 0): nothing changes. copies->capacity >= n * n_kv_heads (checked on
+ * the host: BS_ERR_CAPACITY); 1 <= n <= batch. Two launches. */
+bs_status bs_pages_fork(const bs_dims *dims, const bs_page_map *map, const int32_t *src, const int32_t *dst, int32_t n,
+                        const bs_page_copies *copies, void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                        bs_stream_t stream);
+
+/* The sequences seqs[i], i < n (device int32 [n]), give up their pages: each entry of
+ * their rows becomes -1 and its page's count falls by one; their lengths become 0. A
+ * negative seqs[i] is skipped, a sequence named twice is freed once. An entry outside
+ * the pool, or whose page has count 0, is dropped with BS_ERR_DEVICE_BOUNDS; a seqs[i]
+ * >= batch is skipped with BS_ERR_INVALID_ARG; the rest is done. 1 <= n <= batch. One
+ * launch. */
+bs_status bs_pages_free(const bs_dims *dims, const bs_page_map *map, const int32_t *seqs, int32_t n,
+                        int32_t *dev_status, bs_stream_t stream);
+
+/* Moves the pages in use together: with N pages in use (count > 0), the k-th lowest of
+ * those at or above N moves to the k-th lowest free page below N. Table entries and
+ * counts follow, the moves are listed in `copies`, and *n_live (device int32) = N: pages
+ * [N, n_pages) are free. At most n_pages / 2 moves; more than copies->capacity:
+ * BS_ERR_CAPACITY and nothing moves (*count = 0, *n_live is still written). An entry
+ * outside the pool, or one at or above N on a free page, is left as it is with
+ * BS_ERR_DEVICE_BOUNDS; the rest is done. Three launches. */
+bs_status bs_pages_compact(const bs_dims *dims, const bs_page_map *map, const bs_page_copies *copies, int32_t *n_live,
+                           void *workspace, size_t workspace_bytes, int32_t *dev_status, bs_stream_t stream);
+
+/* Copies the listed pages of one layer's K and V pools (any kv_dtype; 8-bit caches: and
+ * their scales). copies->count is read on the device, at most copies->capacity pairs are
+ * taken. A pair with a page outside the pool is skipped with BS_ERR_DEVICE_BOUNDS. One
+ * launch. */
+bs_status bs_pages_copy(const bs_dims *dims, const bs_pools *pools, const bs_page_copies *copies, int32_t *dev_status,
+                        bs_stream_t stream);
 
 /* Bytes of workspace bs_sparse_decode_attn needs for these dims (0 on bad dims). */
 size_t bs_workspace_size(const bs_dims *dims);

@@ -26,7 +26,7 @@ BS_ERR_CUDA = 5
 BS_ERR_DEVICE_BOUNDS = 6
 BS_ERR_TIMEOUT = 7
 # bs_dtype, bs_head_class, bs_group_reduce
-BS_BF16, BS_FP32 = 0, 1
+BS_BF16, BS_FP32, BS_E4M3, BS_INT8 = 0, 1, 2, 3
 BS_STREAMING, BS_RETRIEVAL, BS_DUAL = 0, 1, 2
 BS_GROUP_MAX, BS_GROUP_MEAN = 0, 1
 
@@ -42,7 +42,7 @@ class Dims(ctypes.Structure):
 
 class KV(ctypes.Structure):
     _fields_ = [("k_pool", ctypes.c_void_p), ("v_pool", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
-                ("seq_lens", ctypes.c_void_p)]
+                ("seq_lens", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
 
 
 class HeadCfg(ctypes.Structure):
@@ -76,6 +76,19 @@ class BlockCache(ctypes.Structure):
 class HostTables(ctypes.Structure):
     _fields_ = [("page_table", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p), ("block_tokens", ctypes.c_void_p),
                 ("evict_bias", ctypes.c_void_p), ("max_blocks_per_unit", ctypes.c_int32)]
+
+
+class Pools(ctypes.Structure):
+    _fields_ = [("k_pool", ctypes.c_void_p), ("v_pool", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p)]
+
+
+class PageMap(ctypes.Structure):
+    _fields_ = [("page_table", ctypes.c_void_p), ("ref_count", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p)]
+
+
+class PageCopies(ctypes.Structure):
+    _fields_ = [("pairs", ctypes.c_void_p), ("count", ctypes.c_void_p), ("capacity", ctypes.c_int32)]
 
 
 class BsError(RuntimeError):
@@ -112,6 +125,20 @@ _SIGS = {
                                           ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int]),
     "bs_lse_merge": (ctypes.c_int, [_P(Dims), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
                                     ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]),
+    "bs_quant_append": (ctypes.c_int, [_P(Dims), _P(Pools), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                       ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64,
+                                       ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p]),
+    "bs_pages_workspace_size": (ctypes.c_size_t, [_P(Dims)]),
+    "bs_pages_reserve": (ctypes.c_int, [_P(Dims), _P(PageMap), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t,
+                                        ctypes.c_void_p, ctypes.c_void_p]),
+    "bs_pages_fork": (ctypes.c_int, [_P(Dims), _P(PageMap), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32,
+                                     _P(PageCopies), ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p,
+                                     ctypes.c_void_p]),
+    "bs_pages_free": (ctypes.c_int, [_P(Dims), _P(PageMap), ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
+                                     ctypes.c_void_p]),
+    "bs_pages_compact": (ctypes.c_int, [_P(Dims), _P(PageMap), _P(PageCopies), ctypes.c_void_p, ctypes.c_void_p,
+                                        ctypes.c_size_t, ctypes.c_void_p, ctypes.c_void_p]),
+    "bs_pages_copy": (ctypes.c_int, [_P(Dims), _P(Pools), _P(PageCopies), ctypes.c_void_p, ctypes.c_void_p]),
     "bs_workspace_size": (ctypes.c_size_t, [_P(Dims)]),
     "bs_decode_step_launches": (ctypes.c_int, [_P(Dims)]),
     "bs_set_wait_limit_ns": (ctypes.c_int, [ctypes.c_uint64]),
@@ -169,6 +196,10 @@ def _stream(stream) -> int | None:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
+def _nbytes(t) -> int:
+    return t.numel() * t.element_size()
+
+
 def check_head_cfg(dims: Dims, cfg_host: HeadCfg, seq_lens_host) -> int:
     """Host-side check of a head configuration held in host memory; returns the status."""
     return lib().bs_check_head_cfg(ctypes.byref(dims), ctypes.byref(cfg_host), _ptr(seq_lens_host))
@@ -197,11 +228,10 @@ def sparse_decode_attn(dims, q, kv, cfg, sel_idx, sel_cnt, out, lse, workspace, 
                        evict_bias=None):
     """a4. evict_bias (None: plain softmax) is the ED-DMA logit bias of every block,
     fp32 [units][max_blocks_per_unit] on the device."""
-    nbytes = workspace.numel() * workspace.element_size()
     _check("bs_sparse_decode_attn",
            lib().bs_sparse_decode_attn(ctypes.byref(dims), _ptr(q), ctypes.byref(kv), ctypes.byref(cfg),
                                        _ptr(sel_idx), _ptr(sel_cnt), _ptr(evict_bias), _ptr(out), _ptr(lse),
-                                       _ptr(workspace), nbytes, _ptr(dev_status), _stream(stream)))
+                                       _ptr(workspace), _nbytes(workspace), _ptr(dev_status), _stream(stream)))
 
 
 def block_setdiff(dims, prev_idx, prev_cnt, cur_idx, cur_cnt, added, added_cnt, removed, removed_cnt, dev_status,
@@ -248,6 +278,57 @@ def lse_merge(dims, out_a, lse_a, out_b, lse_b, out, lse, stream=None):
     """Merge two partial attention results over disjoint token sets (device memory)."""
     _check("bs_lse_merge", lib().bs_lse_merge(ctypes.byref(dims), _ptr(out_a), _ptr(lse_a), _ptr(out_b),
                                               _ptr(lse_b), _ptr(out), _ptr(lse), _stream(stream)))
+
+
+def quant_append(dims, pools: Pools, page_table, seq_lens, tok_begin, row_begin, k_new, v_new, row_stride: int,
+                 n_rows: int, max_new_tokens: int, dev_status, stream=None):
+    """Quantise new tokens' K and V into the pages of an 8-bit cache."""
+    _check("bs_quant_append",
+           lib().bs_quant_append(ctypes.byref(dims), ctypes.byref(pools), _ptr(page_table), _ptr(seq_lens),
+                                 _ptr(tok_begin), _ptr(row_begin), _ptr(k_new), _ptr(v_new), int(row_stride),
+                                 int(n_rows), int(max_new_tokens), _ptr(dev_status), _stream(stream)))
+
+
+def pages_reserve(dims, page_map: PageMap, new_lens, workspace, dev_status, stream=None):
+    """Free pages for every entry below ceil(new_lens / 16) that holds none."""
+    _check("bs_pages_reserve",
+           lib().bs_pages_reserve(ctypes.byref(dims), ctypes.byref(page_map), _ptr(new_lens), _ptr(workspace),
+                                  _nbytes(workspace), _ptr(dev_status), _stream(stream)))
+
+
+def pages_fork(dims, page_map: PageMap, src, dst, copies: PageCopies, workspace, dev_status, stream=None):
+    """Slots dst become copies of sequences src: full pages shared, partial last pages listed in copies."""
+    if src.numel() != dst.numel():
+        raise ValueError(f"src and dst differ in length: {src.numel()} and {dst.numel()}")
+    _check("bs_pages_fork",
+           lib().bs_pages_fork(ctypes.byref(dims), ctypes.byref(page_map), _ptr(src), _ptr(dst), src.numel(),
+                               ctypes.byref(copies), _ptr(workspace), _nbytes(workspace), _ptr(dev_status),
+                               _stream(stream)))
+
+
+def pages_free(dims, page_map: PageMap, seqs, dev_status, stream=None):
+    """The sequences give up their pages; their lengths become 0."""
+    _check("bs_pages_free",
+           lib().bs_pages_free(ctypes.byref(dims), ctypes.byref(page_map), _ptr(seqs), seqs.numel(),
+                               _ptr(dev_status), _stream(stream)))
+
+
+def pages_compact(dims, page_map: PageMap, copies: PageCopies, n_live, workspace, dev_status, stream=None):
+    """Moves the pages in use below their number, n_live; the moves are listed in copies."""
+    _check("bs_pages_compact",
+           lib().bs_pages_compact(ctypes.byref(dims), ctypes.byref(page_map), ctypes.byref(copies), _ptr(n_live),
+                                  _ptr(workspace), _nbytes(workspace), _ptr(dev_status), _stream(stream)))
+
+
+def pages_copy(dims, pools: Pools, copies: PageCopies, dev_status, stream=None):
+    """Copies the listed pages (and their scales) of one layer's pools."""
+    _check("bs_pages_copy",
+           lib().bs_pages_copy(ctypes.byref(dims), ctypes.byref(pools), ctypes.byref(copies), _ptr(dev_status),
+                               _stream(stream)))
+
+
+def pages_workspace_size(dims) -> int:
+    return int(lib().bs_pages_workspace_size(ctypes.byref(dims)))
 
 
 def workspace_size(dims) -> int:

@@ -6,6 +6,7 @@
 
 #include "bs_attn_plan.cuh"
 #include "bs_internal.cuh"
+#include "bs_quant.cuh"
 
 namespace bsi {
 
@@ -23,7 +24,7 @@ bs_status check_dims(const bs_dims *d) {
   if (G > kMaxG) return BS_ERR_SHAPE;
   if (d->head_dim != 64 && d->head_dim != 128) return BS_ERR_SHAPE;
   if (d->page_size != kPage) return BS_ERR_SHAPE;
-  if (d->kv_dtype != BS_BF16 && d->kv_dtype != BS_FP32) return BS_ERR_INVALID_ARG;
+  if (d->kv_dtype != BS_BF16 && d->kv_dtype != BS_FP32 && !is_quant(d->kv_dtype)) return BS_ERR_INVALID_ARG;
   if (d->q_dtype != BS_BF16 && d->q_dtype != BS_FP32) return BS_ERR_INVALID_ARG;
   if (d->max_pages_per_unit < 1 || d->max_blocks_per_unit < 1 || d->max_sel_per_unit < 1 ||
       d->max_subs_per_unit < 1 || d->max_gather_pages_per_unit < 1 || d->n_pages < 1)

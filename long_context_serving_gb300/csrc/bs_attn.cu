@@ -2,6 +2,7 @@
 // kernels are in bs_attn_bf16.cu (bf16 caches: tiled TMA and tensor-core MMA) and
 // bs_attn_f32.cu (fp32 caches), their device code in bs_attn_impl.cuh.
 #include "bs_attn_launch.cuh"
+#include "bs_quant.cuh"
 
 namespace bsi {
 namespace {
@@ -28,7 +29,7 @@ bs_status launch_standalone(const bs_dims *dims, const void *q, const bs_kv *kv,
   a.expect = nullptr;
   a.st = st;
   a.wait_ns = wait_limit_ns();
-  return dims->kv_dtype == BS_BF16 ? launch_attn_bf16(a, false, cs) : launch_attn_f32(a, false, cs);
+  return launch_attn(a, false, cs);
 }
 
 }  // namespace
@@ -44,6 +45,7 @@ extern "C" bs_status bs_sparse_decode_attn(const bs_dims *dims, const void *q, c
   if (!q || !kv || !cfg || !kv->k_pool || !kv->v_pool || !kv->page_table || !kv->seq_lens || !cfg->block_tokens ||
       !sel_idx || !sel_cnt || !out || !lse || !workspace || !dev_status)
     return BS_ERR_INVALID_ARG;
+  if (is_quant(dims->kv_dtype) && (!kv->k_scale || !kv->v_scale)) return BS_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(kv->k_pool) || !aligned16(kv->v_pool) || !aligned16(out) ||
       !aligned16(workspace))
     return BS_ERR_ALIGN;
@@ -103,6 +105,7 @@ extern "C" bs_status bs_sparse_decode_attn_noalloc(const bs_dims *dims, const vo
   if (!q || !kv || !cfg || !kv->k_pool || !kv->v_pool || !kv->page_table || !kv->seq_lens || !cfg->block_tokens ||
       !sel_idx || !sel_cnt || !out || !lse || !dev_status)
     return BS_ERR_INVALID_ARG;
+  if (is_quant(dims->kv_dtype) && (!kv->k_scale || !kv->v_scale)) return BS_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(kv->k_pool) || !aligned16(kv->v_pool) || !aligned16(out)) return BS_ERR_ALIGN;
   const size_t need = bs_workspace_size(dims);
   if (need > kFixedScratchBytes) return BS_ERR_CAPACITY;

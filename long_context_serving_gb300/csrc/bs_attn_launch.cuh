@@ -29,6 +29,16 @@ struct AttnArgs {
 // kernel (streaming units run ahead, the rest wait for their unit's selection).
 bs_status launch_attn_bf16(const AttnArgs &a, bool step, cudaStream_t cs);
 bs_status launch_attn_f32(const AttnArgs &a, bool step, cudaStream_t cs);
+bs_status launch_attn_quant(const AttnArgs &a, bool step, cudaStream_t cs);   // E4M3 and INT8 caches
+
+// By the cache's storage type.
+inline bs_status launch_attn(const AttnArgs &a, bool step, cudaStream_t cs) {
+  switch (a.dims.kv_dtype) {
+    case BS_BF16: return launch_attn_bf16(a, step, cs);
+    case BS_FP32: return launch_attn_f32(a, step, cs);
+    default: return launch_attn_quant(a, step, cs);
+  }
+}
 
 // About two CTAs per SM of the current device (the attention's split target).
 inline int attn_target_ctas() {

@@ -1,0 +1,434 @@
+// Attention over 8-bit caches (E4M3 or INT8 codes, one fp32 scale per page for K and one
+// for V): the kernels and their launcher. The unit's block list, the split plan and the
+// merges are those of the other caches (bs_attn_impl.cuh); only the page math differs.
+//
+// With ks, vs the scales of token t's page and K8, V8 its codes:
+//   x_h(t) = ks (q_h . K8[t]) log2(e) / sqrt(d) + bias2,   o_h += vs (2^(x_h(t) - m) V8[t]).
+//
+// A warp takes whole pages and keeps everything in registers; no shared memory and no CTA
+// barrier in the loop. The codes come straight from global memory in 16-byte loads (D = 64:
+// V in 8-byte ones), the next page's in flight while one is computed: 2 D bytes of K and V
+// a token leave too little arithmetic per byte for staging through shared memory to pay, and
+// each lane needs its own bytes only. Fragment layouts are chosen around those loads; lane
+// = 4 r + c:
+//   K: lane holds 16-byte chunks c (and c + 4) of tokens r and r + 8. A k-step of the MMA may
+//     take any 16 dimensions as long as q agrees, so the four words of a chunk feed four
+//     k-steps: S[16 x 8] = q K8^T with the heads as rows (rows 8..15: the low parts of q,
+//     for an fp32 query) and eight tokens as columns, two such tiles a page.
+//   S leaves lane (r, c) with head r, tokens 2c, 2c + 1, 8 + 2c, 9 + 2c: already the B
+//     fragment of P^T in O^T = V8^T P^T (k = tokens, n = heads).
+//   V: lane holds chunk r (D / 8 dimensions) of those same four tokens, and pairs the tokens'
+//     bytes with one byte permutation per four codes before converting.
+// Precision: the codes are exact in fp16; a query row is multiplied by a power of two that
+// brings its largest element near 2^14 and enters as fp16 hi + lo (bf16 queries: hi alone is
+// exact down to 2^-39 of the row's largest element); P is scaled by 2^14 and enters as hi +
+// lo, so that weights down to 2^-28 of the largest keep 22 bits; sums are fp32. The V scale is
+// applied to each page's product in fp32, so no scale can leave fp16's range.
+#include "bs_attn_impl.cuh"
+#include "bs_attn_launch.cuh"
+#include "bs_quant.cuh"
+
+namespace bsi {
+namespace {
+
+constexpr int kQuantThreads = 128;   // 4 warps
+constexpr int kQuantWarps = kQuantThreads / 32;
+constexpr float kPShift = 14.0f;     // P enters as 2^(x - m + 14)
+
+// Shared memory: the staged selection entries, then (after the loop) the warps' states.
+template <int D>
+struct QuantLayout {
+  static constexpr int kOffO = kSelPreload * 4;                              // [4][8][D]
+  static constexpr int kOffMl = kOffO + kQuantWarps * kMaxG * D * 4;         // m, l: [2][4][8]
+  static constexpr int kOffSum = kOffMl + 2 * kQuantWarps * kMaxG * 4;       // [8][D]
+  static constexpr int kOffScratch = kOffSum + kMaxG * D * 4;                // merge scratch
+  static constexpr int kBytes = kOffScratch + 3 * kMaxG * kAttnMaxSplits * 4;
+};
+
+// D = A B + D, m16n8k16, fp16 inputs, fp32 accumulators.
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                        uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float f16_lo_f(uint32_t w) { return __half2float(__ushort_as_half(w & 0xffffu)); }
+__device__ __forceinline__ float f16_hi_f(uint32_t w) { return __half2float(__ushort_as_half(w >> 16)); }
+
+// The codes of one page that a lane holds.
+template <int D>
+struct PageRegs {
+  uint4 k[D / 64][2];                                                       // [chunk c, c + 4][token r, r + 8]
+  uint32_t v[4][D / 32];                                                    // tokens 2c, 2c+1, 2c+8, 2c+9
+};
+struct PageMeta {
+  int valid;        // tokens that count (0: the page is skipped)
+  float ks, vs, bias2;
+};
+
+template <int D>
+__device__ __forceinline__ void load_page(const uint8_t *kpg, const uint8_t *vpg, PageRegs<D> &p) {
+  const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+#pragma unroll
+  for (int j = 0; j < D / 64; ++j)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) p.k[j][i] = ldg_stream16(kpg + (r + 8 * i) * D + (c + 4 * j) * 16);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint8_t *src = vpg + (2 * c + (i & 1) + 8 * (i >> 1)) * D + r * (D / 8);
+    if constexpr (D == 128) {
+      const uint4 w = ldg_stream16(src);
+      p.v[i][0] = w.x; p.v[i][1] = w.y; p.v[i][2] = w.z; p.v[i][3] = w.w;
+    } else {
+      const uint2 w = ldg_stream8(src);
+      p.v[i][0] = w.x; p.v[i][1] = w.y;
+    }
+  }
+}
+
+// The query rows of a unit as A fragments in the dimension order of the K loads, times
+// 2^e with the row's largest element near 2^14; *unscale gets 2^-e (head r of this lane).
+template <int D, int G8, bool Q32>
+__device__ __forceinline__ void load_q_f16(const void *q, size_t orow0, int G, uint32_t (&hi)[D / 16][2],
+                                           uint32_t (&lo)[D / 16][2], float *unscale) {
+  const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+  float x[D / 16][4];
+  float big = 0.0f;
+#pragma unroll
+  for (int s = 0; s < D / 16; ++s) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[s][i] = 0.0f;
+    if (r < G) {
+      const size_t at = (orow0 + r) * D + 16 * (c + 4 * (s / 4)) + 4 * (s % 4);
+      if constexpr (Q32) {
+        const float4 w = *reinterpret_cast<const float4 *>(static_cast<const float *>(q) + at);
+        x[s][0] = w.x; x[s][1] = w.y; x[s][2] = w.z; x[s][3] = w.w;
+      } else {
+        const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(q) + at);
+        x[s][0] = bf16lo(w.x); x[s][1] = bf16hi(w.x); x[s][2] = bf16lo(w.y); x[s][3] = bf16hi(w.y);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) big = fmaxf(big, fabsf(x[s][i]));
+  }
+  big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+  big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+  // 2^e with e = 14 - floor(log2 big), kept within fp32's normal range; zero and
+  // non-finite rows stay as they are.
+  int e = 0;
+  if (big > 0.0f && big < INFINITY) {
+    e = 14 - (static_cast<int>(__float_as_uint(big) >> 23) - 127);
+    e = max(-120, min(120, e));
+  }
+  const float scale = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
+  *unscale = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+  for (int s = 0; s < D / 16; ++s)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float a = x[s][2 * i] * scale, b = x[s][2 * i + 1] * scale;
+      hi[s][i] = pack_f16(a, b);
+      lo[s][i] = Q32 ? pack_f16(a - f16_lo_f(hi[s][i]), b - f16_hi_f(hi[s][i])) : 0u;
+    }
+}
+
+// A warp's running state: m and l of head lane / 4 (m in log2 units, replicated over the
+// head's four lanes; l a partial sum of 2^(x - m + 14) per lane), and
+// o[i][2 k + j] = O[head 2 c + j][dim r D/8 + 2 i + k].
+template <int D>
+struct WarpState {
+  float m, l;
+  float o[D / 16][4];
+};
+
+template <int D, bool I8, bool Q32>
+__device__ __forceinline__ void quant_page(const PageRegs<D> &p, const PageMeta &t, const uint32_t (&qh)[D / 16][2],
+                                           const uint32_t (&ql)[D / 16][2], float q_scale, WarpState<D> &w) {
+  const int lane = threadIdx.x & 31, c = lane & 3;
+  // ---- S = q K8^T: two tiles of eight tokens --------------------------------------------
+  float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+  for (int j = 0; j < D / 64; ++j)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t word[4] = {p.k[j][i].x, p.k[j][i].y, p.k[j][i].z, p.k[j][i].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        uint32_t b0, b1;
+        codes_to_f16<I8>(word[k], b0, b1);
+        mma_f16(s[i], qh[4 * j + k][0], ql[4 * j + k][0], qh[4 * j + k][1], ql[4 * j + k][1], b0, b1);
+      }
+    }
+  const float f = q_scale * t.ks;
+  float x[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float dot = Q32 ? s[i >> 1][i & 1] + s[i >> 1][2 + (i & 1)] : s[i >> 1][i & 1];
+    x[i] = fmaf(dot, f, t.bias2);
+  }
+  if (t.valid < kPage) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (2 * c + (i & 1) + 8 * (i >> 1) >= t.valid) x[i] = -INFINITY;
+  }
+  // ---- online softmax: this lane's head over the page's 16 tokens -------------------------
+  float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+  if (__any_sync(0xffffffffu, mx > w.m)) {
+    const float m_new = fmaxf(w.m, mx);
+    const float alpha = m_new == -INFINITY ? 1.0f : exp2f(w.m - m_new);
+    w.m = m_new;
+    w.l *= alpha;
+    const float a0 = __shfl_sync(0xffffffffu, alpha, 8 * c), a1 = __shfl_sync(0xffffffffu, alpha, 8 * c + 4);
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i) {
+      w.o[i][0] *= a0;
+      w.o[i][1] *= a1;
+      w.o[i][2] *= a0;
+      w.o[i][3] *= a1;
+    }
+  }
+  const float base = w.m == -INFINITY ? 0.0f : w.m - kPShift;
+  float pr[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) pr[i] = exp2f(x[i] - base);
+  w.l += (pr[0] + pr[1]) + (pr[2] + pr[3]);
+  const uint32_t h0 = pack_f16(pr[0], pr[1]), h1 = pack_f16(pr[2], pr[3]);
+  const uint32_t l0 = pack_f16(pr[0] - f16_lo_f(h0), pr[1] - f16_hi_f(h0));
+  const uint32_t l1 = pack_f16(pr[2] - f16_lo_f(h1), pr[3] - f16_hi_f(h1));
+  // ---- O^T += vs V8^T P^T -----------------------------------------------------------------
+  // Codes past T may be anything (NaN too): zeroed.
+  uint32_t keep[4] = {~0u, ~0u, ~0u, ~0u};
+  if (t.valid < kPage) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (2 * c + (i & 1) + 8 * (i >> 1) >= t.valid) keep[i] = 0u;
+  }
+#pragma unroll
+  for (int g = 0; g < D / 32; ++g) {      // four dimensions of the lane's chunk
+    const uint32_t v0 = p.v[0][g] & keep[0], v1 = p.v[1][g] & keep[1];
+    const uint32_t v2 = p.v[2][g] & keep[2], v3 = p.v[3][g] & keep[3];
+    uint32_t a[4], b[4];                   // fp16 pairs of tokens (2c, 2c+1) and (2c+8, 2c+9) per dimension
+    codes_to_f16<I8>(__byte_perm(v0, v1, 0x5140), a[0], a[1]);
+    codes_to_f16<I8>(__byte_perm(v0, v1, 0x7362), a[2], a[3]);
+    codes_to_f16<I8>(__byte_perm(v2, v3, 0x5140), b[0], b[1]);
+    codes_to_f16<I8>(__byte_perm(v2, v3, 0x7362), b[2], b[3]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+      mma_f16(acc, a[2 * i], a[2 * i + 1], b[2 * i], b[2 * i + 1], h0, h1);
+      mma_f16(acc, a[2 * i], a[2 * i + 1], b[2 * i], b[2 * i + 1], l0, l1);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) w.o[2 * g + i][k] = fmaf(acc[k], t.vs, w.o[2 * g + i][k]);
+    }
+  }
+}
+
+// The end of a split for G heads: merge with the unit's other splits, write out and lse.
+template <int D, int G>
+__device__ __noinline__ void quant_finish(const AttnArgs &a, const UnitBlocks &ub, int u, size_t orow0, unsigned char *smem,
+                                          const float *mfin, const float *lfin, int split, int n_part,
+                                          bool in_cluster) {
+  using L = QuantLayout<D>;
+  const float *osum = reinterpret_cast<const float *>(smem + L::kOffSum);
+  if (in_cluster) {
+    cluster_merge<kQuantThreads, D, G>(orow0, osum, mfin, lfin, a.out, a.lse);
+    // Every CTA of the cluster has read the unit's words: advance its epoch.
+    if (ub.polled && split == 0 && threadIdx.x == 0) a.expect[u] = ub.epoch;
+  } else {
+    finish_split<kQuantThreads, D, G>(ub, u, orow0, osum, mfin, lfin, a.arrivals, a.records, a.out, a.lse,
+                                      reinterpret_cast<float *>(smem + L::kOffScratch), a.expect, n_part);
+  }
+}
+
+// Returns false for a split that took no part (it left at once; see step_ws_splits).
+template <int D, bool I8, bool Q32>
+__device__ bool attn_split_quant(const AttnArgs &a, unsigned char *smem, bool in_step, bool in_cluster) {
+  using L = QuantLayout<D>;
+  constexpr int NT = kQuantThreads, W = kQuantWarps;
+  const bs_dims &dims = a.dims;
+  int32_t *st = a.st;
+  const int u = attn_unit_id(in_cluster), split = attn_split_id(in_cluster);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = dims.n_q_heads / dims.n_kv_heads;
+  const int b = u / dims.n_kv_heads, hk = u % dims.n_kv_heads;
+  const size_t orow0 = static_cast<size_t>(b) * dims.n_q_heads + static_cast<size_t>(hk) * G;
+  int32_t *sel_sm = reinterpret_cast<int32_t *>(smem);
+  const int n_part = in_step && !in_cluster ? step_ws_splits(a, u, attn_n_splits(false)) : attn_n_splits(in_cluster);
+  if (split >= n_part) return false;
+
+  prefetch_page_row<NT>(dims, a.kv, a.cfg, a.plist, u, in_step);
+  UnitBlocks ub = load_unit_blocks<NT>(a, u, sel_sm, in_step, in_cluster);
+  check_split_bound(ub, n_part, split, st);
+  // Every split taking part stays to the end (see attn_split_mma).
+  const int n_pages = ub.ok ? ub.pg.n_pages : 0;
+  const int gp0 = min(split * ub.pg.pps, n_pages);
+  const int gp1 = min(gp0 + ub.pg.pps, n_pages);
+  const int32_t *pt = a.kv.page_table + static_cast<size_t>(u) * dims.max_pages_per_unit;
+  const uint8_t *kpool = static_cast<const uint8_t *>(a.kv.k_pool);
+  const uint8_t *vpool = static_cast<const uint8_t *>(a.kv.v_pool);
+
+  // This warp's pages: gp0 + warp + W i, i < n_mine; resolved 32 at a time, one per lane.
+  const int n_mine = gp1 - gp0 > warp ? (gp1 - gp0 - warp + W - 1) / W : 0;
+  int chunk = -1, ch_phys = 0, ch_valid = 0;
+  float ch_ks = 0.0f, ch_vs = 0.0f, ch_bias = 0.0f;
+  auto fetch = [&](int i, PageRegs<D> &p, PageMeta &t) {
+    if (i / 32 != chunk) {
+      chunk = i / 32;
+      int phys = -1, blk = -1;
+      ch_valid = resolve_page(ub, dims, pt, gp0 + warp + W * (chunk * 32 + lane), gp1, &phys, a.bias ? &blk : nullptr, st);
+      ch_phys = ch_valid > 0 ? phys : 0;
+      ch_bias = block_bias2(a.bias, dims, u, blk, st);
+      if (ch_bias == -INFINITY) ch_valid = 0;   // the block dropped out: nothing of it is read
+      ch_ks = ch_valid > 0 ? __ldg(a.kv.k_scale + ch_phys) : 0.0f;
+      ch_vs = ch_valid > 0 ? __ldg(a.kv.v_scale + ch_phys) : 0.0f;
+    }
+    const int src = i & 31;
+    const int phys = __shfl_sync(0xffffffffu, ch_phys, src);
+    t.valid = __shfl_sync(0xffffffffu, ch_valid, src);
+    t.ks = __shfl_sync(0xffffffffu, ch_ks, src);
+    t.vs = __shfl_sync(0xffffffffu, ch_vs, src);
+    t.bias2 = __shfl_sync(0xffffffffu, ch_bias, src);
+    if (t.valid > 0) {
+      const size_t off = static_cast<size_t>(phys) * (kPage * D);
+      load_page<D>(kpool + off, vpool + off, p);
+    }
+  };
+
+  uint32_t qh[D / 16][2], ql[D / 16][2];
+  float q_scale;
+  PageRegs<D> pa, pb;
+  PageMeta ta, tb;
+  ta.valid = tb.valid = 0;
+  if (n_mine > 0) fetch(0, pa, ta);
+  load_q_f16<D, kMaxG, Q32>(a.q, orow0, G, qh, ql, &q_scale);
+  q_scale *= rsqrtf(static_cast<float>(D)) * kLog2e;
+  WarpState<D> w;
+  w.m = -INFINITY;
+  w.l = 0.0f;
+#pragma unroll
+  for (int i = 0; i < D / 16; ++i) w.o[i][0] = w.o[i][1] = w.o[i][2] = w.o[i][3] = 0.0f;
+  for (int i = 0; i < n_mine; i += 2) {
+    tb.valid = 0;
+    if (i + 1 < n_mine) fetch(i + 1, pb, tb);
+    if (ta.valid > 0) quant_page<D, I8, Q32>(pa, ta, qh, ql, q_scale, w);
+    ta.valid = 0;
+    if (i + 2 < n_mine) fetch(i + 2, pa, ta);
+    if (tb.valid > 0) quant_page<D, I8, Q32>(pb, tb, qh, ql, q_scale, w);
+  }
+
+  // ---- combine the four warps' states ---------------------------------------------
+  float *ow = reinterpret_cast<float *>(smem + L::kOffO);     // [4][8][D]
+  float *mw = reinterpret_cast<float *>(smem + L::kOffMl);    // [4][8]
+  float *lw = mw + W * kMaxG;                                 // [4][8]
+  {
+    const int r = lane >> 2, c = lane & 3;
+    w.l += __shfl_xor_sync(0xffffffffu, w.l, 1);
+    w.l += __shfl_xor_sync(0xffffffffu, w.l, 2);
+    if (c == 0) {
+      mw[warp * kMaxG + r] = w.m - kPShift;   // the sums are of 2^(x - (m - 14))
+      lw[warp * kMaxG + r] = w.l;
+    }
+#pragma unroll
+    for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        *reinterpret_cast<float2 *>(ow + (warp * kMaxG + 2 * c + j) * D + r * (D / 8) + 2 * i) =
+            make_float2(w.o[i][j], w.o[i][2 + j]);
+  }
+  __syncthreads();
+  __shared__ float mfin[kMaxG], lfin[kMaxG], wfin[W][kMaxG];
+  if (tid < G) {
+    float M = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < W; ++k) M = fmaxf(M, mw[k * kMaxG + tid]);
+    float Ls = 0.0f;
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+      const float mi = mw[k * kMaxG + tid];
+      const float wt = (mi == -INFINITY) ? 0.0f : exp2f(mi - M);
+      wfin[k][tid] = wt;
+      Ls = fmaf(lw[k * kMaxG + tid], wt, Ls);
+    }
+    mfin[tid] = M;
+    lfin[tid] = Ls;
+  }
+  __syncthreads();
+  float *osum = reinterpret_cast<float *>(smem + L::kOffSum);
+  for (int i = tid; i < G * D / 4; i += NT) {
+    const int h = i / (D / 4), dq = i % (D / 4);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+      const float wt = wfin[k][h];
+      const float4 v = reinterpret_cast<const float4 *>(ow + (k * kMaxG + h) * D)[dq];
+      acc.x = fmaf(v.x, wt, acc.x);
+      acc.y = fmaf(v.y, wt, acc.y);
+      acc.z = fmaf(v.z, wt, acc.z);
+      acc.w = fmaf(v.w, wt, acc.w);
+    }
+    reinterpret_cast<float4 *>(osum + h * D)[dq] = acc;
+  }
+  __syncthreads();
+  switch (G) {
+    case 1: quant_finish<D, 1>(a, ub, u, orow0, smem, mfin, lfin, split, n_part, in_cluster); break;
+    case 2: quant_finish<D, 2>(a, ub, u, orow0, smem, mfin, lfin, split, n_part, in_cluster); break;
+    case 3: quant_finish<D, 3>(a, ub, u, orow0, smem, mfin, lfin, split, n_part, in_cluster); break;
+    case 4: quant_finish<D, 4>(a, ub, u, orow0, smem, mfin, lfin, split, n_part, in_cluster); break;
+    case 5: quant_finish<D, 5>(a, ub, u, orow0, smem, mfin, lfin, split, n_part, in_cluster); break;
+    case 6: quant_finish<D, 6>(a, ub, u, orow0, smem, mfin, lfin, split, n_part, in_cluster); break;
+    case 7: quant_finish<D, 7>(a, ub, u, orow0, smem, mfin, lfin, split, n_part, in_cluster); break;
+    default: quant_finish<D, 8>(a, ub, u, orow0, smem, mfin, lfin, split, n_part, in_cluster); break;
+  }
+  return true;
+}
+
+template <int D, bool I8, bool Q32>
+__global__ void __launch_bounds__(kQuantThreads) attn_quant_kernel(const __grid_constant__ AttnArgs a, bool step, bool cluster) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  if (step) pdl_launch_dependents();
+  const bool took_part = attn_split_quant<D, I8, Q32>(a, smem, step, cluster);
+  // In the fused step, finish only after the selection kernel has (a split that took no
+  // part leaves at once: split 0 of every unit takes part, so the grid still does).
+  if (step && took_part) pdl_wait();
+}
+
+template <int D, bool I8, bool Q32>
+bs_status launch_quant(const AttnArgs &a, bool step, cudaStream_t cs) {
+  const int units = a.dims.batch * a.dims.n_kv_heads;
+  constexpr int smem = QuantLayout<D>::kBytes;
+  static_assert(smem <= 48 * 1024, "within the default dynamic shared memory");
+  auto kernel = attn_quant_kernel<D, I8, Q32>;
+  static const bool attrs_ok =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
+  if (!attrs_ok) return BS_ERR_CUDA;
+  const bool cluster = attn_mode(units, a.dims.max_gather_pages_per_unit) == kModeCluster;
+  const int splits = attn_grid_splits(units, a.dims.max_gather_pages_per_unit, attn_target_ctas());
+  const dim3 grid = cluster ? dim3(splits, units) : dim3(units, splits);   // (workspace mode: unit-major)
+  const cudaError_t e =
+      launch_ex(kernel, grid, kQuantThreads, smem, cs, cluster && splits > 1 ? splits : 0, step, a, step, cluster);
+  return e == cudaSuccess ? BS_OK : BS_ERR_CUDA;
+}
+
+template <int D>
+bs_status dispatch_types(const AttnArgs &a, bool step, cudaStream_t cs) {
+  const bool i8 = a.dims.kv_dtype == BS_INT8, q32 = a.dims.q_dtype == BS_FP32;
+  if (i8) return q32 ? launch_quant<D, true, true>(a, step, cs) : launch_quant<D, true, false>(a, step, cs);
+  return q32 ? launch_quant<D, false, true>(a, step, cs) : launch_quant<D, false, false>(a, step, cs);
+}
+
+}  // namespace
+
+bs_status launch_attn_quant(const AttnArgs &a, bool step, cudaStream_t cs) {
+  return a.dims.head_dim == 128 ? dispatch_types<128>(a, step, cs) : dispatch_types<64>(a, step, cs);
+}
+
+}  // namespace bsi

@@ -17,6 +17,7 @@
 #include <vector>
 
 #include "bs_internal.cuh"
+#include "bs_quant.cuh"
 
 namespace bsi {
 namespace {
@@ -141,6 +142,7 @@ extern "C" bs_status bs_cpu_sparse_attn(const bs_dims *dims, const void *q, cons
       !tables->block_tokens || !sel_idx || !sel_cnt || !out || !lse || kv->n_pages < 1 ||
       (tables->evict_bias != nullptr && tables->max_blocks_per_unit < 1))
     return BS_ERR_INVALID_ARG;
+  if (is_quant(dims->kv_dtype)) return BS_ERR_INVALID_ARG;
   const int units = dims->batch * dims->n_kv_heads;
   const int nt = std::max(1, std::min(n_threads, units));
   std::atomic<int> next(0);

@@ -247,14 +247,22 @@ __device__ __forceinline__ void unit_error_publish(const bs_dims &dims, const bs
   }
 }
 
-// a1 for unit u: the sub-block holding token T-1 (one warp: call with the 32 lanes of
-// one warp only).
+// a1 for unit u: the sub-block holding token T-1; in an 8-bit cache every sub-block with a
+// token of that token's page, whose codes the append may have rounded again (one warp: call
+// with the 32 lanes of one warp only).
 template <int D>
 __device__ __forceinline__ void unit_summary_update(const bs_dims &dims, const bs_kv &kv, const bs_step_io &io,
                                                     int u, int s, int T, int64_t sum_off, int32_t *st) {
   const int j = (T - 1) / s;
   const int32_t *pt = kv.page_table + static_cast<size_t>(u) * dims.max_pages_per_unit;
   float *row = io.summaries + sum_off + static_cast<int64_t>(j) * D;
+  if (is_quant(dims.kv_dtype)) {
+    for (int i = ((T - 1) & ~(kPage - 1)) / s; i <= j; ++i)
+      if (!summary_update_warp_quant<D>(dims, kv, pt, s, T, i, io.summaries + sum_off + static_cast<int64_t>(i) * D) &&
+          (threadIdx.x & 31) == 0)
+        report(st, BS_ERR_DEVICE_BOUNDS);
+    return;
+  }
   const bool ok = dims.kv_dtype == BS_BF16
                       ? summary_update_warp<D, uint16_t>(static_cast<const uint16_t *>(kv.k_pool), pt, dims.n_pages,
                                                          s, T, j, row)
@@ -711,7 +719,7 @@ bs_status launch_step_attention(const bs_dims &dims, const bs_kv &kv, const bs_h
   a.expect = words.expect;
   a.st = io.dev_status;
   a.wait_ns = wait_limit_ns();
-  return dims.kv_dtype == BS_BF16 ? launch_attn_bf16(a, true, cs) : launch_attn_f32(a, true, cs);
+  return launch_attn(a, true, cs);
 }
 
 template <int D>
@@ -743,6 +751,7 @@ extern "C" bs_status bs_decode_step(const bs_dims *dims, const bs_kv *kv, const 
       !io->prev_idx || !io->prev_cnt || !io->cur_idx || !io->cur_cnt || !io->added || !io->added_cnt ||
       !io->removed || !io->removed_cnt || !io->out || !io->lse || !io->workspace || !io->dev_status)
     return BS_ERR_INVALID_ARG;
+  if (is_quant(dims->kv_dtype) && (!kv->k_scale || !kv->v_scale)) return BS_ERR_INVALID_ARG;
   if (group_reduce != BS_GROUP_MAX && group_reduce != BS_GROUP_MEAN) return BS_ERR_INVALID_ARG;
   if (io->prev_idx == io->cur_idx || io->prev_cnt == io->cur_cnt) return BS_ERR_INVALID_ARG;
   if (!aligned16(io->q) || !aligned16(kv->k_pool) || !aligned16(kv->v_pool) || !aligned16(io->out) ||

@@ -9,6 +9,7 @@
 #pragma once
 
 #include "bs_internal.cuh"
+#include "bs_quant.cuh"
 
 namespace bsi {
 
@@ -67,6 +68,52 @@ __device__ bool summary_update_warp(const KT *pool, const int32_t *pt, int64_t n
       if (t >= t0 && t < page_end) {
 #pragma unroll
         for (int i = 0; i < DPL; ++i) acc[i] += v[r][i];
+      }
+    }
+    t0 = page_end;
+  }
+  const float n = static_cast<float>(hi - lo);
+  float *dst = dst_row + lane * DPL;
+#pragma unroll
+  for (int i = 0; i < DPL; ++i) dst[i] = acc[i] / n;
+  return true;
+}
+
+// The same over an 8-bit cache: K[t] = code * scale of the page, summed in token order.
+template <int D>
+__device__ bool summary_update_warp_quant(const bs_dims &dims, const bs_kv &kv, const int32_t *pt, int s, int T,
+                                          int j, float *dst_row) {
+  constexpr int DPL = D / 32;
+  const int lane = threadIdx.x & 31;
+  const int lo = j * s, hi = min((j + 1) * s, T);
+  const bool i8 = dims.kv_dtype == BS_INT8;
+  float acc[DPL];
+#pragma unroll
+  for (int i = 0; i < DPL; ++i) acc[i] = 0.0f;
+  for (int t0 = lo; t0 < hi;) {
+    const int page_end = min(hi, (t0 / kPage + 1) * kPage);
+    const int phys = __ldg(pt + t0 / kPage);
+    if (phys < 0 || phys >= dims.n_pages) return false;
+    const float scale = kv.k_scale[phys];
+    const uint8_t *base = static_cast<const uint8_t *>(kv.k_pool) + static_cast<size_t>(phys) * kPage * D + lane * DPL;
+    uint32_t w[kPage];
+#pragma unroll
+    for (int r = 0; r < kPage; ++r) {
+      const int t = (t0 & ~(kPage - 1)) + r;
+      w[r] = 0u;
+      if (t >= t0 && t < page_end)
+        w[r] = DPL == 4 ? *reinterpret_cast<const uint32_t *>(base + r * D)
+                        : *reinterpret_cast<const uint16_t *>(base + r * D);
+    }
+#pragma unroll
+    for (int r = 0; r < kPage; ++r) {
+      const int t = (t0 & ~(kPage - 1)) + r;
+      if (t >= t0 && t < page_end) {
+        float f[4];
+        if (i8) codes_to_f32<true>(w[r], f);
+        else codes_to_f32<false>(w[r], f);
+#pragma unroll
+        for (int i = 0; i < DPL; ++i) acc[i] = fmaf(f[i], scale, acc[i]);
       }
     }
     t0 = page_end;

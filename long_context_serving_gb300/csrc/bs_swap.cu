@@ -10,6 +10,7 @@
 // the page holding the appended token T-1 when its block stays cached): copies pages,
 // K and V, from host memory into the block's slot with 16-byte loads issued eight at
 // a time per thread before their stores.
+#include "bs_quant.cuh"
 #include "bs_select_impl.cuh"
 
 namespace bsi {
@@ -194,6 +195,7 @@ extern "C" bs_status bs_block_swap(const bs_dims *dims, const bs_head_cfg *cfg, 
   if (cache->slots_per_unit < 1 || cache->slots_per_unit > kMaxSlots || cache->pages_per_slot < 1 ||
       host->n_pages < 1)
     return BS_ERR_INVALID_ARG;
+  if (is_quant(dims->kv_dtype)) return BS_ERR_INVALID_ARG;   // (the swap moves no page scales)
   if ((reinterpret_cast<uintptr_t>(host->k_pool) | reinterpret_cast<uintptr_t>(host->v_pool) |
        reinterpret_cast<uintptr_t>(cache->k_pool) | reinterpret_cast<uintptr_t>(cache->v_pool)) & 15u)
     return BS_ERR_ALIGN;

@@ -34,10 +34,16 @@ class PagedLayer:
     ``preload_all``: put every token of every step in the pool now (otherwise tokens
     enter the pool when their step appends them).
     ``q_fp32``: pass the queries as fp32 (the same values, widened) over a bf16 cache.
+    ``kv8``: "e4m3" or "int8" keeps the cache in 8 bits with a scale per page; tokens enter
+    it through bs_quant_append (slots without a token hold NaN, or 85 in INT8).
     """
 
-    def __init__(self, wl, device="cuda", fill=float("nan"), preload_all=False, q_fp32=False, ed_dma=False):
+    def __init__(self, wl, device="cuda", fill=float("nan"), preload_all=False, q_fp32=False, ed_dma=False,
+                 kv8=None):
         self.wl = wl
+        if kv8 not in (None, "e4m3", "int8"):
+            raise ValueError(f"kv8 is None, 'e4m3' or 'int8', not {kv8!r}")
+        self.kv8 = kv8
         # ED-DMA attention: the eviction logits also enter the attention as block logits.
         self.ed_dma = bool(ed_dma)
         self.device = torch.device(device)
@@ -57,7 +63,8 @@ class PagedLayer:
                            max_pages_per_unit=max_pages, max_blocks_per_unit=self.max_blocks,
                            max_sel_per_unit=self.max_sel, max_subs_per_unit=int(sub_rows.max()),
                            max_gather_pages_per_unit=int((sel_u * g // 16).max()), n_pages=int(wl.n_pages),
-                           kv_dtype=B.BS_BF16 if wl.dtype == "bf16" else B.BS_FP32,
+                           kv_dtype={"e4m3": B.BS_E4M3, "int8": B.BS_INT8}[kv8] if kv8
+                           else B.BS_BF16 if wl.dtype == "bf16" else B.BS_FP32,
                            q_dtype=B.BS_BF16 if wl.dtype == "bf16" and not q_fp32 else B.BS_FP32)
 
         dev = self.device
@@ -82,8 +89,20 @@ class PagedLayer:
         # Paged pools.
         kv_dt = torch.bfloat16 if wl.dtype == "bf16" else torch.float32
         self.page_table = i32(wl.page_table)
-        self.k_pool = torch.full((wl.n_pages, 16, d), fill, dtype=kv_dt, device=dev)
-        self.v_pool = torch.full((wl.n_pages, 16, d), fill, dtype=kv_dt, device=dev)
+        self.status = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.k_scale = self.v_scale = None
+        if kv8:
+            code = torch.float8_e4m3fn if kv8 == "e4m3" else torch.int8
+            self.k_pool = torch.full((wl.n_pages, 16, d), 0x7F if kv8 == "e4m3" else 85, dtype=torch.uint8,
+                                     device=dev).view(code)
+            self.v_pool = self.k_pool.clone()
+            self.k_scale = torch.full((wl.n_pages,), float("nan"), dtype=torch.float32, device=dev)
+            self.v_scale = self.k_scale.clone()
+            self.pools = B.Pools(k_pool=self.k_pool.data_ptr(), v_pool=self.v_pool.data_ptr(),
+                                 k_scale=self.k_scale.data_ptr(), v_scale=self.v_scale.data_ptr())
+        else:
+            self.k_pool = torch.full((wl.n_pages, 16, d), fill, dtype=kv_dt, device=dev)
+            self.v_pool = torch.full((wl.n_pages, 16, d), fill, dtype=kv_dt, device=dev)
         self._pt_long = self.page_table.long()
         self._K = _kv_tensor(wl.K, wl.dtype, dev)          # logical [U][T_cap][d], source of appends
         self._V = _kv_tensor(wl.V, wl.dtype, dev)
@@ -98,7 +117,8 @@ class PagedLayer:
         self.prefill_lens = i32(wl.T_prefill)
         self.zeros_b = torch.zeros(wl.B, dtype=torch.int32, device=dev)
         self.kv = B.KV(k_pool=self.k_pool.data_ptr(), v_pool=self.v_pool.data_ptr(),
-                       page_table=self.page_table.data_ptr(), seq_lens=0)
+                       page_table=self.page_table.data_ptr(), seq_lens=0,
+                       k_scale=self.k_scale.data_ptr() if kv8 else 0, v_scale=self.v_scale.data_ptr() if kv8 else 0)
 
         # Per-step state and outputs.
         MB, MS = self.max_blocks, self.max_sel
@@ -123,12 +143,14 @@ class PagedLayer:
         self.out = torch.zeros((wl.B, wl.Hq, d), dtype=torch.float32, device=dev)
         self.lse = torch.zeros((wl.B, wl.Hq), dtype=torch.float32, device=dev)
         self.workspace = torch.zeros(max(B.workspace_size(self.dims) // 4, 4), dtype=torch.float32, device=dev)
-        self.status = torch.zeros(1, dtype=torch.int32, device=dev)
 
     # -- caller-side KV writes (not a step of the method) --------------------------
     def _write_tokens(self, lo: np.ndarray, hi: np.ndarray) -> None:
         """Copy logical tokens [lo[b], hi[b]) of every unit into their pool pages."""
         wl = self.wl
+        if self.kv8:
+            self._quant_append(lo, hi)
+            return
         for b in range(wl.B):
             if hi[b] <= lo[b]:
                 continue
@@ -138,6 +160,23 @@ class PagedLayer:
                 self.k_pool[phys, t % 16] = self._K[u, t]
                 self.v_pool[phys, t % 16] = self._V[u, t]
 
+    def _quant_append(self, lo: np.ndarray, hi: np.ndarray) -> None:
+        """The same into an 8-bit cache: the sequences' new tokens as packed rows of all KV
+        heads, quantised into their pages."""
+        wl = self.wl
+        n = np.maximum(hi - lo, 0)
+        if n.sum() == 0:
+            return
+        dt = torch.float32 if self.dims.q_dtype == B.BS_FP32 else torch.bfloat16
+
+        def rows(x):
+            parts = [x[b * wl.Hkv:(b + 1) * wl.Hkv, int(lo[b]):int(lo[b] + n[b])].transpose(0, 1) for b in range(wl.B)]
+            return torch.cat(parts).reshape(int(n.sum()), wl.Hkv * wl.d).to(dt).contiguous()
+
+        i32 = lambda a: torch.as_tensor(np.ascontiguousarray(a, dtype=np.int32), device=self.device)  # noqa: E731
+        B.quant_append(self.dims, self.pools, self.page_table, i32(lo + n), i32(lo), i32(np.cumsum(n) - n),
+                       rows(self._K), rows(self._V), wl.Hkv * wl.d, int(n.sum()), int(n.max()), self.status)
+
     def append(self, step: int) -> None:
         """Write the token appended at ``step`` (position T_prefill + step) into the pools."""
         lo = self.wl.T_prefill.astype(np.int64) + step
@@ -146,7 +185,7 @@ class PagedLayer:
     # -- the five calls ------------------------------------------------------------
     def kv_at(self, seq_lens: torch.Tensor) -> B.KV:
         return B.KV(k_pool=self.kv.k_pool, v_pool=self.kv.v_pool, page_table=self.kv.page_table,
-                    seq_lens=seq_lens.data_ptr())
+                    seq_lens=seq_lens.data_ptr(), k_scale=self.kv.k_scale, v_scale=self.kv.v_scale)
 
     def prefill(self, stream=None) -> None:
         """Summaries of every prefilled token."""
