@@ -35,7 +35,7 @@ __device__ __forceinline__ float page_scale(float a) {
   return __uint_as_float(static_cast<uint32_t>(max(e, -126) + 127) << 23);
 }
 
-// Four codes of four quotients.
+// Codes of eight quotients x / s in fp32 by the rule of bs_quant_append, for any values.
 template <bool I8>
 __device__ __forceinline__ uint32_t encode4(const float (&y)[4]) {
   if constexpr (I8) {
@@ -58,23 +58,67 @@ __device__ __forceinline__ uint32_t encode4(const float (&y)[4]) {
     return w;
   }
 }
+template <bool I8>
+__device__ __forceinline__ uint2 encode8_any(const float (&x)[8], float s) {
+  float y[4];
+  uint2 w;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) y[j] = __fdiv_rn(x[j], s);
+  w.x = encode4<I8>(y);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) y[j] = __fdiv_rn(x[4 + j], s);
+  w.y = encode4<I8>(y);
+  return w;
+}
 
-// x / s in fp32 for every value; a power-of-two s multiplies by its reciprocal (the same
-// rounding of the same number).
-struct Quotient {
+// The same without divisions, for finite x with |x| <= top * s (top 448 or 127) when `exact`.
+// E4M3: a power-of-two s multiplies by its reciprocal, the same rounding of the same number.
+// INT8: n = rint(x * inv), inv = fp32(1 / s), differs from the rule only where the quotient
+// is next to a half: |x inv - x / s| <= 2^-17 and the quotient's own rounding is at most
+// 2^-18 for |x / s| < 128, so a lane with a value within 2^-15 of a half divides.
+template <bool I8>
+struct Encoder {
   float s, inv;
-  bool pow2;
-  __device__ __forceinline__ explicit Quotient(float scale) : s(scale) {
+  bool exact;
+  __device__ __forceinline__ Encoder(float scale, bool finite) : s(scale) {
     const uint32_t bits = __float_as_uint(scale);
-    // 2^e with 2^-e normal: e in [-126, 126]
-    pow2 = (bits & 0x7fffffu) == 0 && bits >= (1u << 23) && bits <= (253u << 23);
-    inv = pow2 ? __uint_as_float((254u << 23) - bits) : 0.0f;
+    // A normal scale whose reciprocal is normal too.
+    const bool normal = bits >= (1u << 23) && bits <= (252u << 23);
+    inv = normal ? __frcp_rn(scale) : 0.0f;
+    exact = finite && normal && (I8 || (bits & 0x7fffffu) == 0);
   }
-  __device__ __forceinline__ float operator()(float x) const { return pow2 ? x * inv : __fdiv_rn(x, s); }
+  __device__ __forceinline__ uint2 operator()(const float (&x)[8]) const {
+    if (!exact) return encode8_any<I8>(x, s);
+    uint2 w;
+    if constexpr (I8) {
+      constexpr float kMagic = 12582912.0f;   // 1.5 * 2^23: the sum's low bits are the integer
+      uint32_t n[8];
+      float off = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float t = fmaf(x[j], inv, kMagic);
+        n[j] = __float_as_uint(t);
+        off = fmaxf(off, fabsf(fmaf(x[j], inv, -(t - kMagic))));
+      }
+      if (off > 0.5f - 0x1p-15f) return encode8_any<I8>(x, s);
+      w.x = __byte_perm(__byte_perm(n[0], n[1], 0x0040), __byte_perm(n[2], n[3], 0x0040), 0x5410);
+      w.y = __byte_perm(__byte_perm(n[4], n[5], 0x0040), __byte_perm(n[6], n[7], 0x0040), 0x5410);
+    } else {
+      float y[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) y[j] = x[j] * inv;
+      w.x = encode4<I8>(y);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) y[j] = x[4 + j] * inv;
+      w.y = encode4<I8>(y);
+    }
+    return w;
+  }
 };
 
+// The page item `it` of a unit: logical page lp0 + it / 2, K (even) or V (odd).
 template <int D, bool I8, bool Q32>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendArgs a) {
+__global__ void __launch_bounds__(kAppendThreads, Q32 ? (D == 128 ? 3 : 5) : 6) append_kernel(const __grid_constant__ AppendArgs a, int per_warp) {
   constexpr int kLanesPerRow = D / 8;              // 8 dimensions a lane
   constexpr int kRowsPerIter = 32 / kLanesPerRow;
   constexpr int kIters = kPage / kRowsPerIter;
@@ -82,28 +126,31 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
   const int u = blockIdx.x, b = u / dims.n_kv_heads, h = u % dims.n_kv_heads;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int T = a.seq_lens[b], t_begin = a.tok_begin[b];
-  const bool first_warp = blockIdx.y == 0 && threadIdx.x == 0;
+  const int64_t row0 = a.row_begin[b];
+  const bool first_thread = blockIdx.y == 0 && threadIdx.x == 0;
   if (t_begin < 0 || T < t_begin) {
-    if (first_warp) report(a.st, BS_ERR_INVALID_ARG);
+    if (first_thread) report(a.st, BS_ERR_INVALID_ARG);
     return;
   }
   if (t_begin == T) return;
   if ((static_cast<int64_t>(T) + kPage - 1) / kPage > dims.max_pages_per_unit) {
-    if (first_warp) report(a.st, BS_ERR_CAPACITY);
+    if (first_thread) report(a.st, BS_ERR_CAPACITY);
     return;
   }
-  const int64_t row0 = a.row_begin[b];
   if (row0 < 0 || row0 + (T - t_begin) > a.n_rows) {
-    if (first_warp) report(a.st, BS_ERR_DEVICE_BOUNDS);
+    if (first_thread) report(a.st, BS_ERR_DEVICE_BOUNDS);
     return;
   }
-  const int lp0 = t_begin / kPage, n_lp = (T - 1) / kPage - lp0 + 1;
+  const int lp0 = t_begin / kPage;
+  const int64_t n_items = 2ll * ((T - 1) / kPage - lp0 + 1);
   const int sub = lane / kLanesPerRow, col = lane % kLanesPerRow;
-  for (int64_t item = static_cast<int64_t>(blockIdx.y) * kAppendWarps + warp; item < 2ll * n_lp;
-       item += static_cast<int64_t>(gridDim.y) * kAppendWarps) {
+  const int32_t *pt = a.page_table + static_cast<size_t>(u) * dims.max_pages_per_unit;
+  const int64_t stride = static_cast<int64_t>(gridDim.y) * kAppendWarps * per_warp;
+  for (int64_t i0 = (static_cast<int64_t>(blockIdx.y) * kAppendWarps + warp) * per_warp; i0 < n_items; i0 += stride)
+    for (int64_t item = i0; item < i0 + per_warp && item < n_items; ++item) {
     const int lp = lp0 + static_cast<int>(item >> 1);
     const bool is_v = item & 1;
-    const int phys = a.page_table[static_cast<size_t>(u) * dims.max_pages_per_unit + lp];
+    const int phys = pt[lp];
     if (phys < 0 || phys >= dims.n_pages) {
       if (lane == 0) report(a.st, BS_ERR_DEVICE_BOUNDS);
       continue;
@@ -117,60 +164,75 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
     constexpr int kVecs = Q32 ? 2 : 1;
     uint4 raw[kIters][kVecs];
     const int64_t first = row0 + (base - t_begin);                       // row of slot 0
+    const char *src = static_cast<const char *>(is_v ? a.v_new : a.k_new) +
+                      ((first + sub) * a.row_stride + static_cast<int64_t>(h) * D + col * 8) * (Q32 ? 4 : 2);
+    const int64_t step = kRowsPerIter * a.row_stride * (Q32 ? 4 : 2);
 #pragma unroll
     for (int i = 0; i < kIters; ++i) {
       const int slot = i * kRowsPerIter + sub;
 #pragma unroll
       for (int j = 0; j < kVecs; ++j) raw[i][j] = make_uint4(0u, 0u, 0u, 0u);
       if (slot >= s0 && slot < s1) {
-        const int64_t at = (first + slot) * a.row_stride + static_cast<int64_t>(h) * D + col * 8;
-        const char *src = static_cast<const char *>(is_v ? a.v_new : a.k_new) + at * (Q32 ? 4 : 2);
 #pragma unroll
-        for (int j = 0; j < kVecs; ++j) raw[i][j] = ldg_stream16(src + 16 * j);
+        for (int j = 0; j < kVecs; ++j) raw[i][j] = ldg_stream16(src + i * step + 16 * j);
       }
     }
-    auto value = [&](int i, int j) -> float {       // value j (0..7) of iteration i
+    auto values = [&](int i, float (&x)[8]) {
       if constexpr (Q32) {
-        const uint4 w = raw[i][j >> 2];
-        const uint32_t x = (j & 3) == 0 ? w.x : (j & 3) == 1 ? w.y : (j & 3) == 2 ? w.z : w.w;
-        return __uint_as_float(x);
+        x[0] = __uint_as_float(raw[i][0].x); x[1] = __uint_as_float(raw[i][0].y);
+        x[2] = __uint_as_float(raw[i][0].z); x[3] = __uint_as_float(raw[i][0].w);
+        x[4] = __uint_as_float(raw[i][1].x); x[5] = __uint_as_float(raw[i][1].y);
+        x[6] = __uint_as_float(raw[i][1].z); x[7] = __uint_as_float(raw[i][1].w);
       } else {
-        const uint4 w = raw[i][0];
-        const uint32_t x = (j >> 1) == 0 ? w.x : (j >> 1) == 1 ? w.y : (j >> 1) == 2 ? w.z : w.w;
-        return (j & 1) ? bf16hi(x) : bf16lo(x);
+        x[0] = bf16lo(raw[i][0].x); x[1] = bf16hi(raw[i][0].x); x[2] = bf16lo(raw[i][0].y); x[3] = bf16hi(raw[i][0].y);
+        x[4] = bf16lo(raw[i][0].z); x[5] = bf16hi(raw[i][0].z); x[6] = bf16lo(raw[i][0].w); x[7] = bf16hi(raw[i][0].w);
       }
     };
-    uint32_t big = 0u;   // magnitudes order like their bits
+    // The largest magnitude: bits order like magnitudes, bf16 pairs are compared two at a time,
+    // and only a page with a non-finite value looks again, without those. keep(word): the
+    // magnitudes of a word that count.
+    auto largest = [&](auto keep) -> uint32_t {
+      uint32_t m = 0u;
 #pragma unroll
-    for (int i = 0; i < kIters; ++i)
+      for (int i = 0; i < kIters; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t m = __float_as_uint(value(i, j)) & 0x7fffffffu;
-        big = max(big, m < 0x7f800000u ? m : 0u);
-      }
-    big = __reduce_max_sync(0xffffffffu, big);
+        for (int j = 0; j < kVecs; ++j) {
+          const uint4 w = raw[i][j];
+          if constexpr (Q32) m = max(m, max(max(keep(w.x), keep(w.y)), max(keep(w.z), keep(w.w))));
+          else m = __vmaxu2(m, __vmaxu2(__vmaxu2(keep(w.x), keep(w.y)), __vmaxu2(keep(w.z), keep(w.w))));
+        }
+      if constexpr (!Q32) m = max(m << 16, m & 0xffff0000u);
+      return __reduce_max_sync(0xffffffffu, m);
+    };
+    uint32_t big = largest([](uint32_t w) { return w & (Q32 ? 0x7fffffffu : 0x7fff7fffu); });
+    const bool finite = big < 0x7f800000u;
+    if (!finite)
+      big = largest([](uint32_t w) {
+        if constexpr (Q32) {
+          const uint32_t m = w & 0x7fffffffu;
+          return m < 0x7f800000u ? m : 0u;
+        } else {
+          const uint32_t m = w & 0x7fff7fffu;
+          return m & __vcmpltu2(m, 0x7f807f80u);
+        }
+      });
     const float to = fmaxf(had, page_scale<I8>(__uint_as_float(big)));
-    const Quotient quo(to);
+    const Encoder<I8> enc(to, finite);
     // ---- codes already there, at the new scale -----------------------------------------
     if (s0 > 0 && to > had) {
+#pragma unroll 1
+      for (int slot = sub; slot < s0; slot += kRowsPerIter) {
+        uint2 *p = reinterpret_cast<uint2 *>(page + slot * D + col * 8);
+        const uint2 old = *p;
+        float f[8], lo[4], hi[4];
+        codes_to_f32<I8>(old.x, lo);
+        codes_to_f32<I8>(old.y, hi);
 #pragma unroll
-      for (int i = 0; i < kIters; ++i) {
-        const int slot = i * kRowsPerIter + sub;
-        if (slot < s0) {
-          uint2 *p = reinterpret_cast<uint2 *>(page + slot * D + col * 8);
-          const uint2 old = *p;
-          float f[4];
-          uint2 now;
-          codes_to_f32<I8>(old.x, f);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) f[j] = quo(__fmul_rn(f[j], had));
-          now.x = encode4<I8>(f);
-          codes_to_f32<I8>(old.y, f);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) f[j] = quo(__fmul_rn(f[j], had));
-          now.y = encode4<I8>(f);
-          *p = now;
+        for (int j = 0; j < 4; ++j) {
+          f[j] = __fmul_rn(lo[j], had);
+          f[4 + j] = __fmul_rn(hi[j], had);
         }
+        *p = encode8_any<I8>(f, to);
       }
     }
     // ---- the new codes ------------------------------------------------------------------
@@ -178,29 +240,24 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
     for (int i = 0; i < kIters; ++i) {
       const int slot = i * kRowsPerIter + sub;
       if (slot >= s0 && slot < s1) {
-        float f[4];
-        uint2 now = make_uint2(0u, 0u);
-        if (to > 0.0f) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) f[j] = quo(value(i, j));
-          now.x = encode4<I8>(f);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) f[j] = quo(value(i, 4 + j));
-          now.y = encode4<I8>(f);
-        }
-        *reinterpret_cast<uint2 *>(page + slot * D + col * 8) = now;
+        float x[8];
+        values(i, x);
+        *reinterpret_cast<uint2 *>(page + slot * D + col * 8) = to > 0.0f ? enc(x) : make_uint2(0u, 0u);
       }
     }
     if (lane == 0) *scale = to;
   }
 }
 
+// Pages a warp takes in turn: one (K or V) while that keeps the launch short; four for long
+// prompts, where a CTA's start is worth several pages.
 template <int D, bool I8, bool Q32>
 bs_status launch_append(const AppendArgs &a, int max_new, cudaStream_t cs) {
   const int units = a.dims.batch * a.dims.n_kv_heads;
   const int64_t items = 2 * ((static_cast<int64_t>(max_new) + kPage - 2) / kPage + 1);   // pages that max_new tokens can touch
-  const int64_t gy = (items + kAppendWarps - 1) / kAppendWarps;
-  append_kernel<D, I8, Q32><<<dim3(units, static_cast<unsigned>(gy < 65535 ? gy : 65535)), kAppendThreads, 0, cs>>>(a);
+  const int per_warp = units * items > 8 * 152 * kAppendWarps ? 4 : 1;
+  const int64_t gy = (items + kAppendWarps * per_warp - 1) / (kAppendWarps * per_warp);
+  append_kernel<D, I8, Q32><<<dim3(units, static_cast<unsigned>(gy < 65535 ? gy : 65535)), kAppendThreads, 0, cs>>>(a, per_warp);
   return launch_status();
 }
 
