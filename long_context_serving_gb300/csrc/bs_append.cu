@@ -58,17 +58,16 @@ __device__ __forceinline__ uint32_t encode4(const float (&y)[4]) {
     return w;
   }
 }
+// (Out of line: rarely taken, and its divisions are long.)
+template <bool I8>
+__device__ __noinline__ uint2 encode8_any(float4 a, float4 b, float s) {
+  const float x[4] = {__fdiv_rn(a.x, s), __fdiv_rn(a.y, s), __fdiv_rn(a.z, s), __fdiv_rn(a.w, s)};
+  const float y[4] = {__fdiv_rn(b.x, s), __fdiv_rn(b.y, s), __fdiv_rn(b.z, s), __fdiv_rn(b.w, s)};
+  return make_uint2(encode4<I8>(x), encode4<I8>(y));
+}
 template <bool I8>
 __device__ __forceinline__ uint2 encode8_any(const float (&x)[8], float s) {
-  float y[4];
-  uint2 w;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) y[j] = __fdiv_rn(x[j], s);
-  w.x = encode4<I8>(y);
-#pragma unroll
-  for (int j = 0; j < 4; ++j) y[j] = __fdiv_rn(x[4 + j], s);
-  w.y = encode4<I8>(y);
-  return w;
+  return encode8_any<I8>(make_float4(x[0], x[1], x[2], x[3]), make_float4(x[4], x[5], x[6], x[7]), s);
 }
 
 // The same without divisions, for finite x with |x| <= top * s (top 448 or 127) when `exact`.
@@ -118,7 +117,7 @@ struct Encoder {
 
 // The page item `it` of a unit: logical page lp0 + it / 2, K (even) or V (odd).
 template <int D, bool I8, bool Q32>
-__global__ void __launch_bounds__(kAppendThreads, Q32 ? (D == 128 ? 3 : 5) : 6) append_kernel(const __grid_constant__ AppendArgs a, int per_warp) {
+__global__ void __launch_bounds__(kAppendThreads, Q32 ? (D == 128 ? 3 : 5) : 8) append_kernel(const __grid_constant__ AppendArgs a, int per_warp) {
   constexpr int kLanesPerRow = D / 8;              // 8 dimensions a lane
   constexpr int kRowsPerIter = 32 / kLanesPerRow;
   constexpr int kIters = kPage / kRowsPerIter;

@@ -29,6 +29,7 @@ bs_status launch_standalone(const bs_dims *dims, const void *q, const bs_kv *kv,
   a.expect = nullptr;
   a.st = st;
   a.wait_ns = wait_limit_ns();
+  a.min_split = attn_min_split_pages(dims->max_gather_pages_per_unit);
   return launch_attn(a, false, cs);
 }
 

@@ -29,7 +29,7 @@ bs_status launch_modes(const AttnArgs &a, bool step, const CUtensorMap &tk, cons
   if (!attrs_ok) return BS_ERR_CUDA;
   const bool cluster = attn_mode(units, a.dims.max_gather_pages_per_unit) == kModeCluster;
   const int smem = MmaLayout<D>::bytes(attn_mma_ring(cluster)) + kSmemAlignSlack;
-  const int splits = attn_grid_splits(units, a.dims.max_gather_pages_per_unit, attn_target_ctas());
+  const int splits = attn_grid_splits(units, a.dims.max_gather_pages_per_unit, attn_target_ctas(), a.min_split);
   const dim3 grid = cluster ? dim3(splits, units) : dim3(units, splits);   // (workspace mode: unit-major)
   const cudaError_t e =
       launch_ex(kernel, grid, kMmaThreads, smem, cs, cluster && splits > 1 ? splits : 0, step, a, tk, tv, step, cluster);

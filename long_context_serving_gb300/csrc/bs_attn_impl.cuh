@@ -215,7 +215,7 @@ __device__ UnitBlocks load_unit_blocks(const AttnArgs &a, int u, int32_t *sel_sm
     }
   }
   ub.pg = unit_pages(ub.T, ub.g, ub.ok ? ub.cnt : 0, last, in_cluster ? static_cast<int>(gridDim.x) : 0,
-                     attn_min_split_pages(dims.max_gather_pages_per_unit));
+                     a.min_split);
   if (ub.plist && ub.pg.n_pages > dims.max_gather_pages_per_unit) {
     if (split == 0 && tid == 0) report(st, BS_ERR_CAPACITY);
     ub.pg.n_pages = 0;
@@ -227,13 +227,13 @@ __device__ UnitBlocks load_unit_blocks(const AttnArgs &a, int u, int32_t *sel_sm
 // head configuration and the length alone (every split of the unit computes the same
 // number before any wait): a selection holds the forced blocks (sink, local window,
 // tail) and at most k others, so its pages are at most min(n_blk, |F| + k) * g/16; with
-// selections up to 1024 pages every split but the last holds at least kMidSplitPages
-// pages, so ceil(pages / kMidSplitPages) bounds the split count. The splits past it can
+// selections up to 1024 pages every split but the last holds at least a.min_split
+// pages, so ceil(pages / min_split) bounds the split count. The splits past it can
 // hold no page: they leave at once instead of holding an SM slot until the unit's
 // selection is published. Any other case: every launched split.
 __device__ __forceinline__ int step_ws_splits(const AttnArgs &a, int u, int launched) {
   const bs_dims &dims = a.dims;
-  if (attn_min_split_pages(dims.max_gather_pages_per_unit) != kMidSplitPages) return launched;
+  if (dims.max_gather_pages_per_unit > kClusterMaxPages) return launched;
   const bs_head_cfg &cfg = a.cfg;
   const int cls = cfg.cls[u], g = cfg.block_tokens[u], s = cfg.sub_tokens[u], k = cfg.k_total[u];
   const int sink = cfg.sink_tokens[u], local = cfg.local_tokens[u];
@@ -245,7 +245,7 @@ __device__ __forceinline__ int step_ws_splits(const AttnArgs &a, int u, int laun
   const long long blocks =
       cls == BS_STREAMING ? n_forced : min(static_cast<long long>(ge.n_blk), static_cast<long long>(n_forced) + k);
   const long long pages = min(blocks * (g / kPage), static_cast<long long>(dims.max_gather_pages_per_unit));
-  const int n = static_cast<int>((pages + kMidSplitPages - 1) / kMidSplitPages);
+  const int n = static_cast<int>((pages + a.min_split - 1) / a.min_split);
   return max(1, min(launched, n));
 }
 

@@ -23,6 +23,7 @@ struct AttnArgs {
   int32_t *expect;       // fused step: epoch of the last selection the attention took, per unit
   int32_t *st;
   uint64_t wait_ns;      // limit of every device-side wait
+  int min_split;         // workspace mode: pages per split, at least (set by the launchers)
 };
 
 // step = true: launched as a programmatic dependent of the fused step's selection

@@ -99,10 +99,9 @@ __host__ __device__ inline int attn_cluster_splits(int units, int max_gather_pag
   return s;
 }
 
-// Splits launched per unit.
-__host__ __device__ inline int attn_grid_splits(int units, int max_gather_pages, int slots) {
+// Splits launched per unit; in workspace mode they hold at least mn pages each.
+__host__ __device__ inline int attn_grid_splits(int units, int max_gather_pages, int slots, int mn) {
   if (attn_cluster_mode(units, max_gather_pages)) return attn_cluster_splits(units, max_gather_pages, slots);
-  const int mn = attn_min_split_pages(max_gather_pages);
   int splits = (max_gather_pages + mn - 1) / mn;
   if (splits > kAttnMaxSplits) splits = kAttnMaxSplits;
   return splits < 1 ? 1 : splits;

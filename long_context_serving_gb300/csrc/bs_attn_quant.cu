@@ -5,25 +5,30 @@
 // With ks, vs the scales of token t's page and K8, V8 its codes:
 //   x_h(t) = ks (q_h . K8[t]) log2(e) / sqrt(d) + bias2,   o_h += vs (2^(x_h(t) - m) V8[t]).
 //
-// A warp takes whole pages and keeps everything in registers; no shared memory and no CTA
-// barrier in the loop. The codes come straight from global memory in 16-byte loads (D = 64:
-// V in 8-byte ones), the next page's in flight while one is computed: 2 D bytes of K and V
-// a token leave too little arithmetic per byte for staging through shared memory to pay, and
-// each lane needs its own bytes only. Fragment layouts are chosen around those loads; lane
-// = 4 r + c:
-//   K: lane holds 16-byte chunks c (and c + 4) of tokens r and r + 8. A k-step of the MMA may
+// A warp takes whole pages, two at a time, out of a ring of its own in shared memory: four
+// pages of K and four of V, filled by 16-byte asynchronous copies (cp.async) and drained
+// without a CTA barrier. While a pair's scores are computed its V and the next pair's K and V
+// are in flight; its K slots are refilled once the scores are done, its V slots once the
+// values are: 12 to 16 KB in flight a warp, 12 warps an SM. (Codes loaded straight into
+// registers instead, the next pair's in flight, left fewer bytes in flight: DESIGN's table.)
+// Rows are stored with their 16-byte chunks permuted (swz8), so that the reads below are free
+// of bank conflicts (D = 64: V two-way). Fragment layouts are chosen around 16-byte reads;
+// lane = 4 r + c:
+//   K: lane reads chunks 2c, 2c + 1 (D = 64: c) of tokens r and r + 8. A k-step of the MMA may
 //     take any 16 dimensions as long as q agrees, so the four words of a chunk feed four
 //     k-steps: S[16 x 8] = q K8^T with the heads as rows (rows 8..15: the low parts of q,
 //     for an fp32 query) and eight tokens as columns, two such tiles a page.
 //   S leaves lane (r, c) with head r, tokens 2c, 2c + 1, 8 + 2c, 9 + 2c: already the B
 //     fragment of P^T in O^T = V8^T P^T (k = tokens, n = heads).
-//   V: lane holds chunk r (D / 8 dimensions) of those same four tokens, and pairs the tokens'
+//   V: lane reads chunk r (D / 8 dimensions) of those same four tokens, and pairs the tokens'
 //     bytes with one byte permutation per four codes before converting.
 // Precision: the codes are exact in fp16; a query row is multiplied by a power of two that
 // brings its largest element near 2^14 and enters as fp16 hi + lo (bf16 queries: hi alone is
 // exact down to 2^-39 of the row's largest element); P is scaled by 2^14 and enters as hi +
 // lo, so that weights down to 2^-28 of the largest keep 22 bits; sums are fp32. The V scale is
 // applied to each page's product in fp32, so no scale can leave fp16's range.
+#include <algorithm>
+
 #include "bs_attn_impl.cuh"
 #include "bs_attn_launch.cuh"
 #include "bs_quant.cuh"
@@ -33,22 +38,56 @@ namespace {
 
 constexpr int kQuantThreads = 128;   // 4 warps
 constexpr int kQuantWarps = kQuantThreads / 32;
+constexpr int kCtasPerSm = 2;
+constexpr int kMinSplit = 8;
 constexpr float kPShift = 14.0f;     // P enters as 2^(x - m + 14)
 
-// Shared memory: the staged selection entries, then (after the loop) the warps' states.
+// Shared memory: the staged selection entries, then the warps' rings; after the loop the
+// warps' states and the merge's scratch take the rings' place.
+constexpr int kRing = 2;             // pages of K (and of V) in a warp's ring: two pairs
 template <int D>
 struct QuantLayout {
-  static constexpr int kOffO = kSelPreload * 4;                              // [4][8][D]
+  static constexpr int kPageBytes = kPage * D;
+  static constexpr int kOffRing = kSelPreload * 4;                           // per warp: K [4], V [4]
+  static constexpr int kWarpBytes = 2 * kRing * kPageBytes;
+  static constexpr int kOffO = kOffRing;                                     // [4][8][D]
   static constexpr int kOffMl = kOffO + kQuantWarps * kMaxG * D * 4;         // m, l: [2][4][8]
   static constexpr int kOffSum = kOffMl + 2 * kQuantWarps * kMaxG * 4;       // [8][D]
   static constexpr int kOffScratch = kOffSum + kMaxG * D * 4;                // merge scratch
-  static constexpr int kBytes = kOffScratch + 3 * kMaxG * kAttnMaxSplits * 4;
+  static constexpr int kBytes = kOffRing + kQuantWarps * kWarpBytes;
+  static_assert(kOffScratch + 3 * kMaxG * kAttnMaxSplits * 4 <= kBytes, "the epilogue fits in the rings");
 };
+
+// Byte offset of 16-byte chunk `ch` of row `row` of a page in a ring slot.
+template <int D>
+__device__ __forceinline__ int swz8(int row, int ch) {
+  return D == 128 ? row * 128 + ((ch ^ (row & 7)) << 4) : row * 64 + ((ch ^ ((row >> 1) & 3)) << 4);
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// A page's codes into a ring slot (all 32 lanes; whole rows a warp instruction).
+template <int D>
+__device__ __forceinline__ void copy_page(uint32_t slot, const uint8_t *pool, int phys) {
+  constexpr int kChunks = D / 16;
+  const int lane = threadIdx.x & 31;
+  const uint8_t *src = pool + static_cast<size_t>(phys) * (kPage * D) + lane * 16;
+#pragma unroll
+  for (int i = 0; i < kPage * kChunks / 32; ++i) {
+    const int at = i * 32 + lane;
+    cp_async16(slot + swz8<D>(at / kChunks, at % kChunks), src + i * 512);
+  }
+}
 
 // D = A B + D, m16n8k16, fp16 inputs, fp32 accumulators.
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                         uint32_t b0, uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -62,40 +101,15 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 __device__ __forceinline__ float f16_lo_f(uint32_t w) { return __half2float(__ushort_as_half(w & 0xffffu)); }
 __device__ __forceinline__ float f16_hi_f(uint32_t w) { return __half2float(__ushort_as_half(w >> 16)); }
 
-// The codes of one page that a lane holds.
-template <int D>
-struct PageRegs {
-  uint4 k[D / 64][2];                                                       // [chunk c, c + 4][token r, r + 8]
-  uint32_t v[4][D / 32];                                                    // tokens 2c, 2c+1, 2c+8, 2c+9
-};
+// What a page's codes mean; valid = 0: the page does not count and nothing of it is read.
 struct PageMeta {
-  int valid;        // tokens that count (0: the page is skipped)
+  int valid;
   float ks, vs, bias2;
 };
 
-template <int D>
-__device__ __forceinline__ void load_page(const uint8_t *kpg, const uint8_t *vpg, PageRegs<D> &p) {
-  const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
-#pragma unroll
-  for (int j = 0; j < D / 64; ++j)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) p.k[j][i] = ldg_stream16(kpg + (r + 8 * i) * D + (c + 4 * j) * 16);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint8_t *src = vpg + (2 * c + (i & 1) + 8 * (i >> 1)) * D + r * (D / 8);
-    if constexpr (D == 128) {
-      const uint4 w = ldg_stream16(src);
-      p.v[i][0] = w.x; p.v[i][1] = w.y; p.v[i][2] = w.z; p.v[i][3] = w.w;
-    } else {
-      const uint2 w = ldg_stream8(src);
-      p.v[i][0] = w.x; p.v[i][1] = w.y;
-    }
-  }
-}
-
 // The query rows of a unit as A fragments in the dimension order of the K loads, times
 // 2^e with the row's largest element near 2^14; *unscale gets 2^-e (head r of this lane).
-template <int D, int G8, bool Q32>
+template <int D, bool Q32>
 __device__ __forceinline__ void load_q_f16(const void *q, size_t orow0, int G, uint32_t (&hi)[D / 16][2],
                                            uint32_t (&lo)[D / 16][2], float *unscale) {
   const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
@@ -106,7 +120,7 @@ __device__ __forceinline__ void load_q_f16(const void *q, size_t orow0, int G, u
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[s][i] = 0.0f;
     if (r < G) {
-      const size_t at = (orow0 + r) * D + 16 * (c + 4 * (s / 4)) + 4 * (s % 4);
+      const size_t at = (orow0 + r) * D + 16 * (D == 128 ? 2 * c + s / 4 : c) + 4 * (s % 4);
       if constexpr (Q32) {
         const float4 w = *reinterpret_cast<const float4 *>(static_cast<const float *>(q) + at);
         x[s][0] = w.x; x[s][1] = w.y; x[s][2] = w.z; x[s][3] = w.w;
@@ -148,38 +162,87 @@ struct WarpState {
   float o[D / 16][4];
 };
 
+// S = q K8^T of the page in `slot`: two tiles of eight tokens; x[i] of token 2c + (i & 1) +
+// 8 (i >> 1).
 template <int D, bool I8, bool Q32>
-__device__ __forceinline__ void quant_page(const PageRegs<D> &p, const PageMeta &t, const uint32_t (&qh)[D / 16][2],
-                                           const uint32_t (&ql)[D / 16][2], float q_scale, WarpState<D> &w) {
-  const int lane = threadIdx.x & 31, c = lane & 3;
-  // ---- S = q K8^T: two tiles of eight tokens --------------------------------------------
+__device__ __forceinline__ void page_scores(const unsigned char *slot, const PageMeta &t, const uint32_t (&qh)[D / 16][2],
+                                            const uint32_t (&ql)[D / 16][2], float q_scale, float *x) {
+  const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
   float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
-  for (int j = 0; j < D / 64; ++j)
+  for (int j = 0; j < D / 64; ++j) {
+    uint4 w[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const uint32_t word[4] = {p.k[j][i].x, p.k[j][i].y, p.k[j][i].z, p.k[j][i].w};
+    for (int i = 0; i < 2; ++i)
+      w[i] = *reinterpret_cast<const uint4 *>(slot + swz8<D>(r + 8 * i, D == 128 ? 2 * c + j : c));
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
         uint32_t b0, b1;
-        codes_to_f16<I8>(word[k], b0, b1);
+        codes_to_f16<I8>(k == 0 ? w[i].x : k == 1 ? w[i].y : k == 2 ? w[i].z : w[i].w, b0, b1);
         mma_f16(s[i], qh[4 * j + k][0], ql[4 * j + k][0], qh[4 * j + k][1], ql[4 * j + k][1], b0, b1);
       }
-    }
+  }
   const float f = q_scale * t.ks;
-  float x[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float dot = Q32 ? s[i >> 1][i & 1] + s[i >> 1][2 + (i & 1)] : s[i >> 1][i & 1];
     x[i] = fmaf(dot, f, t.bias2);
   }
+}
+
+// O^T += vs V8^T P^T of the page in `slot` (h, l: P as fp16 pairs, hi and lo). Codes of tokens
+// that do not count may be anything (NaN too) and are zeroed.
+template <int D, bool I8>
+__device__ __forceinline__ void page_values(const unsigned char *slot, const PageMeta &t, const uint32_t (&h)[2],
+                                            const uint32_t (&l)[2], WarpState<D> &w) {
+  const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+  uint32_t v[4][D / 32];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int tok = 2 * c + (i & 1) + 8 * (i >> 1);
+    if constexpr (D == 128) {
+      const uint4 x = *reinterpret_cast<const uint4 *>(slot + swz8<D>(tok, r));
+      v[i][0] = x.x; v[i][1] = x.y; v[i][2] = x.z; v[i][3] = x.w;
+    } else {
+      const uint2 x = *reinterpret_cast<const uint2 *>(slot + swz8<D>(tok, r >> 1) + 8 * (r & 1));
+      v[i][0] = x.x; v[i][1] = x.y;
+    }
+  }
   if (t.valid < kPage) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (2 * c + (i & 1) + 8 * (i >> 1) >= t.valid) x[i] = -INFINITY;
+      if (2 * c + (i & 1) + 8 * (i >> 1) >= t.valid) {
+#pragma unroll
+        for (int g = 0; g < D / 32; ++g) v[i][g] = 0u;
+      }
   }
-  // ---- online softmax: this lane's head over the page's 16 tokens -------------------------
-  float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+#pragma unroll
+  for (int g = 0; g < D / 32; ++g) {      // four dimensions of the lane's chunk
+    const uint32_t v0 = v[0][g], v1 = v[1][g], v2 = v[2][g], v3 = v[3][g];
+    uint32_t a[4], b[4];                   // fp16 pairs of tokens (2c, 2c+1) and (2c+8, 2c+9) per dimension
+    codes_to_f16<I8>(__byte_perm(v0, v1, 0x5140), a[0], a[1]);
+    codes_to_f16<I8>(__byte_perm(v0, v1, 0x7362), a[2], a[3]);
+    codes_to_f16<I8>(__byte_perm(v2, v3, 0x5140), b[0], b[1]);
+    codes_to_f16<I8>(__byte_perm(v2, v3, 0x7362), b[2], b[3]);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+      mma_f16(acc, a[2 * i], a[2 * i + 1], b[2 * i], b[2 * i + 1], h[0], h[1]);
+      mma_f16(acc, a[2 * i], a[2 * i + 1], b[2 * i], b[2 * i + 1], l[0], l[1]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) w.o[2 * g + i][k] = fmaf(acc[k], t.vs, w.o[2 * g + i][k]);
+    }
+  }
+}
+
+// Online softmax of this lane's head over the 32 tokens of two pages: x becomes the weights
+// 2^(x - m + 14), the running state is rescaled when the maximum rises.
+template <int D>
+__device__ __forceinline__ void softmax_pair(float (&x)[8], WarpState<D> &w) {
+  const int c = threadIdx.x & 3;
+  float mx = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
   mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
   mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
   if (__any_sync(0xffffffffu, mx > w.m)) {
@@ -197,38 +260,15 @@ __device__ __forceinline__ void quant_page(const PageRegs<D> &p, const PageMeta 
     }
   }
   const float base = w.m == -INFINITY ? 0.0f : w.m - kPShift;
-  float pr[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) pr[i] = exp2f(x[i] - base);
-  w.l += (pr[0] + pr[1]) + (pr[2] + pr[3]);
-  const uint32_t h0 = pack_f16(pr[0], pr[1]), h1 = pack_f16(pr[2], pr[3]);
-  const uint32_t l0 = pack_f16(pr[0] - f16_lo_f(h0), pr[1] - f16_hi_f(h0));
-  const uint32_t l1 = pack_f16(pr[2] - f16_lo_f(h1), pr[3] - f16_hi_f(h1));
-  // ---- O^T += vs V8^T P^T -----------------------------------------------------------------
-  // Codes past T may be anything (NaN too): zeroed.
-  uint32_t keep[4] = {~0u, ~0u, ~0u, ~0u};
-  if (t.valid < kPage) {
+  for (int i = 0; i < 8; ++i) x[i] = exp2f(x[i] - base);
+  w.l += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+}
+__device__ __forceinline__ void split_weights(const float *x, uint32_t (&h)[2], uint32_t (&l)[2]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (2 * c + (i & 1) + 8 * (i >> 1) >= t.valid) keep[i] = 0u;
-  }
-#pragma unroll
-  for (int g = 0; g < D / 32; ++g) {      // four dimensions of the lane's chunk
-    const uint32_t v0 = p.v[0][g] & keep[0], v1 = p.v[1][g] & keep[1];
-    const uint32_t v2 = p.v[2][g] & keep[2], v3 = p.v[3][g] & keep[3];
-    uint32_t a[4], b[4];                   // fp16 pairs of tokens (2c, 2c+1) and (2c+8, 2c+9) per dimension
-    codes_to_f16<I8>(__byte_perm(v0, v1, 0x5140), a[0], a[1]);
-    codes_to_f16<I8>(__byte_perm(v0, v1, 0x7362), a[2], a[3]);
-    codes_to_f16<I8>(__byte_perm(v2, v3, 0x5140), b[0], b[1]);
-    codes_to_f16<I8>(__byte_perm(v2, v3, 0x7362), b[2], b[3]);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float acc[4] = {0.f, 0.f, 0.f, 0.f};
-      mma_f16(acc, a[2 * i], a[2 * i + 1], b[2 * i], b[2 * i + 1], h0, h1);
-      mma_f16(acc, a[2 * i], a[2 * i + 1], b[2 * i], b[2 * i + 1], l0, l1);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) w.o[2 * g + i][k] = fmaf(acc[k], t.vs, w.o[2 * g + i][k]);
-    }
+  for (int i = 0; i < 2; ++i) {
+    h[i] = pack_f16(x[2 * i], x[2 * i + 1]);
+    l[i] = pack_f16(x[2 * i] - f16_lo_f(h[i]), x[2 * i + 1] - f16_hi_f(h[i]));
   }
 }
 
@@ -266,6 +306,10 @@ __device__ bool attn_split_quant(const AttnArgs &a, unsigned char *smem, bool in
   if (split >= n_part) return false;
 
   prefetch_page_row<NT>(dims, a.kv, a.cfg, a.plist, u, in_step);
+  uint32_t qh[D / 16][2], ql[D / 16][2];
+  float q_scale;
+  load_q_f16<D, Q32>(a.q, orow0, G, qh, ql, &q_scale);   // (in flight beside the block list's loads)
+  q_scale *= rsqrtf(static_cast<float>(D)) * kLog2e;
   UnitBlocks ub = load_unit_blocks<NT>(a, u, sel_sm, in_step, in_cluster);
   check_split_bound(ub, n_part, split, st);
   // Every split taking part stays to the end (see attn_split_mma).
@@ -276,54 +320,102 @@ __device__ bool attn_split_quant(const AttnArgs &a, unsigned char *smem, bool in
   const uint8_t *kpool = static_cast<const uint8_t *>(a.kv.k_pool);
   const uint8_t *vpool = static_cast<const uint8_t *>(a.kv.v_pool);
 
-  // This warp's pages: gp0 + warp + W i, i < n_mine; resolved 32 at a time, one per lane.
+  // This warp's pages: gp0 + warp + W i, i < n_mine; resolved 32 at a time, one per lane. The
+  // copies run up to kRing pages ahead of the arithmetic, so the chunk before is kept too.
+  struct Chunk {
+    int phys, valid;
+    float ks, vs, bias2;
+  };
   const int n_mine = gp1 - gp0 > warp ? (gp1 - gp0 - warp + W - 1) / W : 0;
-  int chunk = -1, ch_phys = 0, ch_valid = 0;
-  float ch_ks = 0.0f, ch_vs = 0.0f, ch_bias = 0.0f;
-  auto fetch = [&](int i, PageRegs<D> &p, PageMeta &t) {
-    if (i / 32 != chunk) {
-      chunk = i / 32;
-      int phys = -1, blk = -1;
-      ch_valid = resolve_page(ub, dims, pt, gp0 + warp + W * (chunk * 32 + lane), gp1, &phys, a.bias ? &blk : nullptr, st);
-      ch_phys = ch_valid > 0 ? phys : 0;
-      ch_bias = block_bias2(a.bias, dims, u, blk, st);
-      if (ch_bias == -INFINITY) ch_valid = 0;   // the block dropped out: nothing of it is read
-      ch_ks = ch_valid > 0 ? __ldg(a.kv.k_scale + ch_phys) : 0.0f;
-      ch_vs = ch_valid > 0 ? __ldg(a.kv.v_scale + ch_phys) : 0.0f;
-    }
+  int chunk = -1;
+  Chunk now = {0, 0, 0.0f, 0.0f, 0.0f}, before = now;
+  unsigned char *ring = smem + L::kOffRing + warp * L::kWarpBytes;
+  const uint32_t kring = smem_u32(ring), vring = kring + kRing * L::kPageBytes;
+  auto meta = [&](int i) {
+    const bool cur = i / 32 == chunk;
     const int src = i & 31;
-    const int phys = __shfl_sync(0xffffffffu, ch_phys, src);
-    t.valid = __shfl_sync(0xffffffffu, ch_valid, src);
-    t.ks = __shfl_sync(0xffffffffu, ch_ks, src);
-    t.vs = __shfl_sync(0xffffffffu, ch_vs, src);
-    t.bias2 = __shfl_sync(0xffffffffu, ch_bias, src);
-    if (t.valid > 0) {
-      const size_t off = static_cast<size_t>(phys) * (kPage * D);
-      load_page<D>(kpool + off, vpool + off, p);
+    PageMeta t;
+    t.valid = i < n_mine ? __shfl_sync(0xffffffffu, cur ? now.valid : before.valid, src) : 0;
+    t.ks = __shfl_sync(0xffffffffu, cur ? now.ks : before.ks, src);
+    t.vs = __shfl_sync(0xffffffffu, cur ? now.vs : before.vs, src);
+    t.bias2 = __shfl_sync(0xffffffffu, cur ? now.bias2 : before.bias2, src);
+    return t;
+  };
+  // Starts the copies of page i's K (or V); one group per pair, empty past the end.
+  auto copy = [&](int i, uint32_t to, const uint8_t *pool) {
+    if (i >= n_mine) return;
+    const bool cur = i / 32 == chunk;
+    const int valid = __shfl_sync(0xffffffffu, cur ? now.valid : before.valid, i & 31);
+    const int phys = __shfl_sync(0xffffffffu, cur ? now.phys : before.phys, i & 31);
+    if (valid > 0) copy_page<D>(to + (i % kRing) * L::kPageBytes, pool, phys);
+  };
+  auto copy_k = [&](int i) {
+    if (i < n_mine && i / 32 != chunk) {   // (i is even: a pair lies in one chunk)
+      before = now;
+      chunk = i / 32;
+      int blk = -1;
+      now.valid = resolve_page(ub, dims, pt, gp0 + warp + W * (chunk * 32 + lane), gp1, &now.phys, a.bias ? &blk : nullptr, st);
+      now.bias2 = block_bias2(a.bias, dims, u, blk, st);
+      if (now.bias2 == -INFINITY) now.valid = 0;   // the block dropped out: nothing of it is read
+      now.ks = now.valid > 0 ? __ldg(a.kv.k_scale + now.phys) : 0.0f;
+      now.vs = now.valid > 0 ? __ldg(a.kv.v_scale + now.phys) : 0.0f;
     }
+    copy(i, kring, kpool);
+    copy(i + 1, kring, kpool);
+    cp_commit();
+  };
+  auto copy_v = [&](int i) {
+    copy(i, vring, vpool);
+    copy(i + 1, vring, vpool);
+    cp_commit();
   };
 
-  uint32_t qh[D / 16][2], ql[D / 16][2];
-  float q_scale;
-  PageRegs<D> pa, pb;
-  PageMeta ta, tb;
-  ta.valid = tb.valid = 0;
-  if (n_mine > 0) fetch(0, pa, ta);
-  load_q_f16<D, kMaxG, Q32>(a.q, orow0, G, qh, ql, &q_scale);
-  q_scale *= rsqrtf(static_cast<float>(D)) * kLog2e;
   WarpState<D> w;
   w.m = -INFINITY;
   w.l = 0.0f;
 #pragma unroll
   for (int i = 0; i < D / 16; ++i) w.o[i][0] = w.o[i][1] = w.o[i][2] = w.o[i][3] = 0.0f;
-  for (int i = 0; i < n_mine; i += 2) {
-    tb.valid = 0;
-    if (i + 1 < n_mine) fetch(i + 1, pb, tb);
-    if (ta.valid > 0) quant_page<D, I8, Q32>(pa, ta, qh, ql, q_scale, w);
-    ta.valid = 0;
-    if (i + 2 < n_mine) fetch(i + 2, pa, ta);
-    if (tb.valid > 0) quant_page<D, I8, Q32>(pb, tb, qh, ql, q_scale, w);
+#pragma unroll
+  for (int i = 0; i < kRing; i += 2) {
+    copy_k(i);
+    copy_v(i);
   }
+  for (int i = 0; i < n_mine; i += 2) {
+    const unsigned char *ks = ring + (i % kRing) * L::kPageBytes, *vs = ks + kRing * L::kPageBytes;
+    const PageMeta t[2] = {meta(i), meta(i + 1)};
+    const bool any = t[0].valid + t[1].valid > 0;   // (none: dropped, or outside the pool)
+    cp_wait<kRing - 1>();            // this pair's K has landed
+    __syncwarp();
+    float x[8];
+    if (any) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) page_scores<D, I8, Q32>(ks + j * L::kPageBytes, t[j], qh, ql, q_scale, x + 4 * j);
+    }
+    __syncwarp();
+    copy_k(i + kRing);
+    cp_wait<kRing - 1>();            // its V too
+    __syncwarp();
+    if (any) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        if (t[j].valid < kPage) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (2 * (lane & 3) + (k & 1) + 8 * (k >> 1) >= t[j].valid) x[4 * j + k] = -INFINITY;
+        }
+      softmax_pair<D>(x, w);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        uint32_t h[2], l[2];
+        split_weights(x + 4 * j, h, l);
+        page_values<D, I8>(vs + j * L::kPageBytes, t[j], h, l, w);
+      }
+    }
+    __syncwarp();
+    copy_v(i + kRing);
+  }
+  cp_wait<0>();
+  __syncthreads();           // the rings' place is taken by the states below
 
   // ---- combine the four warps' states ---------------------------------------------
   float *ow = reinterpret_cast<float *>(smem + L::kOffO);     // [4][8][D]
@@ -392,7 +484,7 @@ __device__ bool attn_split_quant(const AttnArgs &a, unsigned char *smem, bool in
 }
 
 template <int D, bool I8, bool Q32>
-__global__ void __launch_bounds__(kQuantThreads) attn_quant_kernel(const __grid_constant__ AttnArgs a, bool step, bool cluster) {
+__global__ void __launch_bounds__(kQuantThreads, kCtasPerSm) attn_quant_kernel(const __grid_constant__ AttnArgs a, bool step, bool cluster) {
   extern __shared__ __align__(16) unsigned char smem[];
   if (step) pdl_launch_dependents();
   const bool took_part = attn_split_quant<D, I8, Q32>(a, smem, step, cluster);
@@ -402,16 +494,25 @@ __global__ void __launch_bounds__(kQuantThreads) attn_quant_kernel(const __grid_
 }
 
 template <int D, bool I8, bool Q32>
-bs_status launch_quant(const AttnArgs &a, bool step, cudaStream_t cs) {
+bs_status launch_quant(AttnArgs a, bool step, cudaStream_t cs) {
   const int units = a.dims.batch * a.dims.n_kv_heads;
+  const int mg = a.dims.max_gather_pages_per_unit;
+  if (mg <= kClusterMaxPages) {
+    const int slots = attn_target_ctas() / 2 * kCtasPerSm;
+    const int64_t even = (static_cast<int64_t>(units) * mg + slots - 1) / slots;
+    a.min_split = static_cast<int>(std::max<int64_t>(kMinSplit, (even + kQuantWarps - 1) / kQuantWarps * kQuantWarps));
+  }
   constexpr int smem = QuantLayout<D>::kBytes;
-  static_assert(smem <= 48 * 1024, "within the default dynamic shared memory");
   auto kernel = attn_quant_kernel<D, I8, Q32>;
   static const bool attrs_ok =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess &&
       cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
   if (!attrs_ok) return BS_ERR_CUDA;
-  const bool cluster = attn_mode(units, a.dims.max_gather_pages_per_unit) == kModeCluster;
-  const int splits = attn_grid_splits(units, a.dims.max_gather_pages_per_unit, attn_target_ctas());
+  const bool cluster = attn_mode(units, mg) == kModeCluster;
+  int splits = attn_grid_splits(units, mg, attn_target_ctas(), a.min_split);
+  // A cluster's merge costs more than a few pages: no more splits than leave each kMinSplit.
+  if (cluster)
+    while (splits > 1 && mg < splits * kMinSplit) splits >>= 1;
   const dim3 grid = cluster ? dim3(splits, units) : dim3(units, splits);   // (workspace mode: unit-major)
   const cudaError_t e =
       launch_ex(kernel, grid, kQuantThreads, smem, cs, cluster && splits > 1 ? splits : 0, step, a, step, cluster);

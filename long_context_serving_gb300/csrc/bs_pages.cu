@@ -2,18 +2,22 @@
 //
 // A page is free when its reference count is 0. Which free page a call takes is fixed (the
 // k-th page asked for gets the k-th lowest free one), so everything rests on ranks:
-//   * a scan kernel turns the counts into a bitmap of free pages (a ballot per 32 pages) with
-//     each word's rank inside its tile and a count per tile, at most kMaxTiles tiles; beside
-//     it, other CTAs of the same launch count what each unit asks for and check the arguments;
-//   * the next kernel, on the same stream, sums tiles and requests before its own (block
-//     scans over at most kMaxTiles and `units` ints) and gives each request its page: binary
-//     search over the tiles' ranks, over the tile's words, then inside the word.
-// The bitmap is a snapshot, so counts may be written while others still look pages up, and no
+//   * a scan kernel reads the counts once: each tile (at most kMaxTiles of them) lists its free
+//     pages in ascending order and counts them (and, for compact, keeps their bitmap with each
+//     word's rank); beside it, other CTAs of the same launch count what each unit asks for and
+//     check the arguments;
+//   * the next kernel, a programmatic dependent (it starts up while the scan runs), sums tiles
+//     and requests before its own (block scans over at most kMaxTiles and `units` ints) and
+//     gives each request its page: a binary search over the tiles' ranks in shared memory, then
+//     one load from the tile's list. (Binary searches over bitmap words instead: a request cost
+//     about fifteen dependent loads; a batch turnover of 43K pages took 25.6 us, now TURNOVER.)
+// The lists are a snapshot, so counts may be written while others still look pages up, and no
 // floating-point or order-dependent atomics are involved: integer counts only.
 // Bound by latency (a few dependent loads a launch) except for the copies, which are bound by
 // HBM.
 #include <algorithm>
 
+#include "bs_attn_launch.cuh"
 #include "bs_quant.cuh"
 
 namespace bsi {
@@ -24,6 +28,8 @@ constexpr int kPgWarps = kPgThreads / 32;
 constexpr int kMaxTiles = 1024;
 constexpr int kMinTilePages = 4096;
 constexpr int kApplyCtas = 304;     // two CTAs per SM
+constexpr int kMaxCtas = 8 * kApplyCtas;   // one wave; each takes a contiguous share beyond
+constexpr int kBatch = 4;           // row entries a thread has in flight at once
 
 __host__ __device__ inline int64_t tile_pages_for(int64_t n_pages) {
   int64_t t = kMinTilePages;
@@ -32,21 +38,22 @@ __host__ __device__ inline int64_t tile_pages_for(int64_t n_pages) {
 }
 
 // Workspace (int32 words): header [8] | tile_free [kMaxTiles] | need [units] | err [units] |
-// bitmap [words] | word rank [words] | remap [n_pages].
+// bitmap [words] | word rank [words] | list [n_pages] | remap [n_pages].
 struct PgWs {
   int32_t *head;        // [0] pages in use, [1] moves allowed (compact)
   int32_t *tile_free;
   int32_t *need, *err;
   uint32_t *bits;
   int32_t *rank;        // free pages of the word's tile before the word
-  int32_t *remap;
+  int32_t *list;        // tile t's free pages, ascending, from list[t * tile_pages]
+  int32_t *remap;       // where a moved page went
   int32_t n_tiles;
   int64_t n_words, tile_pages;
 };
 __host__ inline size_t pg_ws_ints(const bs_dims &d) {
   const size_t units = static_cast<size_t>(d.batch) * d.n_kv_heads;
   const size_t words = (static_cast<size_t>(d.n_pages) + 31) / 32;
-  return 8 + kMaxTiles + 2 * units + 2 * words + static_cast<size_t>(d.n_pages);
+  return 8 + kMaxTiles + 2 * units + 2 * words + 2 * static_cast<size_t>(d.n_pages);
 }
 __host__ inline PgWs pg_ws(const bs_dims &d, void *workspace) {
   const size_t units = static_cast<size_t>(d.batch) * d.n_kv_heads;
@@ -60,9 +67,13 @@ __host__ inline PgWs pg_ws(const bs_dims &d, void *workspace) {
   w.err = w.need + units;
   w.bits = reinterpret_cast<uint32_t *>(w.err + units);
   w.rank = reinterpret_cast<int32_t *>(w.bits + w.n_words);
-  w.remap = w.rank + w.n_words;
+  w.list = w.rank + w.n_words;
+  w.remap = w.list + d.n_pages;
   return w;
 }
+
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // Exclusive prefix sum of one int per thread over the CTA; *total gets the sum. All threads.
 __device__ __forceinline__ int cta_scan(int v, int *tmp, int *total) {
@@ -109,12 +120,14 @@ __device__ __forceinline__ int cta_max(int v, int *tmp) {
 }
 
 // ---------------------------------------------------------------------------
-// Tile t of the counts: the bitmap's words, their ranks, the tile's count.
+// Tile t of the counts: the list of its free pages, their number and, with `words`, the
+// bitmap's words and ranks.
 // ---------------------------------------------------------------------------
-__device__ void scan_tile(const bs_dims &dims, const int32_t *ref, const PgWs &ws, int t) {
+__device__ void scan_tile(const bs_dims &dims, const int32_t *ref, const PgWs &ws, int t, bool words) {
   __shared__ int tmp[kPgWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   __shared__ uint32_t wsm[kMinTilePages / 32];
+  __shared__ int rsm[kMinTilePages / 32];
   const int64_t p0 = static_cast<int64_t>(t) * ws.tile_pages;
   const int64_t p1 = min(p0 + ws.tile_pages, dims.n_pages);
   int run = 0;
@@ -137,10 +150,23 @@ __device__ void scan_tile(const bs_dims &dims, const int32_t *ref, const PgWs &w
     int total;
     const int before = cta_scan(__popc(mine), tmp, &total);
     if (tid < n_words) {
-      ws.bits[q / 32 + tid] = mine;
-      ws.rank[q / 32 + tid] = run + before;
+      rsm[tid] = run + before;
+      if (words) {
+        ws.bits[q / 32 + tid] = mine;
+        ws.rank[q / 32 + tid] = run + before;
+      }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int w = warp * kPer + i;
+      if (v[i] == 0) {   // (0 only for a page of the pool)
+        const uint32_t below = wsm[w] & ((1u << lane) - 1u);
+        ws.list[p0 + rsm[w] + __popc(below)] = static_cast<int32_t>(q + w * 32 + lane);
+      }
     }
     run += total;
+    __syncthreads();
   }
   if (tid == 0) ws.tile_free[t] = run;
 }
@@ -182,16 +208,7 @@ __device__ __forceinline__ int kth_free(const PgWs &ws, const int *before, int k
     if (before[mid] <= k) lo = mid;
     else hi = mid - 1;
   }
-  k -= before[lo];
-  const int64_t w_tile = ws.tile_pages / 32;
-  int64_t a = static_cast<int64_t>(lo) * w_tile, b = min(a + w_tile, ws.n_words) - 1;
-  while (a < b) {                         // the last word that starts at rank <= k
-    const int64_t mid = (a + b + 1) >> 1;
-    if (ws.rank[mid] <= k) a = mid;
-    else b = mid - 1;
-  }
-  k -= ws.rank[a];
-  return static_cast<int>(a * 32) + static_cast<int>(__fns(ws.bits[a], 0, k + 1));
+  return ws.list[lo * ws.tile_pages + (k - before[lo])];
 }
 
 // What the units before `first` ask for, what all ask for, and the worst error of any
@@ -222,8 +239,9 @@ __device__ __forceinline__ Requests sum_requests(const PgWs &ws, int n, int firs
 // reserve
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(kPgThreads) reserve_scan(bs_dims dims, bs_page_map map, const int32_t *new_lens, PgWs ws) {
+  pdl_trigger();
   if (static_cast<int>(blockIdx.x) < ws.n_tiles) {
-    scan_tile(dims, map.ref_count, ws, blockIdx.x);
+    scan_tile(dims, map.ref_count, ws, blockIdx.x, false);
     return;
   }
   __shared__ long long tmp[kPgWarps];
@@ -249,6 +267,7 @@ __global__ void __launch_bounds__(kPgThreads) reserve_apply(bs_dims dims, bs_pag
   __shared__ int before[kMaxTiles + 1];
   __shared__ int tmp[kPgWarps];
   const int units = dims.batch * dims.n_kv_heads;
+  pdl_wait();
   // A contiguous share of the units per CTA.
   const int u0 = static_cast<int>(static_cast<int64_t>(units) * blockIdx.x / gridDim.x);
   const int u1 = static_cast<int>(static_cast<int64_t>(units) * (blockIdx.x + 1) / gridDim.x);
@@ -263,16 +282,27 @@ __global__ void __launch_bounds__(kPgThreads) reserve_apply(bs_dims dims, bs_pag
     if (ws.need[u] == 0) continue;
     const int n = static_cast<int>((static_cast<int64_t>(max(new_lens[u / dims.n_kv_heads], 0)) + kPage - 1) / kPage);
     int32_t *row = map.page_table + static_cast<size_t>(u) * dims.max_pages_per_unit;
-    for (int i0 = 0; i0 < n; i0 += kPgThreads) {
-      const int i = i0 + threadIdx.x;
-      const bool lacks = i < n && row[i] < 0;
-      int total;
-      const int r = cta_scan(lacks ? 1 : 0, tmp, &total);
-      if (lacks) {
-        const int p = kth_free(ws, before, k + r);
-        row[i] = p;
-        map.ref_count[p] = 1;
+    for (int i0 = 0; i0 < n; i0 += kPgThreads * kBatch) {
+      const int first = i0 + threadIdx.x * kBatch;   // a thread's entries are neighbours: ranks ascend
+      bool lacks[kBatch];
+      int mine = 0;
+#pragma unroll
+      for (int e = 0; e < kBatch; ++e) {
+        lacks[e] = first + e < n && row[first + e] < 0;
+        mine += lacks[e] ? 1 : 0;
       }
+      int total;
+      int r = k + cta_scan(mine, tmp, &total);
+      int page[kBatch];
+#pragma unroll
+      for (int e = 0; e < kBatch; ++e)
+        if (lacks[e]) page[e] = kth_free(ws, before, r++);
+#pragma unroll
+      for (int e = 0; e < kBatch; ++e)
+        if (lacks[e]) {
+          row[first + e] = page[e];
+          map.ref_count[page[e]] = 1;
+        }
       k += total;
     }
   }
@@ -283,8 +313,9 @@ __global__ void __launch_bounds__(kPgThreads) reserve_apply(bs_dims dims, bs_pag
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(kPgThreads) fork_scan(bs_dims dims, bs_page_map map, const int32_t *src, const int32_t *dst,
                                                         int n, PgWs ws) {
+  pdl_trigger();
   if (static_cast<int>(blockIdx.x) < ws.n_tiles) {
-    scan_tile(dims, map.ref_count, ws, blockIdx.x);
+    scan_tile(dims, map.ref_count, ws, blockIdx.x, false);
     return;
   }
   __shared__ int tmp[kPgWarps];
@@ -304,6 +335,7 @@ __global__ void __launch_bounds__(kPgThreads) fork_scan(bs_dims dims, bs_page_ma
         }
         const int32_t *from = map.page_table + (static_cast<size_t>(s) * dims.n_kv_heads + h) * MP;
         const int32_t *to = map.page_table + (static_cast<size_t>(d) * dims.n_kv_heads + h) * MP;
+#pragma unroll 4
         for (int j = threadIdx.x; j < MP; j += kPgThreads)
           if (to[j] >= 0) err = BS_ERR_INVALID_ARG;
         const int T = map.seq_lens[s];
@@ -313,9 +345,14 @@ __global__ void __launch_bounds__(kPgThreads) fork_scan(bs_dims dims, bs_page_ma
         } else if (np > MP) {
           err = max(err, static_cast<int>(BS_ERR_CAPACITY));
         } else {
-          for (int j = threadIdx.x; j < np; j += kPgThreads) {
-            const int p = from[j];
-            if (p >= 0 && (p >= dims.n_pages || map.ref_count[p] <= 0)) err = max(err, static_cast<int>(BS_ERR_DEVICE_BOUNDS));
+          for (int j0 = threadIdx.x; j0 < np; j0 += kPgThreads * kBatch) {
+            int p[kBatch];
+#pragma unroll
+            for (int e = 0; e < kBatch; ++e) p[e] = j0 + e * kPgThreads < np ? from[j0 + e * kPgThreads] : -1;
+#pragma unroll
+            for (int e = 0; e < kBatch; ++e)
+              if (p[e] >= 0 && (p[e] >= dims.n_pages || map.ref_count[p[e]] <= 0))
+                err = max(err, static_cast<int>(BS_ERR_DEVICE_BOUNDS));
           }
           if (T % kPage != 0 && from[T / kPage] >= 0) need = 1;
         }
@@ -332,6 +369,7 @@ __global__ void __launch_bounds__(kPgThreads) fork_scan(bs_dims dims, bs_page_ma
 __global__ void __launch_bounds__(kPgThreads) fork_apply(bs_dims dims, bs_page_map map, const int32_t *src, const int32_t *dst,
                                                          int n, bs_page_copies copies, PgWs ws, int32_t *st) {
   __shared__ int before[kMaxTiles + 1];
+  pdl_wait();
   const int items = n * dims.n_kv_heads, MP = dims.max_pages_per_unit;
   const int i0 = static_cast<int>(static_cast<int64_t>(items) * blockIdx.x / gridDim.x);
   const int i1 = static_cast<int>(static_cast<int64_t>(items) * (blockIdx.x + 1) / gridDim.x);
@@ -351,6 +389,7 @@ __global__ void __launch_bounds__(kPgThreads) fork_apply(bs_dims dims, bs_page_m
     const int T = map.seq_lens[s], full = T / kPage;
     const int32_t *from = map.page_table + (static_cast<size_t>(s) * dims.n_kv_heads + h) * MP;
     int32_t *to = map.page_table + (static_cast<size_t>(d) * dims.n_kv_heads + h) * MP;
+#pragma unroll 4
     for (int j = threadIdx.x; j < full; j += kPgThreads) {
       const int p = from[j];
       to[j] = p < 0 ? -1 : p;
@@ -387,17 +426,22 @@ __global__ void __launch_bounds__(kPgThreads) free_kernel(bs_dims dims, bs_page_
     for (int j = threadIdx.x; j < i; j += kPgThreads) again |= seqs[j] == s ? 1 : 0;
     if (cta_max(again, tmp)) continue;
     int32_t *row = map.page_table + (static_cast<size_t>(s) * dims.n_kv_heads + h) * dims.max_pages_per_unit;
-    for (int j = threadIdx.x; j < dims.max_pages_per_unit; j += kPgThreads) {
-      const int p = row[j];
-      if (p == -1) continue;
-      row[j] = -1;
-      if (p < 0) continue;
-      if (p >= dims.n_pages) {
-        report(st, BS_ERR_DEVICE_BOUNDS);
-      } else if (atomicSub(map.ref_count + p, 1) <= 0) {
-        atomicAdd(map.ref_count + p, 1);
-        report(st, BS_ERR_DEVICE_BOUNDS);
+    for (int j0 = threadIdx.x; j0 < dims.max_pages_per_unit; j0 += kPgThreads * kBatch) {
+      int p[kBatch], had[kBatch];
+#pragma unroll
+      for (int e = 0; e < kBatch; ++e) p[e] = j0 + e * kPgThreads < dims.max_pages_per_unit ? row[j0 + e * kPgThreads] : -1;
+#pragma unroll
+      for (int e = 0; e < kBatch; ++e) {
+        had[e] = 1;
+        if (p[e] != -1) row[j0 + e * kPgThreads] = -1;
+        if (p[e] >= 0) had[e] = p[e] < dims.n_pages ? atomicSub(map.ref_count + p[e], 1) : -1;
       }
+#pragma unroll
+      for (int e = 0; e < kBatch; ++e)
+        if (had[e] <= 0) {
+          if (p[e] < dims.n_pages) atomicAdd(map.ref_count + p[e], 1);
+          report(st, BS_ERR_DEVICE_BOUNDS);
+        }
     }
     if (h == 0 && threadIdx.x == 0) map.seq_lens[s] = 0;
   }
@@ -407,13 +451,16 @@ __global__ void __launch_bounds__(kPgThreads) free_kernel(bs_dims dims, bs_page_
 // compact
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(kPgThreads) compact_scan(bs_dims dims, bs_page_map map, PgWs ws) {
-  scan_tile(dims, map.ref_count, ws, blockIdx.x);
+  pdl_trigger();
+  scan_tile(dims, map.ref_count, ws, blockIdx.x, true);
 }
 
 // One thread per page: a page in use at or above N moves.
 __global__ void __launch_bounds__(kPgThreads) compact_move(bs_dims dims, bs_page_map map, bs_page_copies copies, int32_t *n_live,
                                                            PgWs ws, int32_t *st) {
   __shared__ int before[kMaxTiles + 1];
+  pdl_trigger();
+  pdl_wait();
   load_tile_ranks(ws, before);
   const int n_pages = static_cast<int>(dims.n_pages);
   const int N = n_pages - before[ws.n_tiles];
@@ -443,6 +490,7 @@ __global__ void __launch_bounds__(kPgThreads) compact_move(bs_dims dims, bs_page
 }
 
 __global__ void __launch_bounds__(kPgThreads) compact_table(bs_dims dims, bs_page_map map, PgWs ws, int32_t *st) {
+  pdl_wait();
   const int N = ws.head[0];
   const bool go = ws.head[1] != 0;
   if (!go) return;
@@ -490,6 +538,12 @@ __global__ void __launch_bounds__(kCopyPageThreads) copy_kernel(bs_dims dims, bs
   }
 }
 
+// Launches the kernel after this call's previous one as its programmatic dependent.
+template <typename K, typename... Args>
+bs_status launch_next(K kernel, int ctas, cudaStream_t cs, Args... args) {
+  return launch_ex(kernel, dim3(ctas), kPgThreads, 0, cs, 0, true, args...) == cudaSuccess ? BS_OK : BS_ERR_CUDA;
+}
+
 bs_status check_map(const bs_dims *dims, const bs_page_map *map, const int32_t *dev_status) {
   bs_status s = check_dims(dims);
   if (s != BS_OK) return s;
@@ -527,10 +581,9 @@ bs_status bs_pages_reserve(const bs_dims *dims, const bs_page_map *map, const in
   const PgWs ws = pg_ws(*dims, workspace);
   const int units = dims->batch * dims->n_kv_heads;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  reserve_scan<<<ws.n_tiles + std::min(units, 8 * kApplyCtas), kPgThreads, 0, cs>>>(*dims, *map, new_lens, ws);
+  reserve_scan<<<ws.n_tiles + std::min(units, kMaxCtas), kPgThreads, 0, cs>>>(*dims, *map, new_lens, ws);
   if (cudaGetLastError() != cudaSuccess) return BS_ERR_CUDA;
-  reserve_apply<<<std::min(units, kApplyCtas), kPgThreads, 0, cs>>>(*dims, *map, new_lens, ws, dev_status);
-  return launch_status();
+  return launch_next(reserve_apply, std::min(units, kMaxCtas), cs, *dims, *map, new_lens, ws, dev_status);
 }
 
 bs_status bs_pages_fork(const bs_dims *dims, const bs_page_map *map, const int32_t *src, const int32_t *dst, int32_t n,
@@ -548,10 +601,9 @@ bs_status bs_pages_fork(const bs_dims *dims, const bs_page_map *map, const int32
   if (s != BS_OK) return s;
   const PgWs ws = pg_ws(*dims, workspace);
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  fork_scan<<<ws.n_tiles + std::min(items, 8 * kApplyCtas), kPgThreads, 0, cs>>>(*dims, *map, src, dst, n, ws);
+  fork_scan<<<ws.n_tiles + std::min(items, kMaxCtas), kPgThreads, 0, cs>>>(*dims, *map, src, dst, n, ws);
   if (cudaGetLastError() != cudaSuccess) return BS_ERR_CUDA;
-  fork_apply<<<std::min(items, kApplyCtas), kPgThreads, 0, cs>>>(*dims, *map, src, dst, n, *copies, ws, dev_status);
-  return launch_status();
+  return launch_next(fork_apply, std::min(items, kMaxCtas), cs, *dims, *map, src, dst, n, *copies, ws, dev_status);
 }
 
 bs_status bs_pages_free(const bs_dims *dims, const bs_page_map *map, const int32_t *seqs, int32_t n,
@@ -560,7 +612,7 @@ bs_status bs_pages_free(const bs_dims *dims, const bs_page_map *map, const int32
   bs_status s = check_map(dims, map, dev_status);
   if (s != BS_OK) return s;
   if (!seqs || n < 1 || n > dims->batch) return BS_ERR_INVALID_ARG;
-  free_kernel<<<std::min(n * dims->n_kv_heads, 8 * kApplyCtas), kPgThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
+  free_kernel<<<std::min(n * dims->n_kv_heads, kMaxCtas), kPgThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
       *dims, *map, seqs, n, dev_status);
   return launch_status();
 }
@@ -580,13 +632,12 @@ bs_status bs_pages_compact(const bs_dims *dims, const bs_page_map *map, const bs
   compact_scan<<<ws.n_tiles, kPgThreads, 0, cs>>>(*dims, *map, ws);
   if (cudaGetLastError() != cudaSuccess) return BS_ERR_CUDA;
   const int64_t ctas = (dims->n_pages + kPgThreads - 1) / kPgThreads;
-  compact_move<<<static_cast<int>(std::min<int64_t>(ctas, 4 * kApplyCtas)), kPgThreads, 0, cs>>>(*dims, *map, *copies, n_live,
-                                                                                                ws, dev_status);
-  if (cudaGetLastError() != cudaSuccess) return BS_ERR_CUDA;
+  s = launch_next(compact_move, static_cast<int>(std::min<int64_t>(ctas, 4 * kApplyCtas)), cs, *dims, *map, *copies, n_live, ws,
+                  dev_status);
+  if (s != BS_OK) return s;
   const int64_t entries = static_cast<int64_t>(dims->batch) * dims->n_kv_heads * dims->max_pages_per_unit;
-  compact_table<<<static_cast<int>(std::min<int64_t>((entries + kPgThreads - 1) / kPgThreads, 4 * kApplyCtas)), kPgThreads, 0,
-                  cs>>>(*dims, *map, ws, dev_status);
-  return launch_status();
+  return launch_next(compact_table, static_cast<int>(std::min<int64_t>((entries + kPgThreads - 1) / kPgThreads, 4 * kApplyCtas)),
+                     cs, *dims, *map, ws, dev_status);
 }
 
 bs_status bs_pages_copy(const bs_dims *dims, const bs_pools *pools, const bs_page_copies *copies, int32_t *dev_status,

@@ -719,6 +719,7 @@ bs_status launch_step_attention(const bs_dims &dims, const bs_kv &kv, const bs_h
   a.expect = words.expect;
   a.st = io.dev_status;
   a.wait_ns = wait_limit_ns();
+  a.min_split = attn_min_split_pages(dims.max_gather_pages_per_unit);
   return launch_attn(a, true, cs);
 }
 
