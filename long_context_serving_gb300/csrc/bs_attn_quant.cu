@@ -43,8 +43,8 @@ constexpr int kMinSplit = 8;
 constexpr float kPShift = 14.0f;     // P enters as 2^(x - m + 14)
 
 // Shared memory: the staged selection entries, then the warps' rings; after the loop the
-// warps' states and the merge's scratch take the rings' place.
-constexpr int kRing = 2;             // pages of K (and of V) in a warp's ring: two pairs
+// warps' states take the rings' place.
+constexpr int kRing = 2;             // pages of K (and of V) in a warp's ring: pairs
 template <int D>
 struct QuantLayout {
   static constexpr int kPageBytes = kPage * D;
@@ -52,10 +52,10 @@ struct QuantLayout {
   static constexpr int kWarpBytes = 2 * kRing * kPageBytes;
   static constexpr int kOffO = kOffRing;                                     // [4][8][D]
   static constexpr int kOffMl = kOffO + kQuantWarps * kMaxG * D * 4;         // m, l: [2][4][8]
-  static constexpr int kOffSum = kOffMl + 2 * kQuantWarps * kMaxG * 4;       // [8][D]
-  static constexpr int kOffScratch = kOffSum + kMaxG * D * 4;                // merge scratch
-  static constexpr int kBytes = kOffRing + kQuantWarps * kWarpBytes;
-  static_assert(kOffScratch + 3 * kMaxG * kAttnMaxSplits * 4 <= kBytes, "the epilogue fits in the rings");
+  static constexpr int kOffSum = kOffMl + 2 * kQuantWarps * kMaxG * 4;       // [8][D], m [8], l [8]
+  static constexpr int kEnd = kOffSum + kMaxG * D * 4 + 2 * kMaxG * 4;
+  static constexpr int kRings = kOffRing + kQuantWarps * kWarpBytes;
+  static constexpr int kBytes = kEnd > kRings ? kEnd : kRings;
 };
 
 // Byte offset of 16-byte chunk `ch` of row `row` of a page in a ring slot.
@@ -272,20 +272,135 @@ __device__ __forceinline__ void split_weights(const float *x, uint32_t (&h)[2], 
   }
 }
 
-// The end of a split for G heads: merge with the unit's other splits, write out and lse.
-template <int D, int G>
-__device__ __noinline__ void quant_finish(const AttnArgs &a, const UnitBlocks &ub, int u, size_t orow0, unsigned char *smem,
-                                          const float *mfin, const float *lfin, int split, int n_part,
-                                          bool in_cluster) {
+// One float4 column of the merge of n states of a head, visited in order, eight in flight at
+// once: load(k, m, l, o) gives state k's maximum (log2 units), sum and unnormalised column.
+// A state with m = -inf has weight 0; a NaN stays one.
+template <class Load>
+__device__ __forceinline__ void merge_column(int n, Load load, float4 &o, float &m, float &l) {
+  constexpr int kFlight = 8;
+  o = make_float4(0.f, 0.f, 0.f, 0.f);
+  m = -INFINITY;
+  l = 0.0f;
+  for (int k0 = 0; k0 < n; k0 += kFlight) {
+    float mk[kFlight], lk[kFlight];
+    float4 v[kFlight];
+#pragma unroll
+    for (int k = 0; k < kFlight; ++k) {
+      mk[k] = -INFINITY;
+      lk[k] = 0.0f;
+      v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (k0 + k < n) load(k0 + k, mk[k], lk[k], v[k]);
+    }
+    float m_new = m;
+#pragma unroll
+    for (int k = 0; k < kFlight; ++k) m_new = fmaxf(m_new, mk[k]);
+    const float base = m_new == -INFINITY ? 0.0f : m_new;
+    const float a = exp2f(m - base);
+    o.x *= a; o.y *= a; o.z *= a; o.w *= a;
+    l *= a;
+#pragma unroll
+    for (int k = 0; k < kFlight; ++k) {
+      const float wt = exp2f(mk[k] - base);
+      o.x = fmaf(v[k].x, wt, o.x);
+      o.y = fmaf(v[k].y, wt, o.y);
+      o.z = fmaf(v[k].z, wt, o.z);
+      o.w = fmaf(v[k].w, wt, o.w);
+      l = fmaf(lk[k], wt, l);
+    }
+    m = m_new;
+  }
+}
+
+// o / l and lse = ln 2 (m + log2 l); a state with l = 0 (nothing attended) gives zeros and -inf.
+__device__ __forceinline__ void write_column(const float4 &o, float m, float l, float *orow, float *lse_h, int dq) {
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  reinterpret_cast<float4 *>(orow)[dq] =
+      l == 0.0f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+  if (dq == 0) *lse_h = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+// The end of a split: the four warps' states (ow [4][8][D], mw and lw [4][8], in shared
+// memory and visible) merged, and merged with the unit's other splits: ns splits take part.
+// One writes its output itself; a cluster's meet in distributed shared memory (each CTA
+// merges a slice of the columns, a second barrier keeps every CTA until its peers have read
+// it); in workspace mode each writes a record, takes an arrival ticket, and the last merges
+// the records in split order.
+template <int D>
+__device__ void finish_quant(const AttnArgs &a, const UnitBlocks &ub, int u, int split, int ns, bool in_cluster, int G,
+                             size_t orow0, unsigned char *smem) {
   using L = QuantLayout<D>;
-  const float *osum = reinterpret_cast<const float *>(smem + L::kOffSum);
+  constexpr int NT = kQuantThreads, W = kQuantWarps, QD = D / 4, REC = attn_record_floats(D);
+  const int tid = threadIdx.x;
+  const float *ow = reinterpret_cast<const float *>(smem + L::kOffO);
+  const float *mw = reinterpret_cast<const float *>(smem + L::kOffMl), *lw = mw + W * kMaxG;
+  float *osum = reinterpret_cast<float *>(smem + L::kOffSum);     // [8][D], then m [8], l [8]
+  float *msum = osum + kMaxG * D, *lsum = msum + kMaxG;
+  float *base = a.records + static_cast<size_t>(u) * kAttnMaxSplits * G * REC;
+  for (int i = tid; i < G * QD; i += NT) {
+    const int h = i / QD, dq = i % QD;
+    float4 o;
+    float m, l;
+    merge_column(W, [&](int k, float &mk, float &lk, float4 &v) {
+      mk = mw[k * kMaxG + h];
+      lk = lw[k * kMaxG + h];
+      v = reinterpret_cast<const float4 *>(ow + (k * kMaxG + h) * D)[dq];
+    }, o, m, l);
+    if (ns == 1) {
+      write_column(o, m, l, a.out + (orow0 + h) * D, a.lse + orow0 + h, dq);
+      continue;
+    }
+    float *row = in_cluster ? osum + h * D : base + (static_cast<size_t>(split) * G + h) * REC;
+    reinterpret_cast<float4 *>(row)[dq] = o;
+    if (dq == 0) {
+      (in_cluster ? msum[h] : row[D]) = m;
+      (in_cluster ? lsum[h] : row[D + 1]) = l;
+    }
+  }
+  if (ns == 1) {
+    if (ub.polled && tid == 0) a.expect[u] = ub.epoch;
+    return;
+  }
   if (in_cluster) {
-    cluster_merge<kQuantThreads, D, G>(orow0, osum, mfin, lfin, a.out, a.lse);
+    cluster_sync_all();
+    const int rank = static_cast<int>(cluster_rank());
+    for (int i = rank + ns * tid; i < G * QD; i += ns * NT) {
+      const int h = i / QD, dq = i % QD;
+      float4 o;
+      float m, l;
+      merge_column(ns, [&](int k, float &mk, float &lk, float4 &v) {
+        mk = ld_peer(peer_addr(msum + h, k));
+        lk = ld_peer(peer_addr(lsum + h, k));
+        v = ld_peer4(peer_addr(osum + h * D + 4 * dq, k));
+      }, o, m, l);
+      write_column(o, m, l, a.out + (orow0 + h) * D, a.lse + orow0 + h, dq);
+    }
+    cluster_sync_all();
     // Every CTA of the cluster has read the unit's words: advance its epoch.
-    if (ub.polled && split == 0 && threadIdx.x == 0) a.expect[u] = ub.epoch;
-  } else {
-    finish_split<kQuantThreads, D, G>(ub, u, orow0, osum, mfin, lfin, a.arrivals, a.records, a.out, a.lse,
-                                      reinterpret_cast<float *>(smem + L::kOffScratch), a.expect, n_part);
+    if (ub.polled && split == 0 && tid == 0) a.expect[u] = ub.epoch;
+    return;
+  }
+  // The CTA barrier orders every thread's record writes before thread 0's release; the last
+  // split acquires.
+  __shared__ int is_last;
+  __syncthreads();
+  if (tid == 0) is_last = atomic_add_acq_rel_gpu(a.arrivals + u, 1) == ns - 1;
+  __syncthreads();
+  if (!is_last) return;
+  for (int i = tid; i < G * QD; i += NT) {
+    const int h = i / QD, dq = i % QD;
+    float4 o;
+    float m, l;
+    merge_column(ns, [&](int k, float &mk, float &lk, float4 &v) {
+      const float *row = base + (static_cast<size_t>(k) * G + h) * REC;
+      mk = __ldcg(row + D);
+      lk = __ldcg(row + D + 1);
+      v = __ldcg(reinterpret_cast<const float4 *>(row) + dq);
+    }, o, m, l);
+    write_column(o, m, l, a.out + (orow0 + h) * D, a.lse + orow0 + h, dq);
+  }
+  if (tid == 0) {
+    a.arrivals[u] = 0;  // ready for the next call
+    if (ub.polled) a.expect[u] = ub.epoch;
   }
 }
 
@@ -312,7 +427,10 @@ __device__ bool attn_split_quant(const AttnArgs &a, unsigned char *smem, bool in
   q_scale *= rsqrtf(static_cast<float>(D)) * kLog2e;
   UnitBlocks ub = load_unit_blocks<NT>(a, u, sel_sm, in_step, in_cluster);
   check_split_bound(ub, n_part, split, st);
-  // Every split taking part stays to the end (see attn_split_mma).
+  // A cluster's splits, and in the fused step those of step_ws_splits, all stay to the end.
+  // The stand-alone call's know the unit's count at once: those past its pages leave.
+  const int ns = in_step || in_cluster ? n_part : max(1, ub.pg.n_split);
+  if (split >= ns) return false;
   const int n_pages = ub.ok ? ub.pg.n_pages : 0;
   const int gp0 = min(split * ub.pg.pps, n_pages);
   const int gp1 = min(gp0 + ub.pg.pps, n_pages);
@@ -437,49 +555,7 @@ __device__ bool attn_split_quant(const AttnArgs &a, unsigned char *smem, bool in
             make_float2(w.o[i][j], w.o[i][2 + j]);
   }
   __syncthreads();
-  __shared__ float mfin[kMaxG], lfin[kMaxG], wfin[W][kMaxG];
-  if (tid < G) {
-    float M = -INFINITY;
-#pragma unroll
-    for (int k = 0; k < W; ++k) M = fmaxf(M, mw[k * kMaxG + tid]);
-    float Ls = 0.0f;
-#pragma unroll
-    for (int k = 0; k < W; ++k) {
-      const float mi = mw[k * kMaxG + tid];
-      const float wt = (mi == -INFINITY) ? 0.0f : exp2f(mi - M);
-      wfin[k][tid] = wt;
-      Ls = fmaf(lw[k * kMaxG + tid], wt, Ls);
-    }
-    mfin[tid] = M;
-    lfin[tid] = Ls;
-  }
-  __syncthreads();
-  float *osum = reinterpret_cast<float *>(smem + L::kOffSum);
-  for (int i = tid; i < G * D / 4; i += NT) {
-    const int h = i / (D / 4), dq = i % (D / 4);
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int k = 0; k < W; ++k) {
-      const float wt = wfin[k][h];
-      const float4 v = reinterpret_cast<const float4 *>(ow + (k * kMaxG + h) * D)[dq];
-      acc.x = fmaf(v.x, wt, acc.x);
-      acc.y = fmaf(v.y, wt, acc.y);
-      acc.z = fmaf(v.z, wt, acc.z);
-      acc.w = fmaf(v.w, wt, acc.w);
-    }
-    reinterpret_cast<float4 *>(osum + h * D)[dq] = acc;
-  }
-  __syncthreads();
-  switch (G) {
-    case 1: quant_finish<D, 1>(a, ub, u, orow0, smem, mfin, lfin, split, n_part, in_cluster); break;
-    case 2: quant_finish<D, 2>(a, ub, u, orow0, smem, mfin, lfin, split, n_part, in_cluster); break;
-    case 3: quant_finish<D, 3>(a, ub, u, orow0, smem, mfin, lfin, split, n_part, in_cluster); break;
-    case 4: quant_finish<D, 4>(a, ub, u, orow0, smem, mfin, lfin, split, n_part, in_cluster); break;
-    case 5: quant_finish<D, 5>(a, ub, u, orow0, smem, mfin, lfin, split, n_part, in_cluster); break;
-    case 6: quant_finish<D, 6>(a, ub, u, orow0, smem, mfin, lfin, split, n_part, in_cluster); break;
-    case 7: quant_finish<D, 7>(a, ub, u, orow0, smem, mfin, lfin, split, n_part, in_cluster); break;
-    default: quant_finish<D, 8>(a, ub, u, orow0, smem, mfin, lfin, split, n_part, in_cluster); break;
-  }
+  finish_quant<D>(a, ub, u, split, ns, in_cluster, G, orow0, smem);
   return true;
 }
 
