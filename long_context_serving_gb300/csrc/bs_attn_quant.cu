@@ -5,12 +5,11 @@
 // With ks, vs the scales of token t's page and K8, V8 its codes:
 //   x_h(t) = ks (q_h . K8[t]) log2(e) / sqrt(d) + bias2,   o_h += vs (2^(x_h(t) - m) V8[t]).
 //
-// A warp takes whole pages, two at a time, out of a ring of its own in shared memory: four
-// pages of K and four of V, filled by 16-byte asynchronous copies (cp.async) and drained
-// without a CTA barrier. While a pair's scores are computed its V and the next pair's K and V
-// are in flight; its K slots are refilled once the scores are done, its V slots once the
-// values are: 12 to 16 KB in flight a warp, 12 warps an SM. (Codes loaded straight into
-// registers instead, the next pair's in flight, left fewer bytes in flight: DESIGN's table.)
+// A warp takes whole pages, two at a time, through two buffers of its own in shared memory,
+// one for a pair's K and one for its V, filled by 16-byte asynchronous copies (cp.async) and
+// drained without a CTA barrier. K of the next pair is in flight from the end of this pair's
+// scores, its V from the end of this pair's values: 4 to 8 KB a warp, eight warps an SM. (Rings
+// of two and three pairs were slower, as were codes loaded straight into registers.)
 // Rows are stored with their 16-byte chunks permuted (swz8), so that the reads below are free
 // of bank conflicts (D = 64: V two-way). Fragment layouts are chosen around 16-byte reads;
 // lane = 4 r + c:
@@ -44,18 +43,20 @@ constexpr float kPShift = 14.0f;     // P enters as 2^(x - m + 14)
 
 // Shared memory: the staged selection entries, then the warps' rings; after the loop the
 // warps' states take the rings' place.
-constexpr int kRing = 2;             // pages of K (and of V) in a warp's ring: pairs
 template <int D>
 struct QuantLayout {
   static constexpr int kPageBytes = kPage * D;
-  static constexpr int kOffRing = kSelPreload * 4;                           // per warp: K [4], V [4]
-  static constexpr int kWarpBytes = 2 * kRing * kPageBytes;
+  static constexpr int kOffRing = kSelPreload * 4;                           // per warp: a pair of K, a pair of V
+  static constexpr int kWarpBytes = 4 * kPageBytes;
   static constexpr int kOffO = kOffRing;                                     // [4][8][D]
   static constexpr int kOffMl = kOffO + kQuantWarps * kMaxG * D * 4;         // m, l: [2][4][8]
-  static constexpr int kOffSum = kOffMl + 2 * kQuantWarps * kMaxG * 4;       // [8][D], m [8], l [8]
-  static constexpr int kEnd = kOffSum + kMaxG * D * 4 + 2 * kMaxG * 4;
+  static constexpr int kEnd = kOffMl + 2 * kQuantWarps * kMaxG * 4;
   static constexpr int kRings = kOffRing + kQuantWarps * kWarpBytes;
-  static constexpr int kBytes = kEnd > kRings ? kEnd : kRings;
+  // What a cluster's other CTAs send while this one may still be in its loop: per column
+  // entry, o (float4) and (m, l).
+  static constexpr int kOffRecvO = kEnd > kRings ? kEnd : kRings;
+  static constexpr int kOffRecvMl = kOffRecvO + kMaxG * D * 4;
+  static constexpr int kBytes = kOffRecvMl + kMaxG * (D / 4) * 8;
 };
 
 // Byte offset of 16-byte chunk `ch` of row `row` of a page in a ring slot.
@@ -101,10 +102,13 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 __device__ __forceinline__ float f16_lo_f(uint32_t w) { return __half2float(__ushort_as_half(w & 0xffffu)); }
 __device__ __forceinline__ float f16_hi_f(uint32_t w) { return __half2float(__ushort_as_half(w >> 16)); }
 
-// What a page's codes mean; valid = 0: the page does not count and nothing of it is read.
+// A page in flight and what its codes mean; no valid tokens: it does not count and nothing
+// of it is read.
 struct PageMeta {
-  int valid;
+  uint32_t page;   // physical page << 5 | valid tokens (pools hold less than 2^27 pages)
   float ks, vs, bias2;
+  __device__ __forceinline__ int valid() const { return static_cast<int>(page & 31u); }
+  __device__ __forceinline__ int phys() const { return static_cast<int>(page >> 5); }
 };
 
 // The query rows of a unit as A fragments in the dimension order of the K loads, times
@@ -210,10 +214,10 @@ __device__ __forceinline__ void page_values(const unsigned char *slot, const Pag
       v[i][0] = x.x; v[i][1] = x.y;
     }
   }
-  if (t.valid < kPage) {
+  if (t.valid() < kPage) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      if (2 * c + (i & 1) + 8 * (i >> 1) >= t.valid) {
+      if (2 * c + (i & 1) + 8 * (i >> 1) >= t.valid()) {
 #pragma unroll
         for (int g = 0; g < D / 32; ++g) v[i][g] = 0u;
       }
@@ -237,6 +241,12 @@ __device__ __forceinline__ void page_values(const unsigned char *slot, const Pag
   }
 }
 
+__device__ __forceinline__ float exp2_ftz(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // Online softmax of this lane's head over the 32 tokens of two pages: x becomes the weights
 // 2^(x - m + 14), the running state is rescaled when the maximum rises.
 template <int D>
@@ -247,7 +257,7 @@ __device__ __forceinline__ void softmax_pair(float (&x)[8], WarpState<D> &w) {
   mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
   if (__any_sync(0xffffffffu, mx > w.m)) {
     const float m_new = fmaxf(w.m, mx);
-    const float alpha = m_new == -INFINITY ? 1.0f : exp2f(w.m - m_new);
+    const float alpha = m_new == -INFINITY ? 1.0f : exp2_ftz(w.m - m_new);
     w.m = m_new;
     w.l *= alpha;
     const float a0 = __shfl_sync(0xffffffffu, alpha, 8 * c), a1 = __shfl_sync(0xffffffffu, alpha, 8 * c + 4);
@@ -261,7 +271,7 @@ __device__ __forceinline__ void softmax_pair(float (&x)[8], WarpState<D> &w) {
   }
   const float base = w.m == -INFINITY ? 0.0f : w.m - kPShift;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = exp2f(x[i] - base);
+  for (int i = 0; i < 8; ++i) x[i] = exp2_ftz(x[i] - base);   // (a weight below 2^-140 of the largest is 0)
   w.l += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
 }
 __device__ __forceinline__ void split_weights(const float *x, uint32_t (&h)[2], uint32_t (&l)[2]) {
@@ -319,12 +329,25 @@ __device__ __forceinline__ void write_column(const float4 &o, float m, float l, 
   if (dq == 0) *lse_h = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
+// The first barrier of a cluster's life, in two halves: arrived at on entry, waited for
+// before the first access to a peer's memory.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void st_peer4(uint32_t a, const float4 &v) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(a), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w) : "memory");
+}
+__device__ __forceinline__ void st_peer2(uint32_t a, float x, float y) {
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(x), "f"(y) : "memory");
+}
+
 // The end of a split: the four warps' states (ow [4][8][D], mw and lw [4][8], in shared
 // memory and visible) merged, and merged with the unit's other splits: ns splits take part.
-// One writes its output itself; a cluster's meet in distributed shared memory (each CTA
-// merges a slice of the columns, a second barrier keeps every CTA until its peers have read
-// it); in workspace mode each writes a record, takes an arrival ticket, and the last merges
-// the records in split order.
+// One writes its output itself. A cluster's CTA r merges the columns r, r + ns, ...: every CTA
+// sends its own to the owner's shared memory (each has started: attn_split_quant) and one
+// cluster barrier later the owner merges what it got, in split order. (Reading the peers'
+// memory instead needs a second barrier, which keeps every CTA until it has been read: 2.3 to
+// 2.6 us from the last CTA's loop to the end, against 1.8 to 2.3.) In workspace mode each writes a record, takes an
+// arrival ticket, and the last merges the records in split order.
 template <int D>
 __device__ void finish_quant(const AttnArgs &a, const UnitBlocks &ub, int u, int split, int ns, bool in_cluster, int G,
                              size_t orow0, unsigned char *smem) {
@@ -333,8 +356,9 @@ __device__ void finish_quant(const AttnArgs &a, const UnitBlocks &ub, int u, int
   const int tid = threadIdx.x;
   const float *ow = reinterpret_cast<const float *>(smem + L::kOffO);
   const float *mw = reinterpret_cast<const float *>(smem + L::kOffMl), *lw = mw + W * kMaxG;
-  float *osum = reinterpret_cast<float *>(smem + L::kOffSum);     // [8][D], then m [8], l [8]
-  float *msum = osum + kMaxG * D, *lsum = msum + kMaxG;
+  float4 *recv_o = reinterpret_cast<float4 *>(smem + L::kOffRecvO);
+  float2 *recv_ml = reinterpret_cast<float2 *>(smem + L::kOffRecvMl);
+  if (in_cluster && ns > 1) cluster_wait();   // every CTA of the cluster has started
   float *base = a.records + static_cast<size_t>(u) * kAttnMaxSplits * G * REC;
   for (int i = tid; i < G * QD; i += NT) {
     const int h = i / QD, dq = i % QD;
@@ -349,11 +373,17 @@ __device__ void finish_quant(const AttnArgs &a, const UnitBlocks &ub, int u, int
       write_column(o, m, l, a.out + (orow0 + h) * D, a.lse + orow0 + h, dq);
       continue;
     }
-    float *row = in_cluster ? osum + h * D : base + (static_cast<size_t>(split) * G + h) * REC;
+    if (in_cluster) {
+      const int owner = i % ns, at = i / ns * ns + split;   // (ns divides G * D / 4)
+      st_peer4(peer_addr(recv_o + at, owner), o);
+      st_peer2(peer_addr(recv_ml + at, owner), m, l);
+      continue;
+    }
+    float *row = base + (static_cast<size_t>(split) * G + h) * REC;
     reinterpret_cast<float4 *>(row)[dq] = o;
     if (dq == 0) {
-      (in_cluster ? msum[h] : row[D]) = m;
-      (in_cluster ? lsum[h] : row[D + 1]) = l;
+      row[D] = m;
+      row[D + 1] = l;
     }
   }
   if (ns == 1) {
@@ -364,17 +394,17 @@ __device__ void finish_quant(const AttnArgs &a, const UnitBlocks &ub, int u, int
     cluster_sync_all();
     const int rank = static_cast<int>(cluster_rank());
     for (int i = rank + ns * tid; i < G * QD; i += ns * NT) {
-      const int h = i / QD, dq = i % QD;
+      const int h = i / QD, dq = i % QD, at = i / ns * ns;
       float4 o;
       float m, l;
       merge_column(ns, [&](int k, float &mk, float &lk, float4 &v) {
-        mk = ld_peer(peer_addr(msum + h, k));
-        lk = ld_peer(peer_addr(lsum + h, k));
-        v = ld_peer4(peer_addr(osum + h * D + 4 * dq, k));
+        const float2 ml = recv_ml[at + k];
+        mk = ml.x;
+        lk = ml.y;
+        v = recv_o[at + k];
       }, o, m, l);
       write_column(o, m, l, a.out + (orow0 + h) * D, a.lse + orow0 + h, dq);
     }
-    cluster_sync_all();
     // Every CTA of the cluster has read the unit's words: advance its epoch.
     if (ub.polled && split == 0 && tid == 0) a.expect[u] = ub.epoch;
     return;
@@ -418,9 +448,10 @@ __device__ bool attn_split_quant(const AttnArgs &a, unsigned char *smem, bool in
   const size_t orow0 = static_cast<size_t>(b) * dims.n_q_heads + static_cast<size_t>(hk) * G;
   int32_t *sel_sm = reinterpret_cast<int32_t *>(smem);
   const int n_part = in_step && !in_cluster ? step_ws_splits(a, u, attn_n_splits(false)) : attn_n_splits(in_cluster);
-  if (split >= n_part) return false;
+  if (split >= n_part) return false;   // (never in a cluster)
+  if (in_cluster && n_part > 1) cluster_arrive();
 
-  prefetch_page_row<NT>(dims, a.kv, a.cfg, a.plist, u, in_step);
+  if (in_step) prefetch_page_row<NT>(dims, a.kv, a.cfg, a.plist, u, in_step);
   uint32_t qh[D / 16][2], ql[D / 16][2];
   float q_scale;
   load_q_f16<D, Q32>(a.q, orow0, G, qh, ql, &q_scale);   // (in flight beside the block list's loads)
@@ -438,53 +469,45 @@ __device__ bool attn_split_quant(const AttnArgs &a, unsigned char *smem, bool in
   const uint8_t *kpool = static_cast<const uint8_t *>(a.kv.k_pool);
   const uint8_t *vpool = static_cast<const uint8_t *>(a.kv.v_pool);
 
-  // This warp's pages: gp0 + warp + W i, i < n_mine; resolved 32 at a time, one per lane. The
-  // copies run up to kRing pages ahead of the arithmetic, so the chunk before is kept too.
-  struct Chunk {
-    int phys, valid;
-    float ks, vs, bias2;
-  };
+  // This warp's pages: gp0 + warp + W i, i < n_mine; resolved 32 at a time, one per lane.
   const int n_mine = gp1 - gp0 > warp ? (gp1 - gp0 - warp + W - 1) / W : 0;
-  int chunk = -1;
-  Chunk now = {0, 0, 0.0f, 0.0f, 0.0f}, before = now;
-  unsigned char *ring = smem + L::kOffRing + warp * L::kWarpBytes;
-  const uint32_t kring = smem_u32(ring), vring = kring + kRing * L::kPageBytes;
-  auto meta = [&](int i) {
-    const bool cur = i / 32 == chunk;
-    const int src = i & 31;
-    PageMeta t;
-    t.valid = i < n_mine ? __shfl_sync(0xffffffffu, cur ? now.valid : before.valid, src) : 0;
-    t.ks = __shfl_sync(0xffffffffu, cur ? now.ks : before.ks, src);
-    t.vs = __shfl_sync(0xffffffffu, cur ? now.vs : before.vs, src);
-    t.bias2 = __shfl_sync(0xffffffffu, cur ? now.bias2 : before.bias2, src);
-    return t;
-  };
-  // Starts the copies of page i's K (or V); one group per pair, empty past the end.
-  auto copy = [&](int i, uint32_t to, const uint8_t *pool) {
-    if (i >= n_mine) return;
-    const bool cur = i / 32 == chunk;
-    const int valid = __shfl_sync(0xffffffffu, cur ? now.valid : before.valid, i & 31);
-    const int phys = __shfl_sync(0xffffffffu, cur ? now.phys : before.phys, i & 31);
-    if (valid > 0) copy_page<D>(to + (i % kRing) * L::kPageBytes, pool, phys);
-  };
-  auto copy_k = [&](int i) {
-    if (i < n_mine && i / 32 != chunk) {   // (i is even: a pair lies in one chunk)
-      before = now;
-      chunk = i / 32;
-      int blk = -1;
-      now.valid = resolve_page(ub, dims, pt, gp0 + warp + W * (chunk * 32 + lane), gp1, &now.phys, a.bias ? &blk : nullptr, st);
-      now.bias2 = block_bias2(a.bias, dims, u, blk, st);
-      if (now.bias2 == -INFINITY) now.valid = 0;   // the block dropped out: nothing of it is read
-      now.ks = now.valid > 0 ? __ldg(a.kv.k_scale + now.phys) : 0.0f;
-      now.vs = now.valid > 0 ? __ldg(a.kv.v_scale + now.phys) : 0.0f;
+  uint32_t ch_page = 0;   // physical page (27 bits) and valid tokens (5 bits)
+  float ch_ks = 0.0f, ch_vs = 0.0f, ch_bias = 0.0f;
+  unsigned char *kring = smem + L::kOffRing + warp * L::kWarpBytes, *vring = kring + 2 * L::kPageBytes;
+  const uint32_t kslot = smem_u32(kring), vslot = smem_u32(vring);
+  const bool biased = a.bias != nullptr;
+  // Pages i, i + 1 (i even: both lie in one chunk of 32).
+  auto meta = [&](int i, PageMeta (&t)[2]) {
+    if (i >= n_mine) {
+      t[0].page = t[1].page = 0u;
+      return;
     }
-    copy(i, kring, kpool);
-    copy(i + 1, kring, kpool);
-    cp_commit();
+    if ((i & 31) == 0) {
+      int phys = -1, blk = -1;
+      int valid = resolve_page(ub, dims, pt, gp0 + warp + W * (i + lane), gp1, &phys, biased ? &blk : nullptr, st);
+      ch_bias = block_bias2(a.bias, dims, u, blk, st);
+      if (ch_bias == -INFINITY) valid = 0;   // the block dropped out: nothing of it is read
+      ch_page = valid > 0 ? static_cast<uint32_t>(phys) << 5 | static_cast<uint32_t>(valid) : 0u;
+      ch_ks = valid > 0 ? __ldg(a.kv.k_scale + phys) : 0.0f;   // (not waited for until the pair is computed)
+      ch_vs = valid > 0 ? __ldg(a.kv.v_scale + phys) : 0.0f;
+    }
+#pragma unroll
+    for (int j = 0; j < 2; ++j) t[j].page = __shfl_sync(0xffffffffu, ch_page, (i & 31) + j);
   };
-  auto copy_v = [&](int i) {
-    copy(i, vring, vpool);
-    copy(i + 1, vring, vpool);
+  // What the pair's codes mean, once it is computed (before the next meta of a chunk's end).
+  auto scales = [&](int i, PageMeta (&t)[2]) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      t[j].ks = __shfl_sync(0xffffffffu, ch_ks, (i & 31) + j);
+      t[j].vs = __shfl_sync(0xffffffffu, ch_vs, (i & 31) + j);
+      t[j].bias2 = biased ? __shfl_sync(0xffffffffu, ch_bias, (i & 31) + j) : 0.0f;
+    }
+  };
+  // One group of copies a pair and pool, empty past the end.
+  auto copy_pair = [&](const PageMeta (&t)[2], uint32_t to, const uint8_t *pool) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      if (t[j].valid() > 0) copy_page<D>(to + j * L::kPageBytes, pool, t[j].phys());
     cp_commit();
   };
 
@@ -493,44 +516,46 @@ __device__ bool attn_split_quant(const AttnArgs &a, unsigned char *smem, bool in
   w.l = 0.0f;
 #pragma unroll
   for (int i = 0; i < D / 16; ++i) w.o[i][0] = w.o[i][1] = w.o[i][2] = w.o[i][3] = 0.0f;
-#pragma unroll
-  for (int i = 0; i < kRing; i += 2) {
-    copy_k(i);
-    copy_v(i);
-  }
+  PageMeta t[2];
+  meta(0, t);
+  copy_pair(t, kslot, kpool);
+  copy_pair(t, vslot, vpool);
   for (int i = 0; i < n_mine; i += 2) {
-    const unsigned char *ks = ring + (i % kRing) * L::kPageBytes, *vs = ks + kRing * L::kPageBytes;
-    const PageMeta t[2] = {meta(i), meta(i + 1)};
-    const bool any = t[0].valid + t[1].valid > 0;   // (none: dropped, or outside the pool)
-    cp_wait<kRing - 1>();            // this pair's K has landed
+    scales(i, t);
+    const bool any = (t[0].page | t[1].page) != 0u;   // (none: dropped, or outside the pool)
+    cp_wait<1>();            // this pair's K has landed
     __syncwarp();
     float x[8];
     if (any) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) page_scores<D, I8, Q32>(ks + j * L::kPageBytes, t[j], qh, ql, q_scale, x + 4 * j);
+      for (int j = 0; j < 2; ++j) page_scores<D, I8, Q32>(kring + j * L::kPageBytes, t[j], qh, ql, q_scale, x + 4 * j);
     }
     __syncwarp();
-    copy_k(i + kRing);
-    cp_wait<kRing - 1>();            // its V too
+    PageMeta next[2];
+    meta(i + 2, next);
+    copy_pair(next, kslot, kpool);
+    cp_wait<1>();            // its V too
     __syncwarp();
     if (any) {
 #pragma unroll
       for (int j = 0; j < 2; ++j)
-        if (t[j].valid < kPage) {
+        if (t[j].valid() < kPage) {
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            if (2 * (lane & 3) + (k & 1) + 8 * (k >> 1) >= t[j].valid) x[4 * j + k] = -INFINITY;
+            if (2 * (lane & 3) + (k & 1) + 8 * (k >> 1) >= t[j].valid()) x[4 * j + k] = -INFINITY;
         }
       softmax_pair<D>(x, w);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         uint32_t h[2], l[2];
         split_weights(x + 4 * j, h, l);
-        page_values<D, I8>(vs + j * L::kPageBytes, t[j], h, l, w);
+        page_values<D, I8>(vring + j * L::kPageBytes, t[j], h, l, w);
       }
     }
     __syncwarp();
-    copy_v(i + kRing);
+    copy_pair(next, vslot, vpool);
+    t[0] = next[0];
+    t[1] = next[1];
   }
   cp_wait<0>();
   __syncthreads();           // the rings' place is taken by the states below
