@@ -39,6 +39,7 @@ constexpr int kQuantThreads = 128;   // 4 warps
 constexpr int kQuantWarps = kQuantThreads / 32;
 constexpr int kCtasPerSm = 2;
 constexpr int kMinSplit = 8;
+constexpr int kStepSplit = 40;
 constexpr float kPShift = 14.0f;     // P enters as 2^(x - m + 14)
 
 // Shared memory: the staged selection entries, then the warps' rings; after the loop the
@@ -111,28 +112,41 @@ struct PageMeta {
   __device__ __forceinline__ int phys() const { return static_cast<int>(page >> 5); }
 };
 
-// The query rows of a unit as A fragments in the dimension order of the K loads, times
-// 2^e with the row's largest element near 2^14; *unscale gets 2^-e (head r of this lane).
+// A lane's part of the query rows of a unit: row lane / 4 (zeros past the last head), the
+// dimensions of its K chunks. Loaded first, converted once the block list is known, so that
+// the loads are in flight beside the list's.
 template <int D, bool Q32>
-__device__ __forceinline__ void load_q_f16(const void *q, size_t orow0, int G, uint32_t (&hi)[D / 16][2],
-                                           uint32_t (&lo)[D / 16][2], float *unscale) {
-  const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+struct RawQ {
+  static constexpr int kVecs = D / (Q32 ? 16 : 32);
+  uint4 v[kVecs];
+  __device__ __forceinline__ void load(const void *q, size_t orow0, int G) {
+    const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+    const char *src = static_cast<const char *>(q) + ((orow0 + r) * D + (D / 4) * c) * (Q32 ? 4 : 2);
+#pragma unroll
+    for (int i = 0; i < kVecs; ++i) v[i] = r < G ? ldg_stream16(src + 16 * i) : make_uint4(0u, 0u, 0u, 0u);
+  }
+  // Dimensions 4 s .. 4 s + 3 of the part.
+  __device__ __forceinline__ void four(int s, float (&x)[4]) const {
+    if constexpr (Q32) {
+      x[0] = __uint_as_float(v[s].x); x[1] = __uint_as_float(v[s].y);
+      x[2] = __uint_as_float(v[s].z); x[3] = __uint_as_float(v[s].w);
+    } else {
+      const uint32_t a = s & 1 ? v[s / 2].z : v[s / 2].x, b = s & 1 ? v[s / 2].w : v[s / 2].y;
+      x[0] = bf16lo(a); x[1] = bf16hi(a); x[2] = bf16lo(b); x[3] = bf16hi(b);
+    }
+  }
+};
+
+// The query rows as A fragments in the dimension order of the K reads, times 2^e with the
+// row's largest element near 2^14; *unscale gets 2^-e (head lane / 4).
+template <int D, bool Q32>
+__device__ __forceinline__ void q_to_f16(const RawQ<D, Q32> &raw, uint32_t (&hi)[D / 16][2], uint32_t (&lo)[D / 16][2],
+                                         float *unscale) {
   float x[D / 16][4];
   float big = 0.0f;
 #pragma unroll
   for (int s = 0; s < D / 16; ++s) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[s][i] = 0.0f;
-    if (r < G) {
-      const size_t at = (orow0 + r) * D + 16 * (D == 128 ? 2 * c + s / 4 : c) + 4 * (s % 4);
-      if constexpr (Q32) {
-        const float4 w = *reinterpret_cast<const float4 *>(static_cast<const float *>(q) + at);
-        x[s][0] = w.x; x[s][1] = w.y; x[s][2] = w.z; x[s][3] = w.w;
-      } else {
-        const uint2 w = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(q) + at);
-        x[s][0] = bf16lo(w.x); x[s][1] = bf16hi(w.x); x[s][2] = bf16lo(w.y); x[s][3] = bf16hi(w.y);
-      }
-    }
+    raw.four(s, x[s]);
 #pragma unroll
     for (int i = 0; i < 4; ++i) big = fmaxf(big, fabsf(x[s][i]));
   }
@@ -434,6 +448,44 @@ __device__ void finish_quant(const AttnArgs &a, const UnitBlocks &ub, int u, int
   }
 }
 
+// Page gp of the split as resolve_page gives it, with the block's logit in log2 units; its
+// load flies beside the page's. 0 tokens for a page that does not count: past the end,
+// outside the pool or the rows (reported), or of a block that dropped out (logit -inf).
+__device__ __forceinline__ int resolve_quant_page(const UnitBlocks &ub, const AttnArgs &a, const int32_t *pt, int u, int gp,
+                                                  int gp1, int *phys, float *bias2) {
+  *phys = -1;
+  *bias2 = 0.0f;
+  if (gp >= gp1) return 0;
+  const bs_dims &dims = a.dims;
+  const int ppb = ub.pg.ppb, i = gp / ppb;
+  int blk = 0, valid;
+  bool ok = true;
+  const int32_t *where;
+  if (ub.plist) {   // resolved by the selection; all full but the unit's last, which holds token T - 1
+    where = ub.plist + gp;
+    valid = gp == ub.pg.n_pages - 1 ? (ub.T - 1) % kPage + 1 : kPage;
+    if (a.bias) blk = __ldcg(ub.sel + i);
+  } else {
+    blk = ub.block(i);
+    const int64_t lp = static_cast<int64_t>(blk) * ppb + (gp - i * ppb);
+    ok = blk >= 0 && lp < dims.max_pages_per_unit && lp * kPage < ub.T;
+    where = pt + (ok ? lp : 0);
+    valid = static_cast<int>(min(static_cast<int64_t>(kPage), ub.T - lp * kPage));
+  }
+  const bool logit = a.bias != nullptr;
+  ok = ok && (!logit || (blk >= 0 && blk < dims.max_blocks_per_unit));
+  const int p = __ldcg(where);
+  const float e = logit ? __ldg(a.bias + static_cast<size_t>(u) * dims.max_blocks_per_unit + (ok ? blk : 0)) : 0.0f;
+  if (!ok || p < 0 || p >= dims.n_pages) {
+    report(a.st, BS_ERR_DEVICE_BOUNDS);
+    return 0;
+  }
+  *bias2 = e * kLog2e;
+  if (e == -INFINITY) return 0;   // (nothing of it is read)
+  *phys = p;
+  return valid;
+}
+
 // Returns false for a split that took no part (it left at once; see step_ws_splits).
 template <int D, bool I8, bool Q32>
 __device__ bool attn_split_quant(const AttnArgs &a, unsigned char *smem, bool in_step, bool in_cluster) {
@@ -452,10 +504,8 @@ __device__ bool attn_split_quant(const AttnArgs &a, unsigned char *smem, bool in
   if (in_cluster && n_part > 1) cluster_arrive();
 
   if (in_step) prefetch_page_row<NT>(dims, a.kv, a.cfg, a.plist, u, in_step);
-  uint32_t qh[D / 16][2], ql[D / 16][2];
-  float q_scale;
-  load_q_f16<D, Q32>(a.q, orow0, G, qh, ql, &q_scale);   // (in flight beside the block list's loads)
-  q_scale *= rsqrtf(static_cast<float>(D)) * kLog2e;
+  RawQ<D, Q32> raw_q;
+  raw_q.load(a.q, orow0, G);
   UnitBlocks ub = load_unit_blocks<NT>(a, u, sel_sm, in_step, in_cluster);
   check_split_bound(ub, n_part, split, st);
   // A cluster's splits, and in the fused step those of step_ws_splits, all stay to the end.
@@ -483,10 +533,8 @@ __device__ bool attn_split_quant(const AttnArgs &a, unsigned char *smem, bool in
       return;
     }
     if ((i & 31) == 0) {
-      int phys = -1, blk = -1;
-      int valid = resolve_page(ub, dims, pt, gp0 + warp + W * (i + lane), gp1, &phys, biased ? &blk : nullptr, st);
-      ch_bias = block_bias2(a.bias, dims, u, blk, st);
-      if (ch_bias == -INFINITY) valid = 0;   // the block dropped out: nothing of it is read
+      int phys;
+      const int valid = resolve_quant_page(ub, a, pt, u, gp0 + warp + W * (i + lane), gp1, &phys, &ch_bias);
       ch_page = valid > 0 ? static_cast<uint32_t>(phys) << 5 | static_cast<uint32_t>(valid) : 0u;
       ch_ks = valid > 0 ? __ldg(a.kv.k_scale + phys) : 0.0f;   // (not waited for until the pair is computed)
       ch_vs = valid > 0 ? __ldg(a.kv.v_scale + phys) : 0.0f;
@@ -520,6 +568,10 @@ __device__ bool attn_split_quant(const AttnArgs &a, unsigned char *smem, bool in
   meta(0, t);
   copy_pair(t, kslot, kpool);
   copy_pair(t, vslot, vpool);
+  uint32_t qh[D / 16][2], ql[D / 16][2];
+  float q_scale;
+  q_to_f16<D, Q32>(raw_q, qh, ql, &q_scale);
+  q_scale *= rsqrtf(static_cast<float>(D)) * kLog2e;
   for (int i = 0; i < n_mine; i += 2) {
     scales(i, t);
     const bool any = (t[0].page | t[1].page) != 0u;   // (none: dropped, or outside the pool)
@@ -598,10 +650,15 @@ template <int D, bool I8, bool Q32>
 bs_status launch_quant(AttnArgs a, bool step, cudaStream_t cs) {
   const int units = a.dims.batch * a.dims.n_kv_heads;
   const int mg = a.dims.max_gather_pages_per_unit;
+  // Pages per split in workspace mode. The stand-alone call's units start together: as many
+  // as fill one wave if every unit takes its largest selection. In the fused step units start
+  // as they are published, and 36 to 48 pages a split were best (a layer step of the 128K
+  // batch: 69 to 70 us; 77 at 16 pages, 75 at 24, 73 at 32, 72 at 56, 76 by the rule above).
   if (mg <= kClusterMaxPages) {
     const int slots = attn_target_ctas() / 2 * kCtasPerSm;
     const int64_t even = (static_cast<int64_t>(units) * mg + slots - 1) / slots;
-    a.min_split = static_cast<int>(std::max<int64_t>(kMinSplit, (even + kQuantWarps - 1) / kQuantWarps * kQuantWarps));
+    a.min_split = step ? kStepSplit
+                       : static_cast<int>(std::max<int64_t>(kMinSplit, (even + kQuantWarps - 1) / kQuantWarps * kQuantWarps));
   }
   constexpr int smem = QuantLayout<D>::kBytes;
   auto kernel = attn_quant_kernel<D, I8, Q32>;

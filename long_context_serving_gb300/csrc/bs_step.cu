@@ -247,22 +247,24 @@ __device__ __forceinline__ void unit_error_publish(const bs_dims &dims, const bs
   }
 }
 
-// a1 for unit u: the sub-block holding token T-1; in an 8-bit cache every sub-block with a
-// token of that token's page, whose codes the append may have rounded again (one warp: call
-// with the 32 lanes of one warp only).
+// a1 for unit u: the sub-block holding token T-1 (the first warp); in an 8-bit cache every
+// sub-block with a token of that token's page, whose codes the append may have rounded again
+// (a warp each). Called by all threads of the CTA.
 template <int D>
 __device__ __forceinline__ void unit_summary_update(const bs_dims &dims, const bs_kv &kv, const bs_step_io &io,
                                                     int u, int s, int T, int64_t sum_off, int32_t *st) {
   const int j = (T - 1) / s;
   const int32_t *pt = kv.page_table + static_cast<size_t>(u) * dims.max_pages_per_unit;
   float *row = io.summaries + sum_off + static_cast<int64_t>(j) * D;
+  const int warp = threadIdx.x >> 5;
   if (is_quant(dims.kv_dtype)) {
-    for (int i = ((T - 1) & ~(kPage - 1)) / s; i <= j; ++i)
+    for (int i = ((T - 1) & ~(kPage - 1)) / s + warp; i <= j; i += blockDim.x >> 5)
       if (!summary_update_warp_quant<D>(dims, kv, pt, s, T, i, io.summaries + sum_off + static_cast<int64_t>(i) * D) &&
           (threadIdx.x & 31) == 0)
         report(st, BS_ERR_DEVICE_BOUNDS);
     return;
   }
+  if (warp > 0) return;
   const bool ok = dims.kv_dtype == BS_BF16
                       ? summary_update_warp<D, uint16_t>(static_cast<const uint16_t *>(kv.k_pool), pt, dims.n_pages,
                                                          s, T, j, row)
@@ -387,7 +389,7 @@ __global__ void __launch_bounds__(kFrontThreads, 2) step_front_kernel(bs_dims di
   if (!drain()) return;
   if (cj >= n_ctas) return;
   // ---- a1: the sub-block holding the appended token (first CTA, beside the others) --
-  if (cj == 0 && tid < 32) unit_summary_update<D>(dims, kv, io, u, s, T, off, st);
+  if (cj == 0) unit_summary_update<D>(dims, kv, io, u, s, T, off, st);
   if (n_ctas > 1) {
     __syncthreads();
     if (tid == 0) is_last = (ticket_acq_rel(arrivals + u) == n_ctas - 1);
@@ -600,7 +602,7 @@ __global__ void __launch_bounds__(kStepSelThreads) step_select_kernel(bs_dims di
   // a1 by warp 0 while the others wait for the scores: the sub-block holding the
   // appended token lies in the always-forced tail block, which no score of this step
   // reads, and its K pages were written before the score kernel started.
-  if (f.code == BS_OK && threadIdx.x < 32) unit_summary_update<D>(dims, kv, io, u, f.s, f.T, f.off, io.dev_status);
+  if (f.code == BS_OK) unit_summary_update<D>(dims, kv, io, u, f.s, f.T, f.off, io.dev_status);
   if (f.code != BS_OK || f.cls != BS_STREAMING) pdl_wait_front();
   if (f.code != BS_OK) {
     unit_error_publish(dims, io, words, u, f.code);

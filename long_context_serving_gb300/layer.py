@@ -107,6 +107,8 @@ class PagedLayer:
         self._K = _kv_tensor(wl.K, wl.dtype, dev)          # logical [U][T_cap][d], source of appends
         self._V = _kv_tensor(wl.V, wl.dtype, dev)
         upto = np.full(wl.B, T_cap, np.int64) if preload_all else wl.T_prefill.astype(np.int64)
+        if preload_all and kv8:       # (a shorter sequence has no pages past its last step)
+            upto = np.minimum(upto, T_last.astype(np.int64))
         self._write_tokens(np.zeros(wl.B, np.int64), upto)
 
         self.q = _kv_tensor(wl.q, wl.dtype, dev)           # [steps][B][Hq][d]
