@@ -181,6 +181,8 @@ def _check(call: str, status: int) -> None:
 
 
 def _ptr(t) -> int | None:
+    if type(t) is torch.Tensor:
+        return t.data_ptr()
     if t is None:
         return None
     if isinstance(t, int):
@@ -192,7 +194,7 @@ def _ptr(t) -> int | None:
 
 def _stream(stream) -> int | None:
     if stream is None:   # the handle alone: a Stream object takes longer than a call's launches
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 

@@ -296,12 +296,11 @@ __device__ __forceinline__ void split_weights(const float *x, uint32_t (&h)[2], 
   }
 }
 
-// One float4 column of the merge of n states of a head, visited in order, eight in flight at
-// once: load(k, m, l, o) gives state k's maximum (log2 units), sum and unnormalised column.
+// One float4 column of the merge of n states of a head, visited in order, kFlight of them in
+// flight at once: load(k, m, l, o) gives state k's maximum (log2 units), sum and unnormalised column.
 // A state with m = -inf has weight 0; a NaN stays one.
-template <class Load>
+template <int kFlight, class Load>
 __device__ __forceinline__ void merge_column(int n, Load load, float4 &o, float &m, float &l) {
-  constexpr int kFlight = 8;
   o = make_float4(0.f, 0.f, 0.f, 0.f);
   m = -INFINITY;
   l = 0.0f;
@@ -378,7 +377,7 @@ __device__ void finish_quant(const AttnArgs &a, const UnitBlocks &ub, int u, int
     const int h = i / QD, dq = i % QD;
     float4 o;
     float m, l;
-    merge_column(W, [&](int k, float &mk, float &lk, float4 &v) {
+    merge_column<W>(W, [&](int k, float &mk, float &lk, float4 &v) {
       mk = mw[k * kMaxG + h];
       lk = lw[k * kMaxG + h];
       v = reinterpret_cast<const float4 *>(ow + (k * kMaxG + h) * D)[dq];
@@ -411,7 +410,7 @@ __device__ void finish_quant(const AttnArgs &a, const UnitBlocks &ub, int u, int
       const int h = i / QD, dq = i % QD, at = i / ns * ns;
       float4 o;
       float m, l;
-      merge_column(ns, [&](int k, float &mk, float &lk, float4 &v) {
+      merge_column<8>(ns, [&](int k, float &mk, float &lk, float4 &v) {
         const float2 ml = recv_ml[at + k];
         mk = ml.x;
         lk = ml.y;
@@ -434,7 +433,7 @@ __device__ void finish_quant(const AttnArgs &a, const UnitBlocks &ub, int u, int
     const int h = i / QD, dq = i % QD;
     float4 o;
     float m, l;
-    merge_column(ns, [&](int k, float &mk, float &lk, float4 &v) {
+    merge_column<16>(ns, [&](int k, float &mk, float &lk, float4 &v) {
       const float *row = base + (static_cast<size_t>(k) * G + h) * REC;
       mk = __ldcg(row + D);
       lk = __ldcg(row + D + 1);
