@@ -31,6 +31,7 @@ constexpr int kMinTilePages = 4096;
 constexpr int kApplyCtas = 304;     // two CTAs per SM
 constexpr int kMaxCtas = 8 * kApplyCtas;   // one wave; each takes a contiguous share beyond
 constexpr int kBatch = 4;           // row entries a thread has in flight at once
+constexpr int kFreeBatch = 8;       // the same in free
 
 __host__ __device__ inline int64_t tile_pages_for(int64_t n_pages) {
   int64_t t = kMinTilePages;
@@ -173,29 +174,6 @@ __device__ void scan_tile(const bs_dims &dims, const int32_t *ref, const PgWs &w
 }
 static_assert(kMinTilePages / 32 <= kPgThreads, "one word a thread");
 
-// Free pages before each tile, [n_tiles + 1], into shared memory. All threads.
-__device__ __forceinline__ void load_tile_ranks(const PgWs &ws, int *before) {
-  __shared__ int tmp[kPgWarps];
-  constexpr int kPer = kMaxTiles / kPgThreads;
-  int v[kPer], sum = 0;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int t = threadIdx.x * kPer + i;
-    v[i] = t < ws.n_tiles ? ws.tile_free[t] : 0;
-    sum += v[i];
-  }
-  int total;
-  int run = cta_scan(sum, tmp, &total);
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int t = threadIdx.x * kPer + i;
-    if (t <= ws.n_tiles) before[t] = run;
-    run += v[i];
-  }
-  if (threadIdx.x == 0) before[ws.n_tiles] = total;
-  __syncthreads();
-}
-
 // Free pages below page p (0 <= p < n_pages).
 __device__ __forceinline__ int free_rank(const PgWs &ws, const int *before, int64_t p) {
   const int64_t w = p >> 5;
@@ -212,27 +190,70 @@ __device__ __forceinline__ int kth_free(const PgWs &ws, const int *before, int k
   return ws.list[lo * ws.tile_pages + (k - before[lo])];
 }
 
-// What the units before `first` ask for, what all ask for, and the worst error of any
-// (0: none). All threads.
+// What the scan found: free pages before each tile, [n_tiles + 1], into shared memory; what
+// the requesters before `first` ask for, what all n ask for, and the worst error of any (0:
+// none). All threads.
 struct Requests {
   long long before, total;
   int err;
 };
-__device__ __forceinline__ Requests sum_requests(const PgWs &ws, int n, int first) {
-  __shared__ long long tmp[kPgWarps];
-  __shared__ int tmp_i[kPgWarps];
+__device__ __forceinline__ Requests load_plan(const PgWs &ws, int n, int first, int *before) {
+  __shared__ int w_free[kPgWarps], w_err[kPgWarps];
+  __shared__ long long w_pre[kPgWarps], w_all[kPgWarps];
+  constexpr int kPer = kMaxTiles / kPgThreads;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int v[kPer], sum = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int t = threadIdx.x * kPer + i;
+    v[i] = t < ws.n_tiles ? ws.tile_free[t] : 0;
+    sum += v[i];
+  }
   long long pre = 0, all = 0;
   int err = 0;
   for (int i = threadIdx.x; i < n; i += kPgThreads) {
-    const int v = ws.need[i];
-    all += v;
-    if (i < first) pre += v;
+    const int k = ws.need[i];
     err = max(err, ws.err[i]);
+    all += k;
+    if (i < first) pre += k;
   }
-  Requests r;
-  r.before = cta_sum(pre, tmp);
-  r.total = cta_sum(all, tmp);
-  r.err = cta_max(err, tmp_i);
+  int x = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    pre += __shfl_xor_sync(0xffffffffu, pre, o);
+    all += __shfl_xor_sync(0xffffffffu, all, o);
+  }
+  err = __reduce_max_sync(0xffffffffu, err);
+  if (lane == 31) {
+    w_free[warp] = x;
+    w_pre[warp] = pre;
+    w_all[warp] = all;
+    w_err[warp] = err;
+  }
+  __syncthreads();
+  Requests r = {0, 0, 0};
+  int run = x - sum, total = 0;
+#pragma unroll
+  for (int w = 0; w < kPgWarps; ++w) {
+    if (w < warp) run += w_free[w];
+    total += w_free[w];
+    r.before += w_pre[w];
+    r.total += w_all[w];
+    r.err = max(r.err, w_err[w]);
+  }
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int t = threadIdx.x * kPer + i;
+    if (t < ws.n_tiles) before[t] = run;
+    run += v[i];
+  }
+  if (threadIdx.x == 0) before[ws.n_tiles] = total;
+  __syncthreads();
   return r;
 }
 
@@ -272,8 +293,7 @@ __global__ void __launch_bounds__(kPgThreads) reserve_apply(bs_dims dims, bs_pag
   // A contiguous share of the units per CTA.
   const int u0 = static_cast<int>(static_cast<int64_t>(units) * blockIdx.x / gridDim.x);
   const int u1 = static_cast<int>(static_cast<int64_t>(units) * (blockIdx.x + 1) / gridDim.x);
-  const Requests rq = sum_requests(ws, units, u0);
-  load_tile_ranks(ws, before);
+  const Requests rq = load_plan(ws, units, u0, before);
   if (rq.err != BS_OK || rq.total > before[ws.n_tiles]) {
     if (blockIdx.x == 0 && threadIdx.x == 0) report(st, rq.err != BS_OK ? rq.err : BS_ERR_CAPACITY);
     return;
@@ -374,8 +394,7 @@ __global__ void __launch_bounds__(kPgThreads) fork_apply(bs_dims dims, bs_page_m
   const int items = n * dims.n_kv_heads, MP = dims.max_pages_per_unit;
   const int i0 = static_cast<int>(static_cast<int64_t>(items) * blockIdx.x / gridDim.x);
   const int i1 = static_cast<int>(static_cast<int64_t>(items) * (blockIdx.x + 1) / gridDim.x);
-  const Requests rq = sum_requests(ws, items, i0);
-  load_tile_ranks(ws, before);
+  const Requests rq = load_plan(ws, items, i0, before);
   const bool bad = rq.err != BS_OK || rq.total > before[ws.n_tiles];
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     *copies.count = bad ? 0 : static_cast<int>(rq.total);
@@ -425,20 +444,29 @@ __global__ void __launch_bounds__(kPgThreads) free_kernel(bs_dims dims, bs_page_
     }
     int again = 0;   // named before: done there
     for (int j = threadIdx.x; j < i; j += kPgThreads) again |= seqs[j] == s ? 1 : 0;
+    const int MP = dims.max_pages_per_unit;
+    int32_t *row = map.page_table + (static_cast<size_t>(s) * dims.n_kv_heads + h) * MP;
+    int p[kFreeBatch];   // (the first entries are loaded beside the check)
+#pragma unroll
+    for (int e = 0; e < kFreeBatch; ++e) {
+      const int j = threadIdx.x + e * kPgThreads;
+      p[e] = j < MP ? row[j] : -1;
+    }
     if (cta_max(again, tmp)) continue;
-    int32_t *row = map.page_table + (static_cast<size_t>(s) * dims.n_kv_heads + h) * dims.max_pages_per_unit;
-    for (int j0 = threadIdx.x; j0 < dims.max_pages_per_unit; j0 += kPgThreads * kBatch) {
-      int p[kBatch], had[kBatch];
+    for (int j0 = threadIdx.x; j0 < MP; j0 += kPgThreads * kFreeBatch) {
+      int had[kFreeBatch];
+      if (j0 >= kPgThreads * kFreeBatch) {
 #pragma unroll
-      for (int e = 0; e < kBatch; ++e) p[e] = j0 + e * kPgThreads < dims.max_pages_per_unit ? row[j0 + e * kPgThreads] : -1;
+        for (int e = 0; e < kFreeBatch; ++e) p[e] = j0 + e * kPgThreads < MP ? row[j0 + e * kPgThreads] : -1;
+      }
 #pragma unroll
-      for (int e = 0; e < kBatch; ++e) {
+      for (int e = 0; e < kFreeBatch; ++e) {
         had[e] = 1;
         if (p[e] != -1) row[j0 + e * kPgThreads] = -1;
         if (p[e] >= 0) had[e] = p[e] < dims.n_pages ? atomicSub(map.ref_count + p[e], 1) : -1;
       }
 #pragma unroll
-      for (int e = 0; e < kBatch; ++e)
+      for (int e = 0; e < kFreeBatch; ++e)
         if (had[e] <= 0) {
           if (p[e] < dims.n_pages) atomicAdd(map.ref_count + p[e], 1);
           report(st, BS_ERR_DEVICE_BOUNDS);
@@ -462,7 +490,7 @@ __global__ void __launch_bounds__(kPgThreads) compact_move(bs_dims dims, bs_page
   __shared__ int before[kMaxTiles + 1];
   pdl_trigger();
   pdl_wait();
-  load_tile_ranks(ws, before);
+  load_plan(ws, 0, 0, before);
   const int n_pages = static_cast<int>(dims.n_pages);
   const int N = n_pages - before[ws.n_tiles];
   // Pages in use below N: N - (free pages below N); the others move.
