@@ -237,6 +237,10 @@ bs_status bs_select_topk(const bs_dims *dims, const bs_head_cfg *cfg, const int3
  * accurate to fp32 (codes are exact in fp16; each query row is scaled by a power of two
  * and, like the probabilities, enters as fp16 parts hi + lo), whatever the scales. A
  * page whose block logit is -inf is not read; NaN codes in tokens past T do not count.
+ * Their splits differ from the above: in cluster mode S is halved while a selection of
+ * max_gather_pages_per_unit would leave a split fewer than 8 pages; in workspace mode up
+ * to 1024 pages, m = max(8, units * max_gather_pages_per_unit / (2 CTAs per SM), up to a
+ * multiple of 4), so that the splits fill one wave, and m = 40 in the fused step.
  * workspace: device scratch of at least bs_workspace_size(dims) bytes, 16-byte
  * aligned. It starts with four int32 words per unit (padded to 16 bytes): the fused
  * step's selection tickets, the attention's arrival tickets, the fused step's published
@@ -541,10 +545,11 @@ bs_status bs_pages_fork(const bs_dims *dims, const bs_page_map *map, const int32
 
 /* The sequences seqs[i], i < n (device int32 [n]), give up their pages: each entry of
  * their rows becomes -1 and its page's count falls by one; their lengths become 0. A
- * negative seqs[i] is skipped, a sequence named twice is freed once. An entry outside
- * the pool, or whose page has count 0, is dropped with BS_ERR_DEVICE_BOUNDS; a seqs[i]
- * >= batch is skipped with BS_ERR_INVALID_ARG; the rest is done. 1 <= n <= batch. One
- * launch. */
+ * negative seqs[i] is skipped, a sequence named twice is freed once. (A decode call that
+ * finds a length of 0 reports BS_ERR_INVALID_ARG for that sequence and does the others.)
+ * An entry outside the pool, or whose page has count 0, is dropped with
+ * BS_ERR_DEVICE_BOUNDS; a seqs[i] >= batch is skipped with BS_ERR_INVALID_ARG; the rest
+ * is done. 1 <= n <= batch. One launch. */
 bs_status bs_pages_free(const bs_dims *dims, const bs_page_map *map, const int32_t *seqs, int32_t n,
                         int32_t *dev_status, bs_stream_t stream);
 

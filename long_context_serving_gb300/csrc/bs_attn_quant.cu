@@ -27,6 +27,7 @@
 // lo, so that weights down to 2^-28 of the largest keep 22 bits; sums are fp32. The V scale is
 // applied to each page's product in fp32, so no scale can leave fp16's range.
 #include <algorithm>
+#include <atomic>
 
 #include "bs_attn_impl.cuh"
 #include "bs_attn_launch.cuh"
@@ -40,7 +41,7 @@ constexpr int kQuantWarps = kQuantThreads / 32;
 constexpr int kCtasPerSm = 2;
 constexpr int kMinSplit = 8;
 constexpr int kStepSplit = 40;
-constexpr float kPShift = 14.0f;     // P enters as 2^(x - m + 14)
+constexpr float kPScale = 16384.0f;  // weights enter the V products times 2^14, the V scales times 2^-14
 
 // Shared memory: the staged selection entries, then the warps' rings; after the loop the
 // warps' states take the rings' place.
@@ -107,7 +108,7 @@ __device__ __forceinline__ float f16_hi_f(uint32_t w) { return __half2float(__us
 // of it is read.
 struct PageMeta {
   uint32_t page;   // physical page << 5 | valid tokens (pools hold less than 2^27 pages)
-  float ks, vs, bias2;
+  float ks, vs, bias2;   // (vs times 2^-14)
   __device__ __forceinline__ int valid() const { return static_cast<int>(page & 31u); }
   __device__ __forceinline__ int phys() const { return static_cast<int>(page >> 5); }
 };
@@ -172,7 +173,7 @@ __device__ __forceinline__ void q_to_f16(const RawQ<D, Q32> &raw, uint32_t (&hi)
 }
 
 // A warp's running state: m and l of head lane / 4 (m in log2 units, replicated over the
-// head's four lanes; l a partial sum of 2^(x - m + 14) per lane), and
+// head's four lanes; l a partial sum of 2^(x - m) per lane), and
 // o[i][2 k + j] = O[head 2 c + j][dim r D/8 + 2 i + k].
 template <int D>
 struct WarpState {
@@ -262,7 +263,7 @@ __device__ __forceinline__ float exp2_ftz(float x) {
 }
 
 // Online softmax of this lane's head over the 32 tokens of two pages: x becomes the weights
-// 2^(x - m + 14), the running state is rescaled when the maximum rises.
+// 2^(x - m), the running state is rescaled when the maximum rises.
 template <int D>
 __device__ __forceinline__ void softmax_pair(float (&x)[8], WarpState<D> &w) {
   const int c = threadIdx.x & 3;
@@ -283,16 +284,17 @@ __device__ __forceinline__ void softmax_pair(float (&x)[8], WarpState<D> &w) {
       w.o[i][3] *= a1;
     }
   }
-  const float base = w.m == -INFINITY ? 0.0f : w.m - kPShift;
+  const float base = w.m == -INFINITY ? 0.0f : w.m;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = exp2_ftz(x[i] - base);   // (a weight below 2^-140 of the largest is 0)
+  for (int i = 0; i < 8; ++i) x[i] = exp2_ftz(x[i] - base);   // (a weight below 2^-126 of the largest is 0)
   w.l += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
 }
 __device__ __forceinline__ void split_weights(const float *x, uint32_t (&h)[2], uint32_t (&l)[2]) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    h[i] = pack_f16(x[2 * i], x[2 * i + 1]);
-    l[i] = pack_f16(x[2 * i] - f16_lo_f(h[i]), x[2 * i + 1] - f16_hi_f(h[i]));
+    const float a = x[2 * i] * kPScale, b = x[2 * i + 1] * kPScale;
+    h[i] = pack_f16(a, b);
+    l[i] = pack_f16(a - f16_lo_f(h[i]), b - f16_hi_f(h[i]));
   }
 }
 
@@ -546,7 +548,7 @@ __device__ bool attn_split_quant(const AttnArgs &a, unsigned char *smem, bool in
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       t[j].ks = __shfl_sync(0xffffffffu, ch_ks, (i & 31) + j);
-      t[j].vs = __shfl_sync(0xffffffffu, ch_vs, (i & 31) + j);
+      t[j].vs = __shfl_sync(0xffffffffu, ch_vs, (i & 31) + j) * (1.0f / kPScale);
       t[j].bias2 = biased ? __shfl_sync(0xffffffffu, ch_bias, (i & 31) + j) : 0.0f;
     }
   };
@@ -620,7 +622,7 @@ __device__ bool attn_split_quant(const AttnArgs &a, unsigned char *smem, bool in
     w.l += __shfl_xor_sync(0xffffffffu, w.l, 1);
     w.l += __shfl_xor_sync(0xffffffffu, w.l, 2);
     if (c == 0) {
-      mw[warp * kMaxG + r] = w.m - kPShift;   // the sums are of 2^(x - (m - 14))
+      mw[warp * kMaxG + r] = w.m;
       lw[warp * kMaxG + r] = w.l;
     }
 #pragma unroll
@@ -661,10 +663,17 @@ bs_status launch_quant(AttnArgs a, bool step, cudaStream_t cs) {
   }
   constexpr int smem = QuantLayout<D>::kBytes;
   auto kernel = attn_quant_kernel<D, I8, Q32>;
-  static const bool attrs_ok =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess &&
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
-  if (!attrs_ok) return BS_ERR_CUDA;
+  // (once per device: an attribute holds for the one that is current)
+  static std::atomic<uint64_t> set_on{0};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return BS_ERR_CUDA;
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+  if ((set_on.load(std::memory_order_relaxed) & bit) == 0) {
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+      return BS_ERR_CUDA;
+    set_on.fetch_or(bit, std::memory_order_relaxed);
+  }
   const bool cluster = attn_mode(units, mg) == kModeCluster;
   int splits = attn_grid_splits(units, mg, attn_target_ctas(), a.min_split);
   // A cluster's merge costs more than a few pages: no more splits than leave each kMinSplit.
