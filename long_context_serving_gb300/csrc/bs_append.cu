@@ -6,6 +6,7 @@
 // reduction gives the largest magnitude, and the codes leave as full rows of 8-byte stores.
 // One pass: each new value is read once, each code written once; bound by HBM for prompts,
 // by latency for single tokens (one chain of lengths -> page index -> old scale).
+#include "bs_attn_launch.cuh"
 #include "bs_quant.cuh"
 
 namespace bsi {
@@ -13,6 +14,9 @@ namespace {
 
 constexpr int kAppendThreads = 128;
 constexpr int kAppendWarps = kAppendThreads / 32;
+
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 struct AppendArgs {
   bs_dims dims;
@@ -124,6 +128,8 @@ __global__ void __launch_bounds__(kAppendThreads, Q32 ? (D == 128 ? 3 : 5) : 8) 
   const bs_dims &dims = a.dims;
   const int u = blockIdx.x, b = u / dims.n_kv_heads, h = u % dims.n_kv_heads;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_wait();      // everything before this call has finished
+  pdl_trigger();
   const int T = a.seq_lens[b], t_begin = a.tok_begin[b];
   const int64_t row0 = a.row_begin[b];
   const bool first_thread = blockIdx.y == 0 && threadIdx.x == 0;
@@ -256,8 +262,10 @@ bs_status launch_append(const AppendArgs &a, int max_new, cudaStream_t cs) {
   const int64_t items = 2 * ((static_cast<int64_t>(max_new) + kPage - 2) / kPage + 1);   // pages that max_new tokens can touch
   const int per_warp = units * items > 8 * 152 * kAppendWarps ? 4 : 1;
   const int64_t gy = (items + kAppendWarps * per_warp - 1) / (kAppendWarps * per_warp);
-  append_kernel<D, I8, Q32><<<dim3(units, static_cast<unsigned>(gy < 65535 ? gy : 65535)), kAppendThreads, 0, cs>>>(a, per_warp);
-  return launch_status();
+  // (a programmatic dependent: its CTAs are in place when the work before it ends)
+  const dim3 grid(units, static_cast<unsigned>(gy < 65535 ? gy : 65535));
+  return launch_ex(append_kernel<D, I8, Q32>, grid, kAppendThreads, 0, cs, 0, true, a, per_warp) == cudaSuccess ? BS_OK
+                                                                                                                : BS_ERR_CUDA;
 }
 
 template <int D>

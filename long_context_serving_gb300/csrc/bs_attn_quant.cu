@@ -640,7 +640,10 @@ __device__ bool attn_split_quant(const AttnArgs &a, unsigned char *smem, bool in
 template <int D, bool I8, bool Q32>
 __global__ void __launch_bounds__(kQuantThreads, kCtasPerSm) attn_quant_kernel(const __grid_constant__ AttnArgs a, bool step, bool cluster) {
   extern __shared__ __align__(16) unsigned char smem[];
-  if (step) pdl_launch_dependents();
+  // The stand-alone call is a programmatic dependent of whatever ran before it: its CTAs are in
+  // place when that ends, and wait for it before they read anything.
+  if (!step) pdl_wait();
+  pdl_launch_dependents();
   const bool took_part = attn_split_quant<D, I8, Q32>(a, smem, step, cluster);
   // In the fused step, finish only after the selection kernel has (a split that took no
   // part leaves at once: split 0 of every unit takes part, so the grid still does).
@@ -681,7 +684,7 @@ bs_status launch_quant(AttnArgs a, bool step, cudaStream_t cs) {
     while (splits > 1 && mg < splits * kMinSplit) splits >>= 1;
   const dim3 grid = cluster ? dim3(splits, units) : dim3(units, splits);   // (workspace mode: unit-major)
   const cudaError_t e =
-      launch_ex(kernel, grid, kQuantThreads, smem, cs, cluster && splits > 1 ? splits : 0, step, a, step, cluster);
+      launch_ex(kernel, grid, kQuantThreads, smem, cs, cluster && splits > 1 ? splits : 0, true, a, step, cluster);
   return e == cudaSuccess ? BS_OK : BS_ERR_CUDA;
 }
 

@@ -6,7 +6,7 @@
 //     pages in ascending order and counts them (and, for compact, keeps their bitmap with each
 //     word's rank); beside it, other CTAs of the same launch count what each unit asks for and
 //     check the arguments;
-//   * the next kernel, a programmatic dependent (it starts up while the scan runs), sums tiles
+//   * the next kernel (its CTAs in place by the time the scan ends) sums tiles
 //     and requests before its own (block scans over at most kMaxTiles and `units` ints) and
 //     gives each request its page: a binary search over the tiles' ranks in shared memory, then
 //     one load from the tile's list. (Binary searches over bitmap words instead, about fifteen
@@ -74,8 +74,12 @@ __host__ inline PgWs pg_ws(const bs_dims &d, void *workspace) {
   return w;
 }
 
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+// Every kernel here is a programmatic dependent of the work before it: its CTAs are in place
+// when that ends, wait for it before they read anything, and only then let the next one's in.
+__device__ __forceinline__ void pdl_enter() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
 
 // Exclusive prefix sum of one int per thread over the CTA; *total gets the sum. All threads.
 __device__ __forceinline__ int cta_scan(int v, int *tmp, int *total) {
@@ -261,7 +265,7 @@ __device__ __forceinline__ Requests load_plan(const PgWs &ws, int n, int first, 
 // reserve
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(kPgThreads) reserve_scan(bs_dims dims, bs_page_map map, const int32_t *new_lens, PgWs ws) {
-  pdl_trigger();
+  pdl_enter();
   if (static_cast<int>(blockIdx.x) < ws.n_tiles) {
     scan_tile(dims, map.ref_count, ws, blockIdx.x, false);
     return;
@@ -289,7 +293,7 @@ __global__ void __launch_bounds__(kPgThreads) reserve_apply(bs_dims dims, bs_pag
   __shared__ int before[kMaxTiles + 1];
   __shared__ int tmp[kPgWarps];
   const int units = dims.batch * dims.n_kv_heads;
-  pdl_wait();
+  pdl_enter();
   // A contiguous share of the units per CTA.
   const int u0 = static_cast<int>(static_cast<int64_t>(units) * blockIdx.x / gridDim.x);
   const int u1 = static_cast<int>(static_cast<int64_t>(units) * (blockIdx.x + 1) / gridDim.x);
@@ -334,7 +338,7 @@ __global__ void __launch_bounds__(kPgThreads) reserve_apply(bs_dims dims, bs_pag
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(kPgThreads) fork_scan(bs_dims dims, bs_page_map map, const int32_t *src, const int32_t *dst,
                                                         int n, PgWs ws) {
-  pdl_trigger();
+  pdl_enter();
   if (static_cast<int>(blockIdx.x) < ws.n_tiles) {
     scan_tile(dims, map.ref_count, ws, blockIdx.x, false);
     return;
@@ -390,7 +394,7 @@ __global__ void __launch_bounds__(kPgThreads) fork_scan(bs_dims dims, bs_page_ma
 __global__ void __launch_bounds__(kPgThreads) fork_apply(bs_dims dims, bs_page_map map, const int32_t *src, const int32_t *dst,
                                                          int n, bs_page_copies copies, PgWs ws, int32_t *st) {
   __shared__ int before[kMaxTiles + 1];
-  pdl_wait();
+  pdl_enter();
   const int items = n * dims.n_kv_heads, MP = dims.max_pages_per_unit;
   const int i0 = static_cast<int>(static_cast<int64_t>(items) * blockIdx.x / gridDim.x);
   const int i1 = static_cast<int>(static_cast<int64_t>(items) * (blockIdx.x + 1) / gridDim.x);
@@ -434,6 +438,7 @@ __global__ void __launch_bounds__(kPgThreads) fork_apply(bs_dims dims, bs_page_m
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(kPgThreads) free_kernel(bs_dims dims, bs_page_map map, const int32_t *seqs, int n, int32_t *st) {
   __shared__ int tmp[kPgWarps];
+  pdl_enter();
   for (int it = blockIdx.x; it < n * dims.n_kv_heads; it += gridDim.x) {
     const int i = it / dims.n_kv_heads, h = it % dims.n_kv_heads;
     const int s = seqs[i];
@@ -480,7 +485,7 @@ __global__ void __launch_bounds__(kPgThreads) free_kernel(bs_dims dims, bs_page_
 // compact
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(kPgThreads) compact_scan(bs_dims dims, bs_page_map map, PgWs ws) {
-  pdl_trigger();
+  pdl_enter();
   scan_tile(dims, map.ref_count, ws, blockIdx.x, true);
 }
 
@@ -488,8 +493,7 @@ __global__ void __launch_bounds__(kPgThreads) compact_scan(bs_dims dims, bs_page
 __global__ void __launch_bounds__(kPgThreads) compact_move(bs_dims dims, bs_page_map map, bs_page_copies copies, int32_t *n_live,
                                                            PgWs ws, int32_t *st) {
   __shared__ int before[kMaxTiles + 1];
-  pdl_trigger();
-  pdl_wait();
+  pdl_enter();
   load_plan(ws, 0, 0, before);
   const int n_pages = static_cast<int>(dims.n_pages);
   const int N = n_pages - before[ws.n_tiles];
@@ -519,7 +523,7 @@ __global__ void __launch_bounds__(kPgThreads) compact_move(bs_dims dims, bs_page
 }
 
 __global__ void __launch_bounds__(kPgThreads) compact_table(bs_dims dims, bs_page_map map, PgWs ws, int32_t *st) {
-  pdl_wait();
+  pdl_enter();
   const int N = ws.head[0];
   const bool go = ws.head[1] != 0;
   if (!go) return;
@@ -543,6 +547,7 @@ constexpr int kCopyPageThreads = 128;
 
 __global__ void __launch_bounds__(kCopyPageThreads) copy_kernel(bs_dims dims, bs_pools pools, bs_page_copies copies, int page_bytes,
                                                                 bool scales, int32_t *st) {
+  pdl_enter();
   const int n = min(max(*copies.count, 0), copies.capacity);
   const int vecs = page_bytes / 16;
   for (int i = blockIdx.x; i < n; i += gridDim.x) {
@@ -567,10 +572,9 @@ __global__ void __launch_bounds__(kCopyPageThreads) copy_kernel(bs_dims dims, bs
   }
 }
 
-// Launches the kernel after this call's previous one as its programmatic dependent.
-template <typename K, typename... Args>
-bs_status launch_next(K kernel, int ctas, cudaStream_t cs, Args... args) {
-  return launch_ex(kernel, dim3(ctas), kPgThreads, 0, cs, 0, true, args...) == cudaSuccess ? BS_OK : BS_ERR_CUDA;
+template <int NT = kPgThreads, typename K, typename... Args>
+bs_status launch_pg(K kernel, int ctas, cudaStream_t cs, Args... args) {
+  return launch_ex(kernel, dim3(ctas), NT, 0, cs, 0, true, args...) == cudaSuccess ? BS_OK : BS_ERR_CUDA;
 }
 
 bs_status check_map(const bs_dims *dims, const bs_page_map *map, const int32_t *dev_status) {
@@ -610,9 +614,9 @@ bs_status bs_pages_reserve(const bs_dims *dims, const bs_page_map *map, const in
   const PgWs ws = pg_ws(*dims, workspace);
   const int units = dims->batch * dims->n_kv_heads;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  reserve_scan<<<ws.n_tiles + std::min(units, kMaxCtas), kPgThreads, 0, cs>>>(*dims, *map, new_lens, ws);
-  if (cudaGetLastError() != cudaSuccess) return BS_ERR_CUDA;
-  return launch_next(reserve_apply, std::min(units, kMaxCtas), cs, *dims, *map, new_lens, ws, dev_status);
+  s = launch_pg(reserve_scan, ws.n_tiles + std::min(units, kMaxCtas), cs, *dims, *map, new_lens, ws);
+  if (s != BS_OK) return s;
+  return launch_pg(reserve_apply, std::min(units, kMaxCtas), cs, *dims, *map, new_lens, ws, dev_status);
 }
 
 bs_status bs_pages_fork(const bs_dims *dims, const bs_page_map *map, const int32_t *src, const int32_t *dst, int32_t n,
@@ -630,9 +634,9 @@ bs_status bs_pages_fork(const bs_dims *dims, const bs_page_map *map, const int32
   if (s != BS_OK) return s;
   const PgWs ws = pg_ws(*dims, workspace);
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  fork_scan<<<ws.n_tiles + std::min(items, kMaxCtas), kPgThreads, 0, cs>>>(*dims, *map, src, dst, n, ws);
-  if (cudaGetLastError() != cudaSuccess) return BS_ERR_CUDA;
-  return launch_next(fork_apply, std::min(items, kMaxCtas), cs, *dims, *map, src, dst, n, *copies, ws, dev_status);
+  s = launch_pg(fork_scan, ws.n_tiles + std::min(items, kMaxCtas), cs, *dims, *map, src, dst, n, ws);
+  if (s != BS_OK) return s;
+  return launch_pg(fork_apply, std::min(items, kMaxCtas), cs, *dims, *map, src, dst, n, *copies, ws, dev_status);
 }
 
 bs_status bs_pages_free(const bs_dims *dims, const bs_page_map *map, const int32_t *seqs, int32_t n,
@@ -641,9 +645,8 @@ bs_status bs_pages_free(const bs_dims *dims, const bs_page_map *map, const int32
   bs_status s = check_map(dims, map, dev_status);
   if (s != BS_OK) return s;
   if (!seqs || n < 1 || n > dims->batch) return BS_ERR_INVALID_ARG;
-  free_kernel<<<std::min(n * dims->n_kv_heads, kMaxCtas), kPgThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
-      *dims, *map, seqs, n, dev_status);
-  return launch_status();
+  return launch_pg(free_kernel, std::min(n * dims->n_kv_heads, kMaxCtas), reinterpret_cast<cudaStream_t>(stream), *dims, *map,
+                   seqs, n, dev_status);
 }
 
 bs_status bs_pages_compact(const bs_dims *dims, const bs_page_map *map, const bs_page_copies *copies, int32_t *n_live,
@@ -658,14 +661,14 @@ bs_status bs_pages_compact(const bs_dims *dims, const bs_page_map *map, const bs
   if (s != BS_OK) return s;
   const PgWs ws = pg_ws(*dims, workspace);
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  compact_scan<<<ws.n_tiles, kPgThreads, 0, cs>>>(*dims, *map, ws);
-  if (cudaGetLastError() != cudaSuccess) return BS_ERR_CUDA;
+  s = launch_pg(compact_scan, ws.n_tiles, cs, *dims, *map, ws);
+  if (s != BS_OK) return s;
   const int64_t ctas = (dims->n_pages + kPgThreads - 1) / kPgThreads;
-  s = launch_next(compact_move, static_cast<int>(std::min<int64_t>(ctas, 4 * kApplyCtas)), cs, *dims, *map, *copies, n_live, ws,
+  s = launch_pg(compact_move, static_cast<int>(std::min<int64_t>(ctas, 4 * kApplyCtas)), cs, *dims, *map, *copies, n_live, ws,
                   dev_status);
   if (s != BS_OK) return s;
   const int64_t entries = static_cast<int64_t>(dims->batch) * dims->n_kv_heads * dims->max_pages_per_unit;
-  return launch_next(compact_table, static_cast<int>(std::min<int64_t>((entries + kPgThreads - 1) / kPgThreads, 4 * kApplyCtas)),
+  return launch_pg(compact_table, static_cast<int>(std::min<int64_t>((entries + kPgThreads - 1) / kPgThreads, 4 * kApplyCtas)),
                      cs, *dims, *map, ws, dev_status);
 }
 
@@ -681,9 +684,9 @@ bs_status bs_pages_copy(const bs_dims *dims, const bs_pools *pools, const bs_pag
   if (s != BS_OK) return s;
   if (!aligned16(pools->k_pool) || !aligned16(pools->v_pool)) return BS_ERR_ALIGN;
   const int esz = quant ? 1 : dims->kv_dtype == BS_BF16 ? 2 : 4;
-  copy_kernel<<<std::min(copies->capacity, 16 * kApplyCtas), kCopyPageThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(
-      *dims, *pools, *copies, kPage * dims->head_dim * esz, quant, dev_status);
-  return launch_status();
+  return launch_pg<kCopyPageThreads>(copy_kernel, std::min(copies->capacity, 16 * kApplyCtas),
+                                     reinterpret_cast<cudaStream_t>(stream), *dims, *pools, *copies, kPage * dims->head_dim * esz,
+                                     quant, dev_status);
 }
 
 }  // extern "C"
