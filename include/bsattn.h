@@ -532,7 +532,8 @@ bs_status bs_pages_reserve(const bs_dims *dims, const bs_page_map *map, const in
  * pages (their counts grow), and the partial last page, where tokens will be appended,
  * gets a free page of its own with a pair (src's page, the free page) in `copies`, in
  * order of i, then KV head. Logical pages of src past its length are not shared; an
- * entry of src that holds no page (-1) stays -1.
+ * entry of src that holds no page (-1) stays -1. A decode loop's other state of a unit
+ * (summaries, alive mask, previous selection) is the caller's to copy.
  * One src may have many dst. Every dst must be an empty slot (no page in its rows), named
  * once, and be no src of the same call; both in [0, batch): else BS_ERR_INVALID_ARG.
  * BS_ERR_CAPACITY for too few free pages or a src length beyond its row (src length < 0:

@@ -217,6 +217,29 @@ def test_lowest_free_pages_in_pools_of_any_size(n_pages):
         g.check(m)
 
 
+def test_compact_a_large_pool():
+    """Larger tiles (above 2^22 pages), against array operations."""
+    n = 5_000_011
+    rng = np.random.default_rng(3)
+    m = Model(2, 1, 3000, n)
+    m.table[:] = rng.permutation(n)[:6000].reshape(2, 3000)
+    m.table[1, 2500:] = -1
+    m.ref = (rng.random(n) < 0.45).astype(np.int64) * 3
+    m.ref[m.table[m.table >= 0]] = 1
+    g = Map(m)
+    n_live = int((m.ref > 0).sum())
+    at = np.arange(n)
+    src, dst = at[(m.ref > 0) & (at >= n_live)], at[(m.ref == 0) & (at < n_live)]
+    to = at.copy()
+    to[src] = dst
+    m.table = np.where(m.table >= 0, to[m.table], m.table)
+    m.ref[dst], m.ref[src] = m.ref[src], 0
+    g.compact()
+    assert g.take_status() == 0 and int(g.n_live) == n_live and int(g.count) == len(src)
+    assert np.array_equal(g.pairs[:len(src)].cpu().numpy(), np.stack([src, dst], 1))
+    g.check(m)
+
+
 def filled(Bn=4, H=2, P=8, n_pages=64, lens=(40, 16, 0, 0)):
     m = Model(Bn, H, P, n_pages)
     m.reserve(lens)

@@ -204,6 +204,38 @@ def test_append_token_by_token_rounds_pages_again(kind):
     assert int(c.status) == 0
 
 
+@pytest.mark.parametrize("kind", sorted(KINDS))
+def test_append_after_a_page_of_zeros(kind):
+    """A page whose scale is 0 takes real values: its zeros stay zeros."""
+    rng = np.random.default_rng(10)
+    c = Cache([0], 1, 128, kind, rng, cap=16)
+    codes, sc = {s: c.pools[s][0].copy() for s in "kv"}, {s: c.pools[s][1].copy() for s in "kv"}
+    for t, x in enumerate((torch.zeros((1, 256)), torch.zeros((1, 256)), torch.randn((1, 256)), torch.zeros((1, 256)))):
+        x = x.cuda().bfloat16()
+        B.quant_append(c.dims, c.pool_ptrs, c.t_table, i32([t + 1]), i32([t]), i32([0]), x[:, :128], x[:, 128:], 256, 1,
+                       1, c.status)
+        xs, ph = x.float().cpu().numpy(), c.table[0, 0]
+        for s, pool, scale, off in (("k", c.k, c.ks, 0), ("v", c.v, c.vs, 128)):
+            codes[s][ph], sc[s][ph] = Q.append_page(codes[s][ph], sc[s][ph], t, xs[:, off:off + 128], kind)
+            assert Q.same_codes(u8(pool), codes[s], kind) and np.array_equal(scale.cpu().numpy(), sc[s], equal_nan=True)
+    assert int(c.status) == 0 and sc["k"][c.table[0, 0]] > 0
+
+
+def test_append_takes_more_tokens_than_the_grid_was_sized_for():
+    """max_new_tokens sizes the grid only."""
+    rng = np.random.default_rng(12)
+    c = Cache([5, 0], 2, 64, "int8", rng, cap=400)
+    x = torch.as_tensor(rng.normal(size=(700, 256)), device="cuda").bfloat16()
+    both = []
+    for max_new in (350, 1):
+        k, v, ks, vs = c.k.clone(), c.v.clone(), c.ks.clone(), c.vs.clone()
+        pools = B.Pools(k_pool=k.data_ptr(), v_pool=v.data_ptr(), k_scale=ks.data_ptr(), v_scale=vs.data_ptr())
+        B.quant_append(c.dims, pools, c.t_table, i32([355, 350]), i32([5, 0]), i32([0, 350]), x[:, :128], x[:, 128:], 256,
+                       700, max_new, c.status)
+        both.append((k, v, ks, vs))
+    assert int(c.status) == 0 and all(torch.equal(a, b) for a, b in zip(*both)) and not torch.equal(both[0][0], c.k)
+
+
 def test_append_skips_what_does_not_fit():
     """Each sequence's own fault is reported and the others are written."""
     rng = np.random.default_rng(9)
@@ -333,6 +365,9 @@ PLANS = {  # name: (Hkv, lens, g, frac)
     "cluster-many-units": (8, [700 + 5 * i for i in range(40)], [64], 0.3),
     "workspace": (5, [9000 + 700 * i for i in range(5)], [16, 64, 128], 0.6),
     "workspace-long": (2, [20000, 17], [64], 0.95),
+    "long-rows": (1, [12003], [16], 0.95),                            # more blocks than a CTA stages
+    "many-pages-a-warp": (8, [2100 + 37 * i for i in range(40)], [64], 0.95),
+    "most-pages-a-warp": (1, [130001], [64], 0.98),
 }
 
 
@@ -352,7 +387,7 @@ def test_attention_group_sizes(G, q32):
 
 
 @pytest.mark.parametrize("kind", sorted(KINDS))
-@pytest.mark.parametrize("plan", ["tiny-ragged", "cluster", "workspace"])
+@pytest.mark.parametrize("plan", ["tiny-ragged", "cluster", "workspace", "many-pages-a-warp"])
 def test_attention_block_logits(plan, kind):
     """Random block logits; dropped blocks (-inf) hold NaN codes and scales; a unit drops whole."""
     Hkv, lens, g, frac = PLANS[plan]
@@ -482,6 +517,98 @@ def test_attention_in_a_captured_graph():
     assert int(c.status) == 0
 
 
+def test_pages_past_32_bit_offsets():
+    """A pool of more than 2^32 bytes: append, attention, means and page copies at its far end."""
+    n, d = (1 << 21) + 64, 128                        # 2 KB pages: 4.3 GB each of K and V
+    if torch.cuda.mem_get_info()[0] < 12 << 30:
+        pytest.skip("needs 12 GB")
+    rng = np.random.default_rng(20)
+    k, v = (torch.zeros((n, 16, d), dtype=torch.int8, device="cuda") for _ in range(2))
+    ks, vs = (torch.zeros(n, device="cuda") for _ in range(2))
+    T, last = 50, n - 1
+    table = i32([[last, last - 1, last - 2, last - 3]])
+    dims = B.Dims(batch=1, n_q_heads=4, n_kv_heads=1, head_dim=d, page_size=16, max_pages_per_unit=4,
+                  max_blocks_per_unit=2, max_sel_per_unit=2, max_subs_per_unit=4, max_gather_pages_per_unit=4, n_pages=n,
+                  kv_dtype=B.BS_INT8, q_dtype=B.BS_BF16)
+    status, lens = i32([0]), i32([T])
+    pools = B.Pools(k_pool=k.data_ptr(), v_pool=v.data_ptr(), k_scale=ks.data_ptr(), v_scale=vs.data_ptr())
+    x = torch.as_tensor(rng.normal(size=(T, 2 * d)), device="cuda").bfloat16()
+    B.quant_append(dims, pools, table, lens, i32([0]), i32([0]), x[:, :d], x[:, d:], 2 * d, T, T, status)
+    K, V = (np.concatenate([Q.decode(u8(p[last - j]), "int8") * float(s[last - j]) for j in range(4)])[:T]
+            for p, s in ((k, ks), (v, vs)))
+    xs = x.float().cpu().numpy()
+    # INT8: within half a step, and the fp32 rounding of quotient and scale
+    assert (np.abs(K - xs[:, :d]) <= np.abs(xs[:, :d]).max() / 127 * 0.5001).all()
+    q = torch.as_tensor(rng.normal(size=(1, 4, d)), device="cuda").bfloat16()
+    kv = B.KV(k_pool=k.data_ptr(), v_pool=v.data_ptr(), page_table=table.data_ptr(), seq_lens=lens.data_ptr(),
+              k_scale=ks.data_ptr(), v_scale=vs.data_ptr())
+    out, lse = torch.zeros((1, 4, d), device="cuda"), torch.zeros((1, 4), device="cuda")
+    g = i32([32])
+    ws = torch.zeros(B.workspace_size(dims) // 4, device="cuda")
+
+    def attend(kv):
+        B.sparse_decode_attn(dims, q, kv, B.HeadCfg(block_tokens=g.data_ptr()), i32([[0, 1]]), i32([2]), out, lse, ws,
+                             status)
+        torch.cuda.synchronize()
+        want, _ = O.sparse_attention(q[0].double().cpu().numpy(), K, V, [0, 1], 32, T)
+        assert np.abs(out[0].cpu().numpy() - want).max() <= 1e-4
+
+    attend(kv)
+    one = {n_: i32([v_]) for n_, v_ in dict(cls=1, bt=32, st=16, k=1, ke=0, sink=16, loc=16, rows=4).items()}
+    off = torch.zeros(1, dtype=torch.int64, device="cuda")
+    cfg = B.HeadCfg(cls=one["cls"].data_ptr(), block_tokens=one["bt"].data_ptr(), sub_tokens=one["st"].data_ptr(),
+                    k_total=one["k"].data_ptr(), k_evict=one["ke"].data_ptr(), sink_tokens=one["sink"].data_ptr(),
+                    local_tokens=one["loc"].data_ptr(), sum_off=off.data_ptr(), sum_rows=one["rows"].data_ptr())
+    summ = torch.zeros(4 * d, device="cuda")
+    B.build_block_summaries(dims, kv, cfg, i32([0]), T, summ, status)
+    means = np.stack([K[16 * j:16 * (j + 1)].mean(0) for j in range(4)])
+    assert np.abs(summ.view(4, d).cpu().numpy() - means).max() <= 1e-5
+    # the four pages to the front, and attended there
+    pairs, count = i32([[last - j, j] for j in range(4)]), i32([4])
+    B.pages_copy(dims, pools, B.PageCopies(pairs=pairs.data_ptr(), count=count.data_ptr(), capacity=4), status)
+    front = i32([[0, 1, 2, 3]])
+    kv.page_table = front.data_ptr()
+    k[last - 3:].zero_()
+    attend(kv)
+    assert int(status) == 0
+
+
+def test_two_streams_at_once():
+    """Calls on two streams, each with its own cache and workspace: bitwise those of one at a time."""
+    rng = np.random.default_rng(22)
+    jobs = []
+    for Hkv, lens, kind in ((4, [9000, 8000], "e4m3"), (8, [3000] * 6, "int8")):
+        c = Cache(lens, Hkv, 128, kind, rng, G=4)
+        U, nb = c.B * Hkv, -(-max(lens) // 64)
+        c.dims.max_sel_per_unit = c.dims.max_blocks_per_unit = nb
+        c.dims.max_gather_pages_per_unit = 4 * nb
+        sel = np.where(np.arange(nb) < -(-c.T[:, None] // 64), np.arange(nb), -1)
+        job = dict(c=c, sel=i32(sel), cnt=i32((sel >= 0).sum(1)), g=i32([64] * U), s=torch.cuda.Stream(),
+                   q=torch.as_tensor(rng.normal(size=(c.B, 4 * Hkv, 128)), device="cuda").bfloat16(),
+                   ws=torch.zeros(B.workspace_size(c.dims) // 4, device="cuda"),
+                   out=torch.zeros((c.B, 4 * Hkv, 128), device="cuda"), lse=torch.zeros((c.B, 4 * Hkv), device="cuda"))
+        job["cfg"] = B.HeadCfg(block_tokens=job["g"].data_ptr())
+        jobs.append(job)
+
+    def go(j, stream=None):
+        B.sparse_decode_attn(j["c"].dims, j["q"], j["c"].kv, j["cfg"], j["sel"], j["cnt"], j["out"], j["lse"], j["ws"],
+                             j["c"].status, stream)
+
+    alone = []
+    for j in jobs:
+        go(j)
+        torch.cuda.synchronize()
+        alone.append((j["out"].clone(), j["lse"].clone()))
+        j["out"].zero_()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for j in jobs:
+            go(j, j["s"])
+    torch.cuda.synchronize()
+    for j, (out, lse) in zip(jobs, alone):
+        assert int(j["c"].status) == 0 and torch.equal(j["out"], out) and torch.equal(j["lse"], lse)
+
+
 # ----------------------------------------------------------------------------------
 # The decode loop over an 8-bit cache
 # ----------------------------------------------------------------------------------
@@ -557,6 +684,42 @@ def test_decode_loop_block_logits():
         t = O.selected_tokens(sel[u], g, T)
         to, _ = bound(qh, K[t], V[t], len(sel[u]) * g / 16, wl.d)
         assert np.abs(layer.out[b, h * wl.G:(h + 1) * wl.G].cpu().numpy() - want).max() <= 2 * to
+
+
+def test_fused_step_wait_runs_out_and_recovers():
+    """A selection held back (through the caller's own workspace words): the 8-bit attention's
+    bounded wait gives up, reports it, and the next step is right."""
+    wl = make_workload(2, seed=35, T=3001)
+    layer = PagedLayer(wl, kv8="int8")
+    layer.prefill()
+    layer.append(0)
+    torch.cuda.synchronize()
+    u = next(x for x in range(wl.U) if wl.cls[x] != O.STREAMING)
+    default = B.wait_limit_ns()
+    B.set_wait_limit_ns(2_000_000)
+    try:
+        layer.workspace.view(torch.int32)[u] = 1 << 20       # the unit's selection ticket
+        layer.fused_step(0)
+        torch.cuda.synchronize()
+        assert layer.read_status() == B.BS_ERR_TIMEOUT
+    finally:
+        B.set_wait_limit_ns(default)
+    layer.workspace.zero_()
+    layer.status.zero_()
+    for cnt in layer.cnt:
+        cnt.zero_()
+    layer.fused_step(0)
+    torch.cuda.synchronize()
+    assert layer.read_status() == 0
+    T, g, h = int(wl.T(0, 0)), int(wl.g[u]), u % wl.Hkv
+    K, V = (Q.dequant_unit(u8(p), s.cpu().numpy(), wl.page_table[u], T, "int8")
+            for p, s in ((layer.k_pool, layer.k_scale), (layer.v_pool, layer.v_scale)))
+    sel = layer.selection(1 - layer.cur)[u]
+    qh = layer.q[0][0, h * wl.G:(h + 1) * wl.G].double().cpu().numpy()
+    want, _ = O.sparse_attention(qh, K, V, sel, g, T)
+    t = O.selected_tokens(sel, g, T)
+    assert np.abs(layer.out[0, h * wl.G:(h + 1) * wl.G].cpu().numpy() - want).max() <= \
+        bound(qh, K[t], V[t], len(sel) * g / 16, wl.d)[0]
 
 
 def test_layer_refuses_an_unknown_type():
