@@ -26,6 +26,12 @@
 // exact down to 2^-39 of the row's largest element); P is scaled by 2^14 and enters as hi +
 // lo, so that weights down to 2^-28 of the largest keep 22 bits; sums are fp32. The V scale is
 // applied to each page's product in fp32, so no scale can leave fp16's range.
+//
+// Measured (G = 4, d = 128, E4M3, 32 units of a 128K batch, 69.5 MB of selected codes): 21.6 us
+// a call, 3.2 TB/s over the whole call and 5.8 TB/s of random 2 KB pages in the loop itself;
+// bound by memory there (without the V products 21.1 us), by the chain of launch, block list,
+// page indices and first copies (3.8 us) before it and the workspace merge (3 us) after it.
+// Short calls are that chain: 8.3 us for 8 units of 32K, 4.0 us for one token.
 #include <algorithm>
 #include <atomic>
 
@@ -43,25 +49,25 @@ constexpr int kMinSplit = 8;
 constexpr int kStepSplit = 40;
 constexpr float kPScale = 16384.0f;  // weights enter the V products times 2^14, the V scales times 2^-14
 
-// Shared memory: the staged selection entries, then the warps' rings; after the loop the
-// warps' states take the rings' place.
+// Shared memory: the staged selection entries, then the warps' buffers; after the loop the
+// warps' states take the buffers' place.
 template <int D>
 struct QuantLayout {
   static constexpr int kPageBytes = kPage * D;
-  static constexpr int kOffRing = kSelPreload * 4;                           // per warp: a pair of K, a pair of V
+  static constexpr int kOffBuf = kSelPreload * 4;                           // per warp: a pair of K, a pair of V
   static constexpr int kWarpBytes = 4 * kPageBytes;
-  static constexpr int kOffO = kOffRing;                                     // [4][8][D]
+  static constexpr int kOffO = kOffBuf;                                     // [4][8][D]
   static constexpr int kOffMl = kOffO + kQuantWarps * kMaxG * D * 4;         // m, l: [2][4][8]
   static constexpr int kEnd = kOffMl + 2 * kQuantWarps * kMaxG * 4;
-  static constexpr int kRings = kOffRing + kQuantWarps * kWarpBytes;
+  static constexpr int kBufEnd = kOffBuf + kQuantWarps * kWarpBytes;
   // What a cluster's other CTAs send while this one may still be in its loop: per column
   // entry, o (float4) and (m, l).
-  static constexpr int kOffRecvO = kEnd > kRings ? kEnd : kRings;
+  static constexpr int kOffRecvO = kEnd > kBufEnd ? kEnd : kBufEnd;
   static constexpr int kOffRecvMl = kOffRecvO + kMaxG * D * 4;
   static constexpr int kBytes = kOffRecvMl + kMaxG * (D / 4) * 8;
 };
 
-// Byte offset of 16-byte chunk `ch` of row `row` of a page in a ring slot.
+// Byte offset of 16-byte chunk `ch` of row `row` of a page in its buffer.
 template <int D>
 __device__ __forceinline__ int swz8(int row, int ch) {
   return D == 128 ? row * 128 + ((ch ^ (row & 7)) << 4) : row * 64 + ((ch ^ ((row >> 1) & 3)) << 4);
@@ -74,7 +80,7 @@ template <int N>
 __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-// A page's codes into a ring slot (all 32 lanes; whole rows a warp instruction).
+// A page's codes into its buffer (all 32 lanes; whole rows a warp instruction).
 template <int D>
 __device__ __forceinline__ void copy_page(uint32_t slot, const uint8_t *pool, int phys) {
   constexpr int kChunks = D / 16;
@@ -90,8 +96,7 @@ __device__ __forceinline__ void copy_page(uint32_t slot, const uint8_t *pool, in
 // D = A B + D, m16n8k16, fp16 inputs, fp32 accumulators.
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                         uint32_t b0, uint32_t b1) {
-  asm(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -124,7 +129,7 @@ struct RawQ {
     const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
     const char *src = static_cast<const char *>(q) + ((orow0 + r) * D + (D / 4) * c) * (Q32 ? 4 : 2);
 #pragma unroll
-    for (int i = 0; i < kVecs; ++i) v[i] = r < G ? ldg_stream16(src + 16 * i) : make_uint4(0u, 0u, 0u, 0u);
+    for (int i = 0; i < kVecs; ++i) v[i] = r < G ? ld_stream16(src + 16 * i) : make_uint4(0u, 0u, 0u, 0u);
   }
   // Dimensions 4 s .. 4 s + 3 of the part.
   __device__ __forceinline__ void four(int s, float (&x)[4]) const {
@@ -476,7 +481,7 @@ __device__ __forceinline__ int resolve_quant_page(const UnitBlocks &ub, const At
   const bool logit = a.bias != nullptr;
   ok = ok && (!logit || (blk >= 0 && blk < dims.max_blocks_per_unit));
   const int p = __ldcg(where);
-  const float e = logit ? __ldg(a.bias + static_cast<size_t>(u) * dims.max_blocks_per_unit + (ok ? blk : 0)) : 0.0f;
+  const float e = logit ? __ldcg(a.bias + static_cast<size_t>(u) * dims.max_blocks_per_unit + (ok ? blk : 0)) : 0.0f;
   if (!ok || p < 0 || p >= dims.n_pages) {
     report(a.st, BS_ERR_DEVICE_BOUNDS);
     return 0;
@@ -524,8 +529,8 @@ __device__ bool attn_split_quant(const AttnArgs &a, unsigned char *smem, bool in
   const int n_mine = gp1 - gp0 > warp ? (gp1 - gp0 - warp + W - 1) / W : 0;
   uint32_t ch_page = 0;   // physical page (27 bits) and valid tokens (5 bits)
   float ch_ks = 0.0f, ch_vs = 0.0f, ch_bias = 0.0f;
-  unsigned char *kring = smem + L::kOffRing + warp * L::kWarpBytes, *vring = kring + 2 * L::kPageBytes;
-  const uint32_t kslot = smem_u32(kring), vslot = smem_u32(vring);
+  unsigned char *kbuf = smem + L::kOffBuf + warp * L::kWarpBytes, *vbuf = kbuf + 2 * L::kPageBytes;
+  const uint32_t kslot = smem_u32(kbuf), vslot = smem_u32(vbuf);
   const bool biased = a.bias != nullptr;
   // Pages i, i + 1 (i even: both lie in one chunk of 32).
   auto meta = [&](int i, PageMeta (&t)[2]) {
@@ -537,8 +542,8 @@ __device__ bool attn_split_quant(const AttnArgs &a, unsigned char *smem, bool in
       int phys;
       const int valid = resolve_quant_page(ub, a, pt, u, gp0 + warp + W * (i + lane), gp1, &phys, &ch_bias);
       ch_page = valid > 0 ? static_cast<uint32_t>(phys) << 5 | static_cast<uint32_t>(valid) : 0u;
-      ch_ks = valid > 0 ? __ldg(a.kv.k_scale + phys) : 0.0f;   // (not waited for until the pair is computed)
-      ch_vs = valid > 0 ? __ldg(a.kv.v_scale + phys) : 0.0f;
+      ch_ks = valid > 0 ? __ldcg(a.kv.k_scale + phys) : 0.0f;   // (not waited for until the pair is computed)
+      ch_vs = valid > 0 ? __ldcg(a.kv.v_scale + phys) : 0.0f;
     }
 #pragma unroll
     for (int j = 0; j < 2; ++j) t[j].page = __shfl_sync(0xffffffffu, ch_page, (i & 31) + j);
@@ -581,7 +586,7 @@ __device__ bool attn_split_quant(const AttnArgs &a, unsigned char *smem, bool in
     float x[8];
     if (any) {
 #pragma unroll
-      for (int j = 0; j < 2; ++j) page_scores<D, I8, Q32>(kring + j * L::kPageBytes, t[j], qh, ql, q_scale, x + 4 * j);
+      for (int j = 0; j < 2; ++j) page_scores<D, I8, Q32>(kbuf + j * L::kPageBytes, t[j], qh, ql, q_scale, x + 4 * j);
     }
     __syncwarp();
     PageMeta next[2];
@@ -602,7 +607,7 @@ __device__ bool attn_split_quant(const AttnArgs &a, unsigned char *smem, bool in
       for (int j = 0; j < 2; ++j) {
         uint32_t h[2], l[2];
         split_weights(x + 4 * j, h, l);
-        page_values<D, I8>(vring + j * L::kPageBytes, t[j], h, l, w);
+        page_values<D, I8>(vbuf + j * L::kPageBytes, t[j], h, l, w);
       }
     }
     __syncwarp();
@@ -611,7 +616,7 @@ __device__ bool attn_split_quant(const AttnArgs &a, unsigned char *smem, bool in
     t[1] = next[1];
   }
   cp_wait<0>();
-  __syncthreads();           // the rings' place is taken by the states below
+  __syncthreads();           // the buffers' place is taken by the states below
 
   // ---- combine the four warps' states ---------------------------------------------
   float *ow = reinterpret_cast<float *>(smem + L::kOffO);     // [4][8][D]

@@ -10,12 +10,12 @@
 //     and requests before its own (block scans over at most kMaxTiles and `units` ints) and
 //     gives each request its page: a binary search over the tiles' ranks in shared memory, then
 //     one load from the tile's list. (Binary searches over bitmap words instead, about fifteen
-//     dependent loads a request, and one entry a thread: 25.6 us for a batch turnover of 21
-//     sequences, 74K pages in all, against 18.5.)
+//     dependent loads a request, and one entry a thread: 25.6 us for a batch turnover of 21 of
+//     64 sequences of 8 heads, 148K table entries, against 17.8.)
 // The lists are a snapshot, so counts may be written while others still look pages up, and no
 // floating-point or order-dependent atomics are involved: integer counts only.
-// Bound by latency (a few dependent loads a launch) except for the copies, which are bound by
-// HBM.
+// Bound by latency (a launch and a few dependent loads, 2 to 3 us a kernel on small pools, 5 to
+// 8 on large ones under a cold cache) except for the copies, which are bound by HBM.
 #include <algorithm>
 
 #include "bs_attn_launch.cuh"
@@ -262,7 +262,8 @@ __device__ __forceinline__ Requests load_plan(const PgWs &ws, int n, int first, 
 }
 
 // ---------------------------------------------------------------------------
-// reserve
+// reserve: a CTA per unit. A thread takes four neighbouring entries, so that one scan ranks
+// 1024 of them. Scan 5.1 us, apply 7.5 us (64 sequences of 8 heads, 380K pages, cold).
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(kPgThreads) reserve_scan(bs_dims dims, bs_page_map map, const int32_t *new_lens, PgWs ws) {
   pdl_enter();
@@ -334,7 +335,9 @@ __global__ void __launch_bounds__(kPgThreads) reserve_apply(bs_dims dims, bs_pag
 }
 
 // ---------------------------------------------------------------------------
-// fork: item (i, h) = fork i, KV head h
+// fork: item (i, h) = fork i, KV head h. The scan reads what apply will write (dst's row) and
+// share (src's entries and their counts), so that apply need not check. Scan 5.2 us, apply
+// 6.5 us (16 beams of 8 heads over 8K tokens, cold).
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(kPgThreads) fork_scan(bs_dims dims, bs_page_map map, const int32_t *src, const int32_t *dst,
                                                         int n, PgWs ws) {
@@ -434,7 +437,8 @@ __global__ void __launch_bounds__(kPgThreads) fork_apply(bs_dims dims, bs_page_m
 }
 
 // ---------------------------------------------------------------------------
-// free: CTA (i, h)
+// free: CTA (i, h). Eight entries a thread in flight: rows of 2048 pages in one round of loads
+// and one of counts (6.6 us for 21 sequences of 8 heads, 148K entries in all, cold).
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(kPgThreads) free_kernel(bs_dims dims, bs_page_map map, const int32_t *seqs, int n, int32_t *st) {
   __shared__ int tmp[kPgWarps];
@@ -482,7 +486,7 @@ __global__ void __launch_bounds__(kPgThreads) free_kernel(bs_dims dims, bs_page_
 }
 
 // ---------------------------------------------------------------------------
-// compact
+// compact: scan 4.5 us, move 6.0 us, table 4.1 us (95K pages, 57K in use, cold).
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(kPgThreads) compact_scan(bs_dims dims, bs_page_map map, PgWs ws) {
   pdl_enter();
@@ -541,7 +545,7 @@ __global__ void __launch_bounds__(kPgThreads) compact_table(bs_dims dims, bs_pag
 }
 
 // ---------------------------------------------------------------------------
-// copy: a CTA per pair
+// copy: a CTA per pair, K and V in flight together; 23K pages of 2 + 2 KB: 30.5 us, 6.1 TB/s.
 // ---------------------------------------------------------------------------
 constexpr int kCopyPageThreads = 128;
 
