@@ -560,7 +560,7 @@ bs_status bs_pages_free(const bs_dims *dims, const bs_page_map *map, const int32
  * [N, n_pages) are free. At most n_pages / 2 moves; more than copies->capacity:
  * BS_ERR_CAPACITY and nothing moves (*count = 0, *n_live is still written). An entry
  * outside the pool, or one at or above N on a free page, is left as it is with
- * BS_ERR_DEVICE_BOUNDS; the rest is done. Three launches. */
+ * BS_ERR_DEVICE_BOUNDS; the rest is done. Two launches. */
 bs_status bs_pages_compact(const bs_dims *dims, const bs_page_map *map, const bs_page_copies *copies, int32_t *n_live,
                            void *workspace, size_t workspace_bytes, int32_t *dev_status, bs_stream_t stream);
 

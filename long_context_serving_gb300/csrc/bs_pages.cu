@@ -11,11 +11,11 @@
 //     gives each request its page: a binary search over the tiles' ranks in shared memory, then
 //     one load from the tile's list. (Binary searches over bitmap words instead, about fifteen
 //     dependent loads a request, and one entry a thread: 25.6 us for a batch turnover of 21 of
-//     64 sequences of 8 heads, 148K table entries, against 17.8.)
+//     64 sequences of 8 heads, 148K table entries, against 12.3.)
 // The lists are a snapshot, so counts may be written while others still look pages up, and no
 // floating-point or order-dependent atomics are involved: integer counts only.
-// Bound by latency (a launch and a few dependent loads, 2 to 3 us a kernel on small pools, 5 to
-// 8 on large ones under a cold cache) except for the copies, which are bound by HBM.
+// Bound by latency (a launch and a few dependent loads, about 2 us a kernel on small pools, 3 to
+// 5 on large ones) except for the copies, which are bound by HBM.
 #include <algorithm>
 
 #include "bs_attn_launch.cuh"
@@ -39,23 +39,21 @@ __host__ __device__ inline int64_t tile_pages_for(int64_t n_pages) {
   return t;
 }
 
-// Workspace (int32 words): header [8] | tile_free [kMaxTiles] | need [units] | err [units] |
-// bitmap [words] | word rank [words] | list [n_pages] | remap [n_pages].
+// Workspace (int32 words): tile_free [kMaxTiles] | need [units] | err [units] | bitmap [words] |
+// word rank [words] | list [n_pages].
 struct PgWs {
-  int32_t *head;        // [0] pages in use, [1] moves allowed (compact)
   int32_t *tile_free;
   int32_t *need, *err;
   uint32_t *bits;
   int32_t *rank;        // free pages of the word's tile before the word
   int32_t *list;        // tile t's free pages, ascending, from list[t * tile_pages]
-  int32_t *remap;       // where a moved page went
   int32_t n_tiles;
   int64_t n_words, tile_pages;
 };
 __host__ inline size_t pg_ws_ints(const bs_dims &d) {
   const size_t units = static_cast<size_t>(d.batch) * d.n_kv_heads;
   const size_t words = (static_cast<size_t>(d.n_pages) + 31) / 32;
-  return 8 + kMaxTiles + 2 * units + 2 * words + 2 * static_cast<size_t>(d.n_pages);
+  return kMaxTiles + 2 * units + 2 * words + static_cast<size_t>(d.n_pages);
 }
 __host__ inline PgWs pg_ws(const bs_dims &d, void *workspace) {
   const size_t units = static_cast<size_t>(d.batch) * d.n_kv_heads;
@@ -63,14 +61,12 @@ __host__ inline PgWs pg_ws(const bs_dims &d, void *workspace) {
   w.tile_pages = tile_pages_for(d.n_pages);
   w.n_tiles = static_cast<int32_t>((d.n_pages + w.tile_pages - 1) / w.tile_pages);
   w.n_words = (d.n_pages + 31) / 32;
-  w.head = static_cast<int32_t *>(workspace);
-  w.tile_free = w.head + 8;
+  w.tile_free = static_cast<int32_t *>(workspace);
   w.need = w.tile_free + kMaxTiles;
   w.err = w.need + units;
   w.bits = reinterpret_cast<uint32_t *>(w.err + units);
   w.rank = reinterpret_cast<int32_t *>(w.bits + w.n_words);
   w.list = w.rank + w.n_words;
-  w.remap = w.list + d.n_pages;
   return w;
 }
 
@@ -263,7 +259,9 @@ __device__ __forceinline__ Requests load_plan(const PgWs &ws, int n, int first, 
 
 // ---------------------------------------------------------------------------
 // reserve: a CTA per unit. A thread takes four neighbouring entries, so that one scan ranks
-// 1024 of them. Scan 5.1 us, apply 7.5 us (64 sequences of 8 heads, 380K pages, cold).
+// 1024 of them. With the free before it 12.3 us for 21 of 64 sequences of 8 heads, 148K entries
+// in a pool of 383K pages (17.8 with the entries loaded after the scan's end), 6.0 us for one
+// short sequence.
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(kPgThreads) reserve_scan(bs_dims dims, bs_page_map map, const int32_t *new_lens, PgWs ws) {
   pdl_enter();
@@ -294,10 +292,25 @@ __global__ void __launch_bounds__(kPgThreads) reserve_apply(bs_dims dims, bs_pag
   __shared__ int before[kMaxTiles + 1];
   __shared__ int tmp[kPgWarps];
   const int units = dims.batch * dims.n_kv_heads;
-  pdl_enter();
-  // A contiguous share of the units per CTA.
+  // A contiguous share of the units per CTA. The scan changes neither lengths nor rows, and was
+  // let in after everything before it had finished: the first entries are loaded beside it.
   const int u0 = static_cast<int>(static_cast<int64_t>(units) * blockIdx.x / gridDim.x);
   const int u1 = static_cast<int>(static_cast<int64_t>(units) * (blockIdx.x + 1) / gridDim.x);
+  const int MP = dims.max_pages_per_unit;
+  auto unit_pages_wanted = [&](int u) {
+    return (static_cast<int64_t>(max(__ldcg(new_lens + u / dims.n_kv_heads), 0)) + kPage - 1) / kPage;
+  };
+  int entry[kBatch];
+  {
+    const int64_t n0 = min(unit_pages_wanted(u0), static_cast<int64_t>(MP));
+    const int32_t *row = map.page_table + static_cast<size_t>(u0) * MP;
+#pragma unroll
+    for (int e = 0; e < kBatch; ++e) {
+      const int j = static_cast<int>(threadIdx.x) * kBatch + e;
+      entry[e] = j < n0 ? __ldcg(row + j) : 0;
+    }
+  }
+  pdl_enter();
   const Requests rq = load_plan(ws, units, u0, before);
   if (rq.err != BS_OK || rq.total > before[ws.n_tiles]) {
     if (blockIdx.x == 0 && threadIdx.x == 0) report(st, rq.err != BS_OK ? rq.err : BS_ERR_CAPACITY);
@@ -306,15 +319,16 @@ __global__ void __launch_bounds__(kPgThreads) reserve_apply(bs_dims dims, bs_pag
   int k = static_cast<int>(rq.before);
   for (int u = u0; u < u1; ++u) {
     if (ws.need[u] == 0) continue;
-    const int n = static_cast<int>((static_cast<int64_t>(max(new_lens[u / dims.n_kv_heads], 0)) + kPage - 1) / kPage);
-    int32_t *row = map.page_table + static_cast<size_t>(u) * dims.max_pages_per_unit;
+    const int n = static_cast<int>(unit_pages_wanted(u));   // (within the row: else an error above)
+    int32_t *row = map.page_table + static_cast<size_t>(u) * MP;
     for (int i0 = 0; i0 < n; i0 += kPgThreads * kBatch) {
       const int first = i0 + threadIdx.x * kBatch;   // a thread's entries are neighbours: ranks ascend
       bool lacks[kBatch];
       int mine = 0;
 #pragma unroll
       for (int e = 0; e < kBatch; ++e) {
-        lacks[e] = first + e < n && row[first + e] < 0;
+        if (u > u0 || i0 > 0) entry[e] = first + e < n ? row[first + e] : 0;
+        lacks[e] = first + e < n && entry[e] < 0;
         mine += lacks[e] ? 1 : 0;
       }
       int total;
@@ -336,8 +350,9 @@ __global__ void __launch_bounds__(kPgThreads) reserve_apply(bs_dims dims, bs_pag
 
 // ---------------------------------------------------------------------------
 // fork: item (i, h) = fork i, KV head h. The scan reads what apply will write (dst's row) and
-// share (src's entries and their counts), so that apply need not check. Scan 5.2 us, apply
-// 6.5 us (16 beams of 8 heads over 8K tokens, cold).
+// share (src's entries and their counts), so that apply need not check. With the free before
+// and the copy after it 12.5 us for 16 beams of 8 heads over 8K tokens, 8.3 us for three short
+// ones.
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(kPgThreads) fork_scan(bs_dims dims, bs_page_map map, const int32_t *src, const int32_t *dst,
                                                         int n, PgWs ws) {
@@ -438,7 +453,7 @@ __global__ void __launch_bounds__(kPgThreads) fork_apply(bs_dims dims, bs_page_m
 
 // ---------------------------------------------------------------------------
 // free: CTA (i, h). Eight entries a thread in flight: rows of 2048 pages in one round of loads
-// and one of counts (6.6 us for 21 sequences of 8 heads, 148K entries in all, cold).
+// and one of counts.
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(kPgThreads) free_kernel(bs_dims dims, bs_page_map map, const int32_t *seqs, int n, int32_t *st) {
   __shared__ int tmp[kPgWarps];
@@ -486,16 +501,18 @@ __global__ void __launch_bounds__(kPgThreads) free_kernel(bs_dims dims, bs_page_
 }
 
 // ---------------------------------------------------------------------------
-// compact: scan 4.5 us, move 6.0 us, table 4.1 us (95K pages, 57K in use, cold).
+// compact: pages and table entries look their ranks up in the same launch (a remap table in
+// between cost a third one: 9.5 us a small cache with its copy, against 7.7).
 // ---------------------------------------------------------------------------
 __global__ void __launch_bounds__(kPgThreads) compact_scan(bs_dims dims, bs_page_map map, PgWs ws) {
   pdl_enter();
   scan_tile(dims, map.ref_count, ws, blockIdx.x, true);
 }
 
-// One thread per page: a page in use at or above N moves.
-__global__ void __launch_bounds__(kPgThreads) compact_move(bs_dims dims, bs_page_map map, bs_page_copies copies, int32_t *n_live,
-                                                           PgWs ws, int32_t *st) {
+// The first `move_ctas` CTAs: one thread per page, a page in use at or above N moves. The
+// others: one thread per table entry, which finds where its page goes from the same ranks.
+__global__ void __launch_bounds__(kPgThreads) compact_apply(bs_dims dims, bs_page_map map, bs_page_copies copies, int32_t *n_live,
+                                                            PgWs ws, int move_ctas, int32_t *st) {
   __shared__ int before[kMaxTiles + 1];
   pdl_enter();
   load_plan(ws, 0, 0, before);
@@ -507,40 +524,34 @@ __global__ void __launch_bounds__(kPgThreads) compact_move(bs_dims dims, bs_page
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     *n_live = N;
     *copies.count = fits ? moves : 0;
-    ws.head[0] = N;
-    ws.head[1] = fits ? 1 : 0;
     if (!fits) report(st, BS_ERR_CAPACITY);
   }
-  if (!fits || moves == 0) return;
+  if (!fits) return;
   const int live_below_n = N - moves;
-  for (int64_t p = N + static_cast<int64_t>(blockIdx.x) * kPgThreads + threadIdx.x; p < n_pages;
-       p += static_cast<int64_t>(gridDim.x) * kPgThreads) {
-    if (ws.bits[p >> 5] >> (p & 31) & 1u) continue;
-    const int k = static_cast<int>(p) - free_rank(ws, before, p) - live_below_n;
-    const int to = kth_free(ws, before, k);
-    ws.remap[p] = to;
-    copies.pairs[2 * k] = static_cast<int>(p);
-    copies.pairs[2 * k + 1] = to;
-    map.ref_count[to] = map.ref_count[p];
-    map.ref_count[p] = 0;
+  auto is_free = [&](int64_t p) { return (ws.bits[p >> 5] >> (p & 31) & 1u) != 0; };
+  auto move_of = [&](int64_t p) { return static_cast<int>(p) - free_rank(ws, before, p) - live_below_n; };
+  if (static_cast<int>(blockIdx.x) < move_ctas) {
+    for (int64_t p = N + static_cast<int64_t>(blockIdx.x) * kPgThreads + threadIdx.x; p < n_pages;
+         p += static_cast<int64_t>(move_ctas) * kPgThreads) {
+      if (is_free(p)) continue;
+      const int k = move_of(p), to = kth_free(ws, before, k);
+      copies.pairs[2 * k] = static_cast<int>(p);
+      copies.pairs[2 * k + 1] = to;
+      map.ref_count[to] = map.ref_count[p];
+      map.ref_count[p] = 0;
+    }
+    return;
   }
-}
-
-__global__ void __launch_bounds__(kPgThreads) compact_table(bs_dims dims, bs_page_map map, PgWs ws, int32_t *st) {
-  pdl_enter();
-  const int N = ws.head[0];
-  const bool go = ws.head[1] != 0;
-  if (!go) return;
   const int64_t total = static_cast<int64_t>(dims.batch) * dims.n_kv_heads * dims.max_pages_per_unit;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * kPgThreads + threadIdx.x; i < total;
-       i += static_cast<int64_t>(gridDim.x) * kPgThreads) {
+  for (int64_t i = static_cast<int64_t>(blockIdx.x - move_ctas) * kPgThreads + threadIdx.x; i < total;
+       i += static_cast<int64_t>(gridDim.x - move_ctas) * kPgThreads) {
     const int p = map.page_table[i];
     if (p < N) continue;
-    if (p >= dims.n_pages || (ws.bits[p >> 5] >> (p & 31) & 1u)) {
+    if (p >= n_pages || is_free(p)) {
       report(st, BS_ERR_DEVICE_BOUNDS);
       continue;
     }
-    map.page_table[i] = ws.remap[p];
+    map.page_table[i] = kth_free(ws, before, move_of(p));
   }
 }
 
@@ -667,13 +678,10 @@ bs_status bs_pages_compact(const bs_dims *dims, const bs_page_map *map, const bs
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   s = launch_pg(compact_scan, ws.n_tiles, cs, *dims, *map, ws);
   if (s != BS_OK) return s;
-  const int64_t ctas = (dims->n_pages + kPgThreads - 1) / kPgThreads;
-  s = launch_pg(compact_move, static_cast<int>(std::min<int64_t>(ctas, 4 * kApplyCtas)), cs, *dims, *map, *copies, n_live, ws,
-                  dev_status);
-  if (s != BS_OK) return s;
   const int64_t entries = static_cast<int64_t>(dims->batch) * dims->n_kv_heads * dims->max_pages_per_unit;
-  return launch_pg(compact_table, static_cast<int>(std::min<int64_t>((entries + kPgThreads - 1) / kPgThreads, 4 * kApplyCtas)),
-                     cs, *dims, *map, ws, dev_status);
+  const int move_ctas = static_cast<int>(std::min<int64_t>((dims->n_pages + kPgThreads - 1) / kPgThreads, 2 * kApplyCtas));
+  const int table_ctas = static_cast<int>(std::min<int64_t>((entries + kPgThreads - 1) / kPgThreads, 2 * kApplyCtas));
+  return launch_pg(compact_apply, move_ctas + table_ctas, cs, *dims, *map, *copies, n_live, ws, move_ctas, dev_status);
 }
 
 bs_status bs_pages_copy(const bs_dims *dims, const bs_pools *pools, const bs_page_copies *copies, int32_t *dev_status,

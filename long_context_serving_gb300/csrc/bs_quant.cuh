@@ -10,11 +10,11 @@ namespace bsi {
 
 __host__ __device__ __forceinline__ bool is_quant(int kv_dtype) { return kv_dtype == BS_E4M3 || kv_dtype == BS_INT8; }
 
-// A load of data read once: no L1 line is kept for it. (Coherent, not ld.global.nc: a kernel
-// that is in place before the work ahead of it has finished may be reading what that wrote.)
+// A load of data read once, from L2. (Neither ld.global.nc nor an L1 line: a kernel that is in
+// place before the work ahead of it has finished reads what that wrote.)
 __device__ __forceinline__ uint4 ld_stream16(const void *p) {
   uint4 w;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.global.cg.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w)
                : "l"(p)
                : "memory");
