@@ -4,10 +4,10 @@
 // One warp per (page, K or V): a page is the unit of a scale, so the whole of its new rows
 // sit in one warp's registers (16-byte loads, every row's in flight together), one warp
 // reduction gives the largest magnitude, and the codes leave as full rows of 8-byte stores.
-// One pass: each new value is read once, each code written once; bound by HBM for prompts
-// (53.7K tokens of 8 heads, bf16 to INT8: 64.4 us, 5.1 TB/s; 59 us if no quotient ever lay next
-// to a half), by latency for single tokens (64 sequences of 8 heads: 2.9 us; one chain of
-// lengths -> page index -> rows and old scale).
+// One pass: each new value is read once, each code written once. Prompts are bound by HBM and by
+// instruction issue together (53.7K tokens of 8 heads, bf16 to INT8: 64.5 us, 5.1 TB/s, issue
+// slots 69 % busy; 59 us if no quotient ever lay next to a half), single tokens by latency (64
+// sequences of 8 heads: 2.9 us; one chain of lengths -> page index -> rows and old scale).
 #include "bs_attn_launch.cuh"
 #include "bs_quant.cuh"
 
