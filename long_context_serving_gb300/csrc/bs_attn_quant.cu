@@ -515,8 +515,9 @@ __device__ bool attn_split_quant(const AttnArgs &a, unsigned char *smem, bool in
   UnitBlocks ub = load_unit_blocks<NT>(a, u, sel_sm, in_step, in_cluster);
   check_split_bound(ub, n_part, split, st);
   // A cluster's splits, and in the fused step those of step_ws_splits, all stay to the end.
-  // The stand-alone call's know the unit's count at once: those past its pages leave.
-  const int ns = in_step || in_cluster ? n_part : max(1, ub.pg.n_split);
+  // The stand-alone call's know the unit's count at once: those past its pages leave (of a
+  // unit that cannot be attended all but the first, which writes its zeros).
+  const int ns = in_step || in_cluster ? n_part : ub.ok ? max(1, ub.pg.n_split) : 1;
   if (split >= ns) return false;
   const int n_pages = ub.ok ? ub.pg.n_pages : 0;
   const int gp0 = min(split * ub.pg.pps, n_pages);

@@ -481,6 +481,35 @@ def test_attention_bad_pages_and_counts_are_reported():
         assert np.abs(out[1].cpu().numpy() - want).max() <= 1e-4
 
 
+def test_attention_selection_beyond_the_dims_is_refused_whole():
+    """Workspace plan: a unit that selects more pages than max_gather_pages_per_unit allows for is
+    reported and gets zeros; the others are right, and so is the next call on the workspace."""
+    rng = np.random.default_rng(21)
+    c = Cache([12000] + [1000] * 23, 1, 64, "int8", rng, G=2)
+    d = c.dims
+    nb = -(-c.T // 32)
+    d.max_sel_per_unit = d.max_blocks_per_unit = int(nb.max())
+    d.max_gather_pages_per_unit = 300                      # unit 0 selects 750 pages
+    sel, g, cnt = i32(np.where(np.arange(nb.max()) < nb[:, None], np.arange(nb.max()), -1)), i32([32] * 24), i32(nb)
+    q = torch.as_tensor(rng.normal(size=(24, 2, 64)), device="cuda").bfloat16()
+    out, lse = torch.ones((24, 2, 64), device="cuda"), torch.ones((24, 2), device="cuda")
+    ws = torch.zeros(B.workspace_size(d) // 4, device="cuda")
+    K, V = c.unit(5)
+    want, _ = O.sparse_attention(q[5].double().cpu().numpy(), K, V, list(range(nb[5])), 32, 1000)
+    first = O.sparse_attention(q[0].double().cpu().numpy(), *c.unit(0), [0, 1, 9], 32, 12000)[0]
+    for k in range(3):
+        c.status.zero_()
+        if k == 2:                                         # now within the dims
+            cnt[0] = 3
+            sel[0, :3] = i32([0, 1, 9])
+        B.sparse_decode_attn(d, q, c.kv, B.HeadCfg(block_tokens=g.data_ptr()), sel, cnt, out, lse, ws, c.status)
+        torch.cuda.synchronize()
+        assert int(c.status) == (B.BS_ERR_DEVICE_BOUNDS if k < 2 else 0)
+        assert np.abs(out[5].cpu().numpy() - want).max() <= 1e-4
+        assert (out[0] == 0).all() if k < 2 else np.abs(out[0].cpu().numpy() - first).max() <= 1e-4
+        assert torch.equal(ws.view(torch.int32)[:48], torch.zeros(48, dtype=torch.int32, device="cuda"))   # tickets
+
+
 def test_attention_in_a_captured_graph():
     """Captured once, replayed over new queries, codes and lengths."""
     rng = np.random.default_rng(19)
