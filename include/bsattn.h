@@ -36,7 +36,8 @@
  *   passed by pointer; every array they point to, and every array argument, is
  *   DEVICE memory unless the parameter says otherwise.
  * Asynchrony. Each call validates its host-visible arguments, enqueues kernels on
- *   `stream` and returns. Nothing waits for the GPU.
+ *   `stream` and returns. Nothing waits for the GPU. The kernels run on the device that
+ *   is current: `stream` must be one of its streams and every pointer valid there.
  * Errors. Host-detected problems (null pointers, bad shapes, misalignment, a too
  *   small workspace) return a non-zero bs_status before anything is enqueued.
  *   A failed launch returns BS_ERR_CUDA. Problems only the device can see (a page

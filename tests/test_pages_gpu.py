@@ -148,7 +148,8 @@ class Map:
 
 
 @pytest.mark.parametrize("seed,Bn,H,P,n_pages", [(1, 1, 1, 1, 1), (2, 3, 1, 4, 40), (3, 5, 3, 9, 97), (4, 9, 2, 300, 4097),
-                                                 (5, 20, 8, 40, 5000), (6, 6, 4, 700, 8192), (7, 40, 16, 3, 2100)])
+                                                 (5, 20, 8, 40, 5000), (6, 6, 4, 700, 8192), (7, 40, 16, 3, 2100),
+                                                 (8, 400, 8, 2, 9000)])   # (more units than CTAs)
 def test_random_runs_equal_the_model(seed, Bn, H, P, n_pages):
     """Sixty random calls each; after every one the table, counts, lengths and copy list are the model's."""
     rng = np.random.default_rng(seed)
