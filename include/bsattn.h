@@ -215,8 +215,10 @@ bs_status bs_select_topk(const bs_dims *dims, const bs_head_cfg *cfg, const int3
  * pre-exponential logits and the exponential is applied only in the attention; here
  * read as each block's logit added to the attention logit of each of its tokens, so
  * exp(e) weights the block's tokens). Entries must be finite or -inf; a block at -inf
- * drops out, and a unit whose tokens all drop out gets a zero row and lse = -inf. Only
- * the entries of selected blocks are read.
+ * drops out, and a unit whose tokens all drop out gets a zero row and lse = -inf. Over
+ * bf16 and fp32 caches an entry times log2(e) must be finite in fp32 too (magnitudes up
+ * to 2.35e38; lower entries drop the block); over 8-bit caches every finite entry counts,
+ * the type's lowest among them. Only the entries of selected blocks are read.
  * Split-KV: a unit's gathered pages are cut into contiguous pieces; each piece keeps an
  * fp32 online softmax and the partials are merged by log-sum-exp in a fixed order, so
  * the result does not depend on timing. Two plans, chosen from the dims:

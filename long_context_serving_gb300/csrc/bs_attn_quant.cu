@@ -3,7 +3,11 @@
 // merges are those of the other caches (bs_attn_impl.cuh); only the page math differs.
 //
 // With ks, vs the scales of token t's page and K8, V8 its codes:
-//   x_h(t) = ks (q_h . K8[t]) log2(e) / sqrt(d) + bias2,   o_h += vs (2^(x_h(t) - m) V8[t]).
+//   x_h(t) = ks (q_h . K8[t]) / sqrt(d) + e,   o_h += vs (exp(x_h(t) - m) V8[t]).
+//
+// Logits and maxima are kept as they are, not times log2(e), so that every finite block logit e
+// counts (the type's lowest times log2(e) would be -inf); log2(e) enters x - m, whose
+// exponential is 2 to that power.
 //
 // A warp takes whole pages, two at a time, through two buffers of its own in shared memory,
 // one for a pair's K and one for its V, filled by 16-byte asynchronous copies (cp.async) and
@@ -113,7 +117,7 @@ __device__ __forceinline__ float f16_hi_f(uint32_t w) { return __half2float(__us
 // of it is read.
 struct PageMeta {
   uint32_t page;   // physical page << 5 | valid tokens (pools hold less than 2^27 pages)
-  float ks, vs, bias2;   // (vs times 2^-14)
+  float ks, vs, bias;   // (vs times 2^-14)
   __device__ __forceinline__ int valid() const { return static_cast<int>(page & 31u); }
   __device__ __forceinline__ int phys() const { return static_cast<int>(page >> 5); }
 };
@@ -177,8 +181,8 @@ __device__ __forceinline__ void q_to_f16(const RawQ<D, Q32> &raw, uint32_t (&hi)
     }
 }
 
-// A warp's running state: m and l of head lane / 4 (m in log2 units, replicated over the
-// head's four lanes; l a partial sum of 2^(x - m) per lane), and
+// A warp's running state: m and l of head lane / 4 (m replicated over the head's four lanes;
+// l a partial sum of exp(x - m) per lane), and
 // o[i][2 k + j] = O[head 2 c + j][dim r D/8 + 2 i + k].
 template <int D>
 struct WarpState {
@@ -212,7 +216,7 @@ __device__ __forceinline__ void page_scores(const unsigned char *slot, const Pag
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const float dot = Q32 ? s[i >> 1][i & 1] + s[i >> 1][2 + (i & 1)] : s[i >> 1][i & 1];
-    x[i] = fmaf(dot, f, t.bias2);
+    x[i] = fmaf(dot, f, t.bias);
   }
 }
 
@@ -261,14 +265,15 @@ __device__ __forceinline__ void page_values(const unsigned char *slot, const Pag
   }
 }
 
-__device__ __forceinline__ float exp2_ftz(float x) {
+// exp(x) as 2^(x log2 e), results below 2^-126 as 0.
+__device__ __forceinline__ float exp_ftz(float x) {
   float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * kLog2e));
   return y;
 }
 
 // Online softmax of this lane's head over the 32 tokens of two pages: x becomes the weights
-// 2^(x - m), the running state is rescaled when the maximum rises.
+// exp(x - m), the running state is rescaled when the maximum rises.
 template <int D>
 __device__ __forceinline__ void softmax_pair(float (&x)[8], WarpState<D> &w) {
   const int c = threadIdx.x & 3;
@@ -277,7 +282,7 @@ __device__ __forceinline__ void softmax_pair(float (&x)[8], WarpState<D> &w) {
   mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
   if (__any_sync(0xffffffffu, mx > w.m)) {
     const float m_new = fmaxf(w.m, mx);
-    const float alpha = m_new == -INFINITY ? 1.0f : exp2_ftz(w.m - m_new);
+    const float alpha = m_new == -INFINITY ? 1.0f : exp_ftz(w.m - m_new);
     w.m = m_new;
     w.l *= alpha;
     const float a0 = __shfl_sync(0xffffffffu, alpha, 8 * c), a1 = __shfl_sync(0xffffffffu, alpha, 8 * c + 4);
@@ -291,7 +296,7 @@ __device__ __forceinline__ void softmax_pair(float (&x)[8], WarpState<D> &w) {
   }
   const float base = w.m == -INFINITY ? 0.0f : w.m;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = exp2_ftz(x[i] - base);   // (a weight below 2^-126 of the largest is 0)
+  for (int i = 0; i < 8; ++i) x[i] = exp_ftz(x[i] - base);   // (a weight below 2^-126 of the largest is 0)
   w.l += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
 }
 __device__ __forceinline__ void split_weights(const float *x, uint32_t (&h)[2], uint32_t (&l)[2]) {
@@ -304,7 +309,7 @@ __device__ __forceinline__ void split_weights(const float *x, uint32_t (&h)[2], 
 }
 
 // One float4 column of the merge of n states of a head, visited in order, kFlight of them in
-// flight at once: load(k, m, l, o) gives state k's maximum (log2 units), sum and unnormalised column.
+// flight at once: load(k, m, l, o) gives state k's maximum, sum and unnormalised column.
 // A state with m = -inf has weight 0; a NaN stays one.
 template <int kFlight, class Load>
 __device__ __forceinline__ void merge_column(int n, Load load, float4 &o, float &m, float &l) {
@@ -325,12 +330,12 @@ __device__ __forceinline__ void merge_column(int n, Load load, float4 &o, float 
 #pragma unroll
     for (int k = 0; k < kFlight; ++k) m_new = fmaxf(m_new, mk[k]);
     const float base = m_new == -INFINITY ? 0.0f : m_new;
-    const float a = exp2f(m - base);
+    const float a = exp2f((m - base) * kLog2e);
     o.x *= a; o.y *= a; o.z *= a; o.w *= a;
     l *= a;
 #pragma unroll
     for (int k = 0; k < kFlight; ++k) {
-      const float wt = exp2f(mk[k] - base);
+      const float wt = exp2f((mk[k] - base) * kLog2e);
       o.x = fmaf(v[k].x, wt, o.x);
       o.y = fmaf(v[k].y, wt, o.y);
       o.z = fmaf(v[k].z, wt, o.z);
@@ -341,12 +346,12 @@ __device__ __forceinline__ void merge_column(int n, Load load, float4 &o, float 
   }
 }
 
-// o / l and lse = ln 2 (m + log2 l); a state with l = 0 (nothing attended) gives zeros and -inf.
+// o / l and lse = m + log l; a state with l = 0 (nothing attended) gives zeros and -inf.
 __device__ __forceinline__ void write_column(const float4 &o, float m, float l, float *orow, float *lse_h, int dq) {
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   reinterpret_cast<float4 *>(orow)[dq] =
       l == 0.0f ? make_float4(0.f, 0.f, 0.f, 0.f) : make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-  if (dq == 0) *lse_h = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+  if (dq == 0) *lse_h = l == 0.0f ? -INFINITY : m + logf(l);
 }
 
 // The first barrier of a cluster's life, in two halves: arrived at on entry, waited for
@@ -454,13 +459,13 @@ __device__ void finish_quant(const AttnArgs &a, const UnitBlocks &ub, int u, int
   }
 }
 
-// Page gp of the split as resolve_page gives it, with the block's logit in log2 units; its
+// Page gp of the split as resolve_page gives it, with the block's logit; its
 // load flies beside the page's. 0 tokens for a page that does not count: past the end,
 // outside the pool or the rows (reported), or of a block that dropped out (logit -inf).
 __device__ __forceinline__ int resolve_quant_page(const UnitBlocks &ub, const AttnArgs &a, const int32_t *pt, int u, int gp,
-                                                  int gp1, int *phys, float *bias2) {
+                                                  int gp1, int *phys, float *bias) {
   *phys = -1;
-  *bias2 = 0.0f;
+  *bias = 0.0f;
   if (gp >= gp1) return 0;
   const bs_dims &dims = a.dims;
   const int ppb = ub.pg.ppb, i = gp / ppb;
@@ -486,7 +491,7 @@ __device__ __forceinline__ int resolve_quant_page(const UnitBlocks &ub, const At
     report(a.st, BS_ERR_DEVICE_BOUNDS);
     return 0;
   }
-  *bias2 = e * kLog2e;
+  *bias = e;
   if (e == -INFINITY) return 0;   // (nothing of it is read)
   *phys = p;
   return valid;
@@ -555,7 +560,7 @@ __device__ bool attn_split_quant(const AttnArgs &a, unsigned char *smem, bool in
     for (int j = 0; j < 2; ++j) {
       t[j].ks = __shfl_sync(0xffffffffu, ch_ks, (i & 31) + j);
       t[j].vs = __shfl_sync(0xffffffffu, ch_vs, (i & 31) + j) * (1.0f / kPScale);
-      t[j].bias2 = biased ? __shfl_sync(0xffffffffu, ch_bias, (i & 31) + j) : 0.0f;
+      t[j].bias = biased ? __shfl_sync(0xffffffffu, ch_bias, (i & 31) + j) : 0.0f;
     }
   };
   // One group of copies a pair and pool, empty past the end.
@@ -578,7 +583,7 @@ __device__ bool attn_split_quant(const AttnArgs &a, unsigned char *smem, bool in
   uint32_t qh[D / 16][2], ql[D / 16][2];
   float q_scale;
   q_to_f16<D, Q32>(raw_q, qh, ql, &q_scale);
-  q_scale *= rsqrtf(static_cast<float>(D)) * kLog2e;
+  q_scale *= rsqrtf(static_cast<float>(D));
   for (int i = 0; i < n_mine; i += 2) {
     scales(i, t);
     const bool any = (t[0].page | t[1].page) != 0u;   // (none: dropped, or outside the pool)
