@@ -51,7 +51,7 @@ constexpr int kQuantWarps = kQuantThreads / 32;
 constexpr int kCtasPerSm = 2;
 constexpr int kMinSplit = 8;
 constexpr int kStepSplit = 40;
-constexpr float kPScale = 16384.0f;  // weights enter the V products times 2^14, the V scales times 2^-14
+constexpr float kPScale = 16384.0f;  // weights enter the V products times 2^14; the products leave times 2^-14
 
 // Shared memory: the staged selection entries, then the warps' buffers; after the loop the
 // warps' states take the buffers' place.
@@ -117,7 +117,7 @@ __device__ __forceinline__ float f16_hi_f(uint32_t w) { return __half2float(__us
 // of it is read.
 struct PageMeta {
   uint32_t page;   // physical page << 5 | valid tokens (pools hold less than 2^27 pages)
-  float ks, vs, bias;   // (vs times 2^-14)
+  float ks, vs, bias;
   __device__ __forceinline__ int valid() const { return static_cast<int>(page & 31u); }
   __device__ __forceinline__ int phys() const { return static_cast<int>(page >> 5); }
 };
@@ -183,11 +183,11 @@ __device__ __forceinline__ void q_to_f16(const RawQ<D, Q32> &raw, uint32_t (&hi)
 
 // A warp's running state: m and l of head lane / 4 (m replicated over the head's four lanes;
 // l a partial sum of exp(x - m) per lane), and
-// o[i][2 k + j] = O[head 2 c + j][dim r D/8 + 2 i + k].
+// o[i][k] = O[heads 2 c, 2 c + 1][dim r D/8 + 2 i + k].
 template <int D>
 struct WarpState {
   float m, l;
-  float o[D / 16][4];
+  float2 o[D / 16][2];
 };
 
 // S = q K8^T of the page in `slot`: two tiles of eight tokens; x[i] of token 2c + (i & 1) +
@@ -220,8 +220,10 @@ __device__ __forceinline__ void page_scores(const unsigned char *slot, const Pag
   }
 }
 
-// O^T += vs V8^T P^T of the page in `slot` (h, l: P as fp16 pairs, hi and lo). Codes of tokens
-// that do not count may be anything (NaN too) and are zeroed.
+// O^T += vs V8^T P^T of the page in `slot` (h, l: P times 2^14 as fp16 pairs, hi and lo). The
+// products come back to their size before the scale enters: 2^-14 vs may be subnormal. Two-wide
+// fp32 makes that free (the multiplication and the addition take the issue slots of one-wide
+// additions). Codes of tokens that do not count may be anything (NaN too) and are zeroed.
 template <int D, bool I8>
 __device__ __forceinline__ void page_values(const unsigned char *slot, const PageMeta &t, const uint32_t (&h)[2],
                                             const uint32_t (&l)[2], WarpState<D> &w) {
@@ -246,6 +248,7 @@ __device__ __forceinline__ void page_values(const unsigned char *slot, const Pag
         for (int g = 0; g < D / 32; ++g) v[i][g] = 0u;
       }
   }
+  const float2 back = make_float2(1.0f / kPScale, 1.0f / kPScale), vs = make_float2(t.vs, t.vs);
 #pragma unroll
   for (int g = 0; g < D / 32; ++g) {      // four dimensions of the lane's chunk
     const uint32_t v0 = v[0][g], v1 = v[1][g], v2 = v[2][g], v3 = v[3][g];
@@ -260,7 +263,8 @@ __device__ __forceinline__ void page_values(const unsigned char *slot, const Pag
       mma_f16(acc, a[2 * i], a[2 * i + 1], b[2 * i], b[2 * i + 1], h[0], h[1]);
       mma_f16(acc, a[2 * i], a[2 * i + 1], b[2 * i], b[2 * i + 1], l[0], l[1]);
 #pragma unroll
-      for (int k = 0; k < 4; ++k) w.o[2 * g + i][k] = fmaf(acc[k], t.vs, w.o[2 * g + i][k]);
+      for (int k = 0; k < 2; ++k)
+        w.o[2 * g + i][k] = __ffma2_rn(__fmul2_rn(make_float2(acc[2 * k], acc[2 * k + 1]), back), vs, w.o[2 * g + i][k]);
     }
   }
 }
@@ -287,12 +291,9 @@ __device__ __forceinline__ void softmax_pair(float (&x)[8], WarpState<D> &w) {
     w.l *= alpha;
     const float a0 = __shfl_sync(0xffffffffu, alpha, 8 * c), a1 = __shfl_sync(0xffffffffu, alpha, 8 * c + 4);
 #pragma unroll
-    for (int i = 0; i < D / 16; ++i) {
-      w.o[i][0] *= a0;
-      w.o[i][1] *= a1;
-      w.o[i][2] *= a0;
-      w.o[i][3] *= a1;
-    }
+    for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) w.o[i][k] = __fmul2_rn(w.o[i][k], make_float2(a0, a1));
   }
   const float base = w.m == -INFINITY ? 0.0f : w.m;
 #pragma unroll
@@ -559,7 +560,7 @@ __device__ bool attn_split_quant(const AttnArgs &a, unsigned char *smem, bool in
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       t[j].ks = __shfl_sync(0xffffffffu, ch_ks, (i & 31) + j);
-      t[j].vs = __shfl_sync(0xffffffffu, ch_vs, (i & 31) + j) * (1.0f / kPScale);
+      t[j].vs = __shfl_sync(0xffffffffu, ch_vs, (i & 31) + j);
       t[j].bias = biased ? __shfl_sync(0xffffffffu, ch_bias, (i & 31) + j) : 0.0f;
     }
   };
@@ -575,7 +576,7 @@ __device__ bool attn_split_quant(const AttnArgs &a, unsigned char *smem, bool in
   w.m = -INFINITY;
   w.l = 0.0f;
 #pragma unroll
-  for (int i = 0; i < D / 16; ++i) w.o[i][0] = w.o[i][1] = w.o[i][2] = w.o[i][3] = 0.0f;
+  for (int i = 0; i < D / 16; ++i) w.o[i][0] = w.o[i][1] = make_float2(0.0f, 0.0f);
   PageMeta t[2];
   meta(0, t);
   copy_pair(t, kslot, kpool);
@@ -641,7 +642,7 @@ __device__ bool attn_split_quant(const AttnArgs &a, unsigned char *smem, bool in
 #pragma unroll
       for (int j = 0; j < 2; ++j)
         *reinterpret_cast<float2 *>(ow + (warp * kMaxG + 2 * c + j) * D + r * (D / 8) + 2 * i) =
-            make_float2(w.o[i][j], w.o[i][2 + j]);
+            j == 0 ? make_float2(w.o[i][0].x, w.o[i][1].x) : make_float2(w.o[i][0].y, w.o[i][1].y);
   }
   __syncthreads();
   finish_quant<D>(a, ub, u, split, ns, in_cluster, G, orow0, smem);

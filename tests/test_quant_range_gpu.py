@@ -105,3 +105,27 @@ def test_block_logits_of_the_largest_magnitudes(plan, kind, q32):
         tol = (64 * 2.0 ** -23 + 2.0 ** -21) * A + 2.0 ** -15 + nb[u] * 2.0 ** -22 + 2.0 ** -19
         # (a logit of 2^127 and the score beside it: the sum's last place, twice)
         assert (np.abs(lse[b, 2 * h:2 * h + 2] - want_l) <= tol + 2.0 ** -23 * np.abs(want_l)).all(), u
+
+
+@pytest.mark.parametrize("exponent", [-126, -122, -118])
+@pytest.mark.parametrize("d", [64, 128])
+def test_v_scales_near_the_smallest_normal(d, exponent):
+    """INT8 page scales are any fp32 from 2^-126 up: no bit of them is lost on the way. The same
+    cache with its V scales 2^60 larger gives the same results, 2^60 larger, but for what is
+    rounded below 2^-126: each page's sum, rescaling and merge by half of 2^-149, and with it the
+    last place of the result."""
+    rng = np.random.default_rng(52)
+    c = Cache([100, 700], 2, d, "int8", rng, G=3)
+    sc = (2.0 ** exponent * rng.uniform(1, 2, c.n_pages)).astype(np.float32)
+    c.vs.copy_(torch.as_tensor(sc))
+    q = torch.as_tensor(rng.normal(size=(2, 6, d)).astype(np.float32), device="cuda").bfloat16()
+    out, _ = attend_all(c, 32, q)
+    low = (4 * 44 + 64) * 2.0 ** -149                # 44 pages
+    for u in range(4):
+        b, h = divmod(u, 2)
+        want, _, S, R, A = definition(c, u, 32, q)
+        assert within(out[b, 3 * h:3 * h + 3], want, S, R, A, d, -(-c.T[u] // 16), tiny=low), u
+    c.vs.mul_(2.0 ** 60)
+    big, _ = attend_all(c, 32, q)
+    big *= 2.0 ** -60
+    assert (np.abs(out - big) <= 2.0 ** -22 * np.abs(big) + low).all() and np.abs(big).max() > 2.0 ** -122
