@@ -236,9 +236,10 @@ bs_status bs_select_topk(const bs_dims *dims, const bs_head_cfg *cfg, const int3
  *     others leave at once; the merge is the same, as their records were empty).
  * A unit's plan depends on its own sizes only, so a sub-batch launched with the same S
  * gives bitwise the same per-unit results as the full batch.
- * 8-bit caches: K[t] and V[t] are codes times their page's scale. The products are
- * accurate to fp32 (codes are exact in fp16; each query row is scaled by a power of two
- * and, like the probabilities, enters as fp16 parts hi + lo), whatever the scales. A
+ * 8-bit caches: K[t] and V[t] are codes times their page's scale. Codes are exact in
+ * fp16; queries and weights enter as fp16 parts hi + lo, a query element within 2^-22 of
+ * itself or 2^-39 of its row's largest element, a weight within 2^-22 of itself or 2^-38
+ * of its page's largest weight; sums and scales are fp32, whatever the scales. A
  * page whose block logit is -inf is not read; NaN codes in tokens past T do not count.
  * Their splits differ from the above: in cluster mode S is halved while a selection of
  * max_gather_pages_per_unit would leave a split fewer than 8 pages; in workspace mode up

@@ -25,14 +25,18 @@
 //     fragment of P^T in O^T = V8^T P^T (k = tokens, n = heads).
 //   V: lane reads chunk r (D / 8 dimensions) of those same four tokens, and pairs the tokens'
 //     bytes with one byte permutation per four codes before converting.
-// Precision: the codes are exact in fp16; a query row is multiplied by a power of two that
-// brings its largest element near 2^14 and enters as fp16 hi + lo (bf16 queries: hi alone is
-// exact down to 2^-39 of the row's largest element); P is scaled by 2^14 and enters as hi +
-// lo, so that weights down to 2^-28 of the largest keep 22 bits; sums are fp32. The V scale is
-// applied to each page's product in fp32, so no scale can leave fp16's range.
+// Precision: the codes are exact in fp16. A query row is multiplied by the power of two that
+// brings its largest element to [2^14, 2^15) and enters as fp16 hi + lo: an element keeps 2^-22
+// of itself, or 2^-39 of the row's largest where that is more. bf16 queries enter as hi alone,
+// exact down to 2^-31 of the row's largest and within 2^-39 of it below. The weights of a page
+// enter in the same way, at the power of two of that page's largest weight: within 2^-22 of
+// themselves or 2^-38 of that largest, so that pages may differ in their V scales without limit.
+// (One power for all pages, 21.7 us for the 128K batch below, would lose a page whose weights are
+// below 2^-38 of the largest, however large its V scale.) Sums are fp32; the scales are applied to
+// each page's product in fp32, so none can leave fp16's range.
 //
-// Measured (G = 4, d = 128, E4M3, 32 units of a 128K batch, 69.5 MB of selected codes): 21.6 us
-// a call, 3.2 TB/s over the whole call and 5.8 TB/s of random 2 KB pages in the loop itself;
+// Measured (G = 4, d = 128, E4M3, 32 units of a 128K batch, 69.5 MB of selected codes): 22.1 us
+// a call, 3.1 TB/s over the whole call and 5.8 TB/s of random 2 KB pages in the loop itself;
 // bound by memory there (without the V products 21.1 us), by the chain of launch, block list,
 // page indices and first copies (3.8 us) before it and the workspace merge (3 us) after it.
 // Short calls are that chain: 8.3 us for 8 units of 32K, 4.0 us for one token.
@@ -51,7 +55,6 @@ constexpr int kQuantWarps = kQuantThreads / 32;
 constexpr int kCtasPerSm = 2;
 constexpr int kMinSplit = 8;
 constexpr int kStepSplit = 40;
-constexpr float kPScale = 16384.0f;  // weights enter the V products times 2^14; the products leave times 2^-14
 
 // Shared memory: the staged selection entries, then the warps' buffers; after the loop the
 // warps' states take the buffers' place.
@@ -220,13 +223,14 @@ __device__ __forceinline__ void page_scores(const unsigned char *slot, const Pag
   }
 }
 
-// O^T += vs V8^T P^T of the page in `slot` (h, l: P times 2^14 as fp16 pairs, hi and lo). The
-// products come back to their size before the scale enters: 2^-14 vs may be subnormal. Two-wide
-// fp32 makes that free (the multiplication and the addition take the issue slots of one-wide
-// additions). Codes of tokens that do not count may be anything (NaN too) and are zeroed.
+// O^T += vs V8^T P^T of the page in `slot` (h, l: the page's weights at their power of two as
+// fp16 pairs, hi and lo; back: its reciprocal for heads 2 c and 2 c + 1). The products come back to their
+// size before the V scale enters: the two together may be subnormal. Two-wide fp32 makes that
+// free (the multiplication and the addition take the issue slots of one-wide additions). Codes
+// of tokens that do not count may be anything (NaN too) and are zeroed.
 template <int D, bool I8>
 __device__ __forceinline__ void page_values(const unsigned char *slot, const PageMeta &t, const uint32_t (&h)[2],
-                                            const uint32_t (&l)[2], WarpState<D> &w) {
+                                            const uint32_t (&l)[2], float2 back, WarpState<D> &w) {
   const int lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
   uint32_t v[4][D / 32];
 #pragma unroll
@@ -248,7 +252,7 @@ __device__ __forceinline__ void page_values(const unsigned char *slot, const Pag
         for (int g = 0; g < D / 32; ++g) v[i][g] = 0u;
       }
   }
-  const float2 back = make_float2(1.0f / kPScale, 1.0f / kPScale), vs = make_float2(t.vs, t.vs);
+  const float2 vs = make_float2(t.vs, t.vs);
 #pragma unroll
   for (int g = 0; g < D / 32; ++g) {      // four dimensions of the lane's chunk
     const uint32_t v0 = v[0][g], v1 = v[1][g], v2 = v[2][g], v3 = v[3][g];
@@ -278,12 +282,22 @@ __device__ __forceinline__ float exp_ftz(float x) {
 
 // Online softmax of this lane's head over the 32 tokens of two pages: x becomes the weights
 // exp(x - m), the running state is rescaled when the maximum rises.
+//
+// up[j] is the power of two that brings page j's largest weight near 2^14 (weights down to
+// 2^-112) before it enters fp16, back[j] its reciprocal for heads 2 c and 2 c + 1: a page's
+// weights keep their bits relative to that page's largest, so that pages may differ in their V
+// scales as fp32 allows.
 template <int D>
-__device__ __forceinline__ void softmax_pair(float (&x)[8], WarpState<D> &w) {
+__device__ __forceinline__ void softmax_pair(float (&x)[8], WarpState<D> &w, float (&up)[2], float2 (&back)[2]) {
   const int c = threadIdx.x & 3;
-  float mx = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), fmaxf(fmaxf(x[4], x[5]), fmaxf(x[6], x[7])));
-  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-  mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+  float top[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    float mx = fmaxf(fmaxf(x[4 * j], x[4 * j + 1]), fmaxf(x[4 * j + 2], x[4 * j + 3]));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+    top[j] = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+  }
+  const float mx = fmaxf(top[0], top[1]);
   if (__any_sync(0xffffffffu, mx > w.m)) {
     const float m_new = fmaxf(w.m, mx);
     const float alpha = m_new == -INFINITY ? 1.0f : exp_ftz(w.m - m_new);
@@ -296,14 +310,28 @@ __device__ __forceinline__ void softmax_pair(float (&x)[8], WarpState<D> &w) {
       for (int k = 0; k < 2; ++k) w.o[i][k] = __fmul2_rn(w.o[i][k], make_float2(a0, a1));
   }
   const float base = w.m == -INFINITY ? 0.0f : w.m;
+  // The exponent e of the page's largest weight, -112 .. 0: the nearest integer by the low bits
+  // of the sum with 1.5 * 2^23. back's exponent field is 113 + e (7 bits), up's 254 less it; the
+  // two pages' go to the lanes of the products in one word.
+  uint32_t field[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const float t = fmaxf((top[j] - base) * kLog2e, -112.0f) + 12582912.0f;
+    field[j] = __float_as_uint(t) - 0x4b400000u + 113u;
+    up[j] = __uint_as_float((254u - field[j]) << 23);
+  }
+  const uint32_t fields = field[1] << 16 | field[0];
+  const uint32_t f0 = __shfl_sync(0xffffffffu, fields, 8 * c), f1 = __shfl_sync(0xffffffffu, fields, 8 * c + 4);
+  back[0] = make_float2(__uint_as_float(f0 << 23), __uint_as_float(f1 << 23));
+  back[1] = make_float2(__uint_as_float(f0 << 7 & 0x7f800000u), __uint_as_float(f1 << 7 & 0x7f800000u));
 #pragma unroll
   for (int i = 0; i < 8; ++i) x[i] = exp_ftz(x[i] - base);   // (a weight below 2^-126 of the largest is 0)
   w.l += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
 }
-__device__ __forceinline__ void split_weights(const float *x, uint32_t (&h)[2], uint32_t (&l)[2]) {
+__device__ __forceinline__ void split_weights(const float *x, float up, uint32_t (&h)[2], uint32_t (&l)[2]) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const float a = x[2 * i] * kPScale, b = x[2 * i + 1] * kPScale;
+    const float a = x[2 * i] * up, b = x[2 * i + 1] * up;
     h[i] = pack_f16(a, b);
     l[i] = pack_f16(a - f16_lo_f(h[i]), b - f16_hi_f(h[i]));
   }
@@ -609,12 +637,14 @@ __device__ bool attn_split_quant(const AttnArgs &a, unsigned char *smem, bool in
           for (int k = 0; k < 4; ++k)
             if (2 * (lane & 3) + (k & 1) + 8 * (k >> 1) >= t[j].valid()) x[4 * j + k] = -INFINITY;
         }
-      softmax_pair<D>(x, w);
+      float up[2];
+      float2 back[2];
+      softmax_pair<D>(x, w, up, back);
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         uint32_t h[2], l[2];
-        split_weights(x + 4 * j, h, l);
-        page_values<D, I8>(vbuf + j * L::kPageBytes, t[j], h, l, w);
+        split_weights(x + 4 * j, up[j], h, l);
+        page_values<D, I8>(vbuf + j * L::kPageBytes, t[j], h, l, back[j], w);
       }
     }
     __syncwarp();

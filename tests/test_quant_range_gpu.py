@@ -129,3 +129,25 @@ def test_v_scales_near_the_smallest_normal(d, exponent):
     big, _ = attend_all(c, 32, q)
     big *= 2.0 ** -60
     assert (np.abs(out - big) <= 2.0 ** -22 * np.abs(big) + low).all() and np.abs(big).max() > 2.0 ** -122
+
+
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+@pytest.mark.parametrize("order", ["falling", "rising", "mixed"])
+def test_small_weights_of_pages_with_large_scales(order, kind):
+    """Blocks whose weights fall by e^-11 each while their V scales grow by 2^16 each count alike:
+    the V products keep a page's weights relative to that page's largest."""
+    rng = np.random.default_rng(53)
+    c = Cache([640, 640], 1, 64, kind, rng, G=4)
+    g, nb = 32, 20
+    step = {"falling": np.arange(nb) % 8, "rising": 7 - np.arange(nb) % 8, "mixed": rng.integers(0, 8, nb)}[order]
+    bias = np.tile(-11.0 * step, (2, 1)).astype(np.float32)
+    vs = c.vs.cpu().numpy()
+    for u in range(2):
+        pages = c.table[u, :nb * 2]
+        vs[pages] *= np.exp2(16.0 * np.repeat(step, 2) - 60).astype(np.float32)
+    c.vs.copy_(torch.as_tensor(vs))
+    q = torch.as_tensor(rng.normal(size=(2, 4, 64)).astype(np.float32), device="cuda").bfloat16()
+    out, _ = attend_all(c, g, q, bias)
+    for u in range(2):
+        want, _, S, R, A = definition(c, u, g, q, bias)
+        assert within(out[u], want, S, R, A, 64, nb * 2), u
