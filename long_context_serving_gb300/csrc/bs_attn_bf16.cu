@@ -23,10 +23,12 @@ bs_status launch_modes(const AttnArgs &a, bool step, const CUtensorMap &tk, cons
   const int units = a.dims.batch * a.dims.n_kv_heads;
   constexpr int kSmemMax = MmaLayout<D>::bytes(MmaLayout<D>::kRingMax) + kSmemAlignSlack;
   auto kernel = attn_mma_kernel<D, G>;
-  static const bool attrs_ok =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax) == cudaSuccess &&
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
-  if (!attrs_ok) return BS_ERR_CUDA;
+  static OncePerDevice attrs;
+  if (!attrs([&] {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax) == cudaSuccess &&
+               cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
+      }))
+    return BS_ERR_CUDA;
   const bool cluster = attn_mode(units, a.dims.max_gather_pages_per_unit) == kModeCluster;
   const int smem = MmaLayout<D>::bytes(attn_mma_ring(cluster)) + kSmemAlignSlack;
   const int splits = attn_grid_splits(units, a.dims.max_gather_pages_per_unit, attn_target_ctas(), a.min_split);

@@ -18,10 +18,12 @@ template <int D, int G>
 bs_status launch_modes(const AttnArgs &a, bool step, cudaStream_t cs) {
   constexpr int kSmem = FfmaLayout<D, G>::kBytes;
   auto kernel = attn_ffma_kernel<D, G>;
-  static const bool attrs_ok =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) == cudaSuccess &&
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
-  if (!attrs_ok) return BS_ERR_CUDA;
+  static OncePerDevice attrs;
+  if (!attrs([&] {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem) == cudaSuccess &&
+               cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
+      }))
+    return BS_ERR_CUDA;
   const int units = a.dims.batch * a.dims.n_kv_heads;
   const bool cluster = attn_mode(units, a.dims.max_gather_pages_per_unit) == kModeCluster;
   const int splits = attn_grid_splits(units, a.dims.max_gather_pages_per_unit, attn_target_ctas(), a.min_split);

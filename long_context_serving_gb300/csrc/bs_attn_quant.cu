@@ -30,7 +30,8 @@
 // of itself, or 2^-39 of the row's largest where that is more. bf16 queries enter as hi alone,
 // exact down to 2^-31 of the row's largest and within 2^-39 of it below. The weights of a page
 // enter in the same way, at the power of two of that page's largest weight: within 2^-22 of
-// themselves or 2^-38 of that largest, so that pages may differ in their V scales without limit.
+// themselves or 2^-38 of that largest, however the pages' V scales differ (down to weights of
+// 2^-112 of the warp's largest; those below keep fewer bits).
 // (One power for all pages, 21.7 us for the 128K batch below, would lose a page whose weights are
 // below 2^-38 of the largest, however large its V scale.) Sums are fp32; the scales are applied to
 // each page's product in fp32, so none can leave fp16's range.
@@ -41,7 +42,6 @@
 // page indices and first copies (3.8 us) before it and the workspace merge (3 us) after it.
 // Short calls are that chain: 8.3 us for 8 units of 32K, 4.0 us for one token.
 #include <algorithm>
-#include <atomic>
 
 #include "bs_attn_impl.cuh"
 #include "bs_attn_launch.cuh"
@@ -708,17 +708,12 @@ bs_status launch_quant(AttnArgs a, bool step, cudaStream_t cs) {
   }
   constexpr int smem = QuantLayout<D>::kBytes;
   auto kernel = attn_quant_kernel<D, I8, Q32>;
-  // (once per device: an attribute holds for the one that is current)
-  static std::atomic<uint64_t> set_on{0};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return BS_ERR_CUDA;
-  const uint64_t bit = dev < 64 ? 1ull << dev : 0;
-  if ((set_on.load(std::memory_order_relaxed) & bit) == 0) {
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
-      return BS_ERR_CUDA;
-    set_on.fetch_or(bit, std::memory_order_relaxed);
-  }
+  static OncePerDevice attrs;
+  if (!attrs([&] {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) == cudaSuccess &&
+               cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
+      }))
+    return BS_ERR_CUDA;
   const bool cluster = attn_mode(units, mg) == kModeCluster;
   int splits = attn_grid_splits(units, mg, attn_target_ctas(), a.min_split);
   // A cluster's merge costs more than a few pages: no more splits than leave each kMinSplit.

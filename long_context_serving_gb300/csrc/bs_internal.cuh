@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "bsattn.h"
 
 namespace bsi {
@@ -200,6 +202,23 @@ bs_status make_kv_tensor_maps(const bs_dims &d, const bs_kv &kv, CUtensorMap *tk
 // Dynamic shared memory is re-based to a 1024-byte boundary (the 128-byte swizzle
 // atom of TMA copies); kernels that need it allocate this much more.
 constexpr int kSmemAlignSlack = 1024;
+
+// A kernel attribute holds for the device that is current when it is set. One static object a
+// kernel: runs `set` (false: failed, to be tried again) once on each device; devices past the
+// 64th every time.
+struct OncePerDevice {
+  std::atomic<uint64_t> done{0};
+  template <class Set>
+  bool operator()(Set set) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return true;
+    if (!set()) return false;
+    done.fetch_or(bit, std::memory_order_relaxed);
+    return true;
+  }
+};
 
 inline bs_status launch_status() {
   return cudaGetLastError() == cudaSuccess ? BS_OK : BS_ERR_CUDA;

@@ -113,9 +113,11 @@ void launch_score(const bs_dims &dims, const void *q, const bs_head_cfg &cfg, co
   const int nbuf = tpc > 1 ? 2 : 1;
   const int smem = ScoreLayout<D, G>::bytes(nbuf);
   // (a failed attribute call shows up as a failed launch of the two-buffer size)
-  static const cudaError_t attr = cudaFuncSetAttribute(
-      score_kernel<D, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, ScoreLayout<D, G>::bytes(2));
-  (void)attr;
+  static OncePerDevice attrs;
+  attrs([] {
+    return cudaFuncSetAttribute(score_kernel<D, G>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                ScoreLayout<D, G>::bytes(2)) == cudaSuccess;
+  });
   const dim3 grid((max_tiles + tpc - 1) / tpc, units);
   score_kernel<D, G><<<grid, kScoreThreads, smem, cs>>>(dims, q, cfg, seq_lens, summ, reduce, scores, st, tpc);
 }

@@ -68,9 +68,12 @@ extern "C" bs_status bs_select_topk(const bs_dims *dims, const bs_head_cfg *cfg,
     return BS_ERR_INVALID_ARG;
   const int units = dims->batch * dims->n_kv_heads;
   const size_t smem = static_cast<size_t>(dims->max_blocks_per_unit) * 5;
-  static const cudaError_t attr = cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                       static_cast<int>(kMaxBlocks * 5));
-  if (attr != cudaSuccess) return BS_ERR_CUDA;
+  static OncePerDevice attrs;
+  if (!attrs([] {
+        return cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    static_cast<int>(kMaxBlocks * 5)) == cudaSuccess;
+      }))
+    return BS_ERR_CUDA;
   select_kernel<<<units, kSelThreads, (smem + 15) & ~size_t(15), reinterpret_cast<cudaStream_t>(stream)>>>(
       *dims, *cfg, seq_lens, scores, evict_logits, alive, sel_idx, sel_cnt, dev_status);
   return launch_status();

@@ -61,9 +61,12 @@ extern "C" bs_status bs_block_setdiff(const bs_dims *dims, const int32_t *prev_i
   if (dims->max_sel_per_unit > 24576) return BS_ERR_CAPACITY;  // two lists in shared memory
   const int units = dims->batch * dims->n_kv_heads;
   const size_t smem = static_cast<size_t>(dims->max_sel_per_unit) * 2 * sizeof(int32_t);
-  static const cudaError_t attr = cudaFuncSetAttribute(
-      setdiff_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(24576 * 2 * sizeof(int32_t)));
-  if (attr != cudaSuccess) return BS_ERR_CUDA;
+  static OncePerDevice attrs;
+  if (!attrs([] {
+        return cudaFuncSetAttribute(setdiff_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    static_cast<int>(24576 * 2 * sizeof(int32_t))) == cudaSuccess;
+      }))
+    return BS_ERR_CUDA;
   setdiff_kernel<<<units, kDiffThreads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(
       *dims, prev_idx, prev_cnt, cur_idx, cur_cnt, added, added_cnt, removed, removed_cnt, dev_status);
   return launch_status();

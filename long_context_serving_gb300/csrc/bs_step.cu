@@ -626,10 +626,12 @@ template <int D, int G>
 bs_status launch_step(const bs_dims &dims, const bs_kv &kv, const bs_head_cfg &cfg, const bs_step_io &io,
                       int reduce, cudaStream_t cs) {
   constexpr size_t kFrontMaxSmem = 200 * 1024;
-  static const bool attr_ok = cudaFuncSetAttribute(step_front_kernel<D, G>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   static_cast<int>(kFrontMaxSmem)) == cudaSuccess;
-  if (!attr_ok) return BS_ERR_CUDA;
+  static OncePerDevice front_attrs;
+  if (!front_attrs([] {
+        return cudaFuncSetAttribute(step_front_kernel<D, G>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    static_cast<int>(kFrontMaxSmem)) == cudaSuccess;
+      }))
+    return BS_ERR_CUDA;
   const int units = dims.batch * dims.n_kv_heads;
   const int mode = attn_mode(units, dims.max_gather_pages_per_unit);
   const bool lists = mode != kModeWorkspace;   // the attention reads page lists
@@ -645,12 +647,14 @@ bs_status launch_step(const bs_dims &dims, const bs_kv &kv, const bs_head_cfg &c
     // 1. scores in equal shares: the ring of nbuf score tiles, the queries and dot products,
     //    then the plan; nbuf 2 or 3, whichever gives more tiles in flight per SM
     //    (preferring more CTAs).
-    static const bool sc_ok = cudaFuncSetAttribute(step_score_balanced<D, G>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   static_cast<int>(kFrontMaxSmem)) == cudaSuccess &&
-                              cudaFuncSetAttribute(step_select_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   static_cast<int>(kFrontMaxSmem)) == cudaSuccess;
-    if (!sc_ok) return BS_ERR_CUDA;
+    static OncePerDevice apart_attrs;
+    if (!apart_attrs([] {
+          return cudaFuncSetAttribute(step_score_balanced<D, G>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      static_cast<int>(kFrontMaxSmem)) == cudaSuccess &&
+                 cudaFuncSetAttribute(step_select_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                      static_cast<int>(kFrontMaxSmem)) == cudaSuccess;
+        }))
+      return BS_ERR_CUDA;
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms <= 0)
