@@ -126,7 +126,8 @@ typedef struct {
 
 /* Paged KV cache: device pointers. k_scale and v_scale are the page scales of an 8-bit
  * cache (kv_dtype BS_E4M3 or BS_INT8; required there, v_scale not by
- * bs_build_block_summaries) and not looked at otherwise. */
+ * bs_build_block_summaries) and not read otherwise: a caller built when the struct ended at
+ * seq_lens may pass that. */
 typedef struct {
   const void *k_pool, *v_pool;
   const int32_t *page_table;

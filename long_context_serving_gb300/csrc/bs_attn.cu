@@ -14,7 +14,7 @@ bs_status launch_standalone(const bs_dims *dims, const void *q, const bs_kv *kv,
   AttnArgs a;
   a.dims = *dims;
   a.q = q;
-  a.kv = *kv;
+  a.kv = kv_of(*dims, kv);
   a.cfg = *cfg;
   a.sel_idx = sel_idx;
   a.sel_cnt = sel_cnt;

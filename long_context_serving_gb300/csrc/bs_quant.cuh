@@ -10,6 +10,16 @@ namespace bsi {
 
 __host__ __device__ __forceinline__ bool is_quant(int kv_dtype) { return kv_dtype == BS_E4M3 || kv_dtype == BS_INT8; }
 
+// The caller's struct; its scales, which it did not always have, are read for 8-bit caches only.
+inline bs_kv kv_of(const bs_dims &dims, const bs_kv *kv) {
+  bs_kv k{kv->k_pool, kv->v_pool, kv->page_table, kv->seq_lens, nullptr, nullptr};
+  if (is_quant(dims.kv_dtype)) {
+    k.k_scale = kv->k_scale;
+    k.v_scale = kv->v_scale;
+  }
+  return k;
+}
+
 // A load of data read once, from L2. (Neither ld.global.nc nor an L1 line: a kernel that is in
 // place before the work ahead of it has finished reads what that wrote.)
 __device__ __forceinline__ uint4 ld_stream16(const void *p) {

@@ -768,6 +768,6 @@ extern "C" bs_status bs_decode_step(const bs_dims *dims, const bs_kv *kv, const 
   if (dims->max_sel_per_unit > kStepMaxSel) return BS_ERR_CAPACITY;
   const int G = dims->n_q_heads / dims->n_kv_heads;
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  if (dims->head_dim == 128) return dispatch_g<128>(G, *dims, *kv, *cfg, *io, group_reduce, cs);
-  return dispatch_g<64>(G, *dims, *kv, *cfg, *io, group_reduce, cs);
+  if (dims->head_dim == 128) return dispatch_g<128>(G, *dims, kv_of(*dims, kv), *cfg, *io, group_reduce, cs);
+  return dispatch_g<64>(G, *dims, kv_of(*dims, kv), *cfg, *io, group_reduce, cs);
 }

@@ -79,18 +79,19 @@ extern "C" bs_status bs_build_block_summaries(const bs_dims *dims, const bs_kv *
   int gx = (max_new_tokens + 1 + warps - 1) / warps;
   if (gx > 4096) gx = 4096;
   const dim3 grid(gx, units);
+  const bs_kv k = kv_of(*dims, kv);
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
   if (quant && dims->head_dim == 128)
-    summaries_kernel<128, Code8><<<grid, kSumThreads, 0, cs>>>(*dims, *kv, *cfg, tok_begin, summaries, dev_status);
+    summaries_kernel<128, Code8><<<grid, kSumThreads, 0, cs>>>(*dims, k, *cfg, tok_begin, summaries, dev_status);
   else if (quant)
-    summaries_kernel<64, Code8><<<grid, kSumThreads, 0, cs>>>(*dims, *kv, *cfg, tok_begin, summaries, dev_status);
+    summaries_kernel<64, Code8><<<grid, kSumThreads, 0, cs>>>(*dims, k, *cfg, tok_begin, summaries, dev_status);
   else if (dims->head_dim == 128 && dims->kv_dtype == BS_BF16)
-    summaries_kernel<128, uint16_t><<<grid, kSumThreads, 0, cs>>>(*dims, *kv, *cfg, tok_begin, summaries, dev_status);
+    summaries_kernel<128, uint16_t><<<grid, kSumThreads, 0, cs>>>(*dims, k, *cfg, tok_begin, summaries, dev_status);
   else if (dims->head_dim == 128)
-    summaries_kernel<128, float><<<grid, kSumThreads, 0, cs>>>(*dims, *kv, *cfg, tok_begin, summaries, dev_status);
+    summaries_kernel<128, float><<<grid, kSumThreads, 0, cs>>>(*dims, k, *cfg, tok_begin, summaries, dev_status);
   else if (dims->kv_dtype == BS_BF16)
-    summaries_kernel<64, uint16_t><<<grid, kSumThreads, 0, cs>>>(*dims, *kv, *cfg, tok_begin, summaries, dev_status);
+    summaries_kernel<64, uint16_t><<<grid, kSumThreads, 0, cs>>>(*dims, k, *cfg, tok_begin, summaries, dev_status);
   else
-    summaries_kernel<64, float><<<grid, kSumThreads, 0, cs>>>(*dims, *kv, *cfg, tok_begin, summaries, dev_status);
+    summaries_kernel<64, float><<<grid, kSumThreads, 0, cs>>>(*dims, k, *cfg, tok_begin, summaries, dev_status);
   return launch_status();
 }

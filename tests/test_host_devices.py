@@ -168,3 +168,41 @@ def test_every_call_runs_on_every_device_of_a_process(tmp_path):
     r = run_host(tmp_path, DEVICES)
     assert r.returncode == 0, r.stdout + r.stderr
     assert int(r.stdout.split("launches ")[1].split()[0]) >= 5 * 4 * 5 * 7
+
+
+OLD_KV = RUNTIME + r"""
+#include <sys/mman.h>
+#include <unistd.h>
+#include <cstddef>
+// bs_kv as it was before it had scales, at the very end of readable memory.
+int main() {
+  const size_t page = sysconf(_SC_PAGESIZE), old = offsetof(bs_kv, k_scale);
+  char *m = (char *)mmap(nullptr, 2 * page, PROT_READ | PROT_WRITE, MAP_PRIVATE | MAP_ANONYMOUS, -1, 0);
+  if (m == MAP_FAILED || mprotect(m + page, page, PROT_NONE) != 0) return 2;
+  const bs_kv k = cache();
+  const bs_kv *kv = (const bs_kv *)std::memcpy(m + page - old, &k, old);
+  int fails = 0;
+  for (int type : {BS_BF16, BS_FP32})
+    for (int units : {4, 60}) {
+      const bs_dims d = dims_for(type, units, 600, 8000);
+      const bs_head_cfg c = cfg();
+      const size_t ws = bs_workspace_size(&d);
+      const bs_step_io io = step_io(ws);
+      fails += bs_build_block_summaries(&d, kv, &c, P(40), 1, (float *)P(21), P(36), nullptr) != BS_OK;
+      fails += bs_sparse_decode_attn(&d, P(20), kv, &c, P(27), P(28), nullptr, (float *)P(33), (float *)P(34), P(35), ws,
+                                     P(36), nullptr) != BS_OK;
+      fails += bs_sparse_decode_attn_noalloc(&d, P(20), kv, &c, P(27), P(28), nullptr, (float *)P(33), (float *)P(34),
+                                             P(36), nullptr) != BS_OK;
+      fails += bs_decode_step(&d, kv, &c, &io, BS_GROUP_MAX, nullptr) != BS_OK;
+    }
+  std::printf("fails %d\n", fails);
+  return fails != 0;
+}
+"""
+
+
+def test_a_bs_kv_without_scales_is_enough_for_other_caches(tmp_path):
+    """A program built when bs_kv ended at seq_lens passes 32 bytes: no more of them are read unless
+    the cache is 8-bit."""
+    r = run_host(tmp_path, OLD_KV)
+    assert r.returncode == 0, (r.returncode, r.stdout, r.stderr)
