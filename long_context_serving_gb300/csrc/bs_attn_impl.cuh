@@ -287,7 +287,7 @@ __device__ __forceinline__ int resolve_page(const UnitBlocks &ub, const bs_dims 
     report(st, BS_ERR_DEVICE_BOUNDS);
     return 0;
   }
-  const int phys = __ldg(pt + lp);
+  const int phys = __ldcg(pt + lp);
   if (phys < 0 || phys >= dims.n_pages) {
     report(st, BS_ERR_DEVICE_BOUNDS);
     return 0;
@@ -305,7 +305,7 @@ __device__ __forceinline__ float block_bias2(const float *bias, const bs_dims &d
     report(st, BS_ERR_DEVICE_BOUNDS);
     return -INFINITY;
   }
-  return __ldg(bias + static_cast<size_t>(u) * dims.max_blocks_per_unit + c) * kLog2e;
+  return __ldcg(bias + static_cast<size_t>(u) * dims.max_blocks_per_unit + c) * kLog2e;
 }
 
 // Output row of one head from an unnormalised state (o, m in log2 units, l): o / l and

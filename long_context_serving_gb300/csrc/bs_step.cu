@@ -16,7 +16,9 @@
 // unit's splits wait (bounded) until their unit's selection count is published.
 //
 // Both kernels are programmatic dependents of the work before them in the stream: they
-// read only the per-unit head configuration before waiting for it to finish.
+// read only the per-unit head configuration before waiting for it to finish. What that work
+// may have written (the page table, by a page call directly ahead) changes while they are in
+// place, so nothing here is read through ld.global.nc, which takes it for constant.
 #include <algorithm>
 
 #include "bs_attn_launch.cuh"
@@ -196,7 +198,7 @@ __device__ __forceinline__ void unit_select_publish(const bs_dims &dims, const b
             const int c = cur_sm[blk];
             const int lp = c * ppb + pb;
             if (c >= 0 && lp < n_lp && c * g + pb * kPage < T)
-              phys[j] = lp < pt_in_smem ? pt_sm[pt_lead + lp] : __ldg(pt_row + lp);
+              phys[j] = lp < pt_in_smem ? pt_sm[pt_lead + lp] : __ldcg(pt_row + lp);
           }
         }
 #pragma unroll

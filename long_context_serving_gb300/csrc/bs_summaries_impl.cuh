@@ -53,7 +53,7 @@ __device__ bool summary_update_warp(const KT *pool, const int32_t *pt, int64_t n
   // together; the adds stay in token order.
   for (int t0 = lo; t0 < hi;) {
     const int page_end = min(hi, (t0 / kPage + 1) * kPage);
-    const int phys = __ldg(pt + t0 / kPage);
+    const int phys = __ldcg(pt + t0 / kPage);
     if (phys < 0 || phys >= n_pages) return false;
     const KT *base = pool + static_cast<size_t>(phys) * kPage * D + lane * DPL;
     float v[kPage][DPL];
@@ -92,7 +92,7 @@ __device__ bool summary_update_warp_quant(const bs_dims &dims, const bs_kv &kv, 
   for (int i = 0; i < DPL; ++i) acc[i] = 0.0f;
   for (int t0 = lo; t0 < hi;) {
     const int page_end = min(hi, (t0 / kPage + 1) * kPage);
-    const int phys = __ldg(pt + t0 / kPage);
+    const int phys = __ldcg(pt + t0 / kPage);
     if (phys < 0 || phys >= dims.n_pages) return false;
     const float scale = kv.k_scale[phys];
     const uint8_t *base = static_cast<const uint8_t *>(kv.k_pool) + static_cast<size_t>(phys) * kPage * D + lane * DPL;
