@@ -505,7 +505,9 @@ bs_status bs_quant_append(const bs_dims *dims, const bs_pools *pools, const int3
  * map as it was (and *count = 0).
  * ------------------------------------------------------------------------------ */
 
-/* Device pointers; all in/out. */
+/* Device pointers; all in/out. A table entry is a page, or -1 for none; anything else lies
+ * outside the pool (reserve, which writes every entry that holds no page, puts a page in place
+ * of any below 0). */
 typedef struct {
   int32_t *page_table;  /* [units][max_pages_per_unit]: page of each logical page, -1 none */
   int32_t *ref_count;   /* [n_pages]: page-table entries that hold the page, >= 0 */

@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(kPgThreads) fork_scan(bs_dims dims, bs_page_ma
             for (int e = 0; e < kBatch; ++e) p[e] = j0 + e * kPgThreads < np ? from[j0 + e * kPgThreads] : -1;
 #pragma unroll
             for (int e = 0; e < kBatch; ++e)
-              if (p[e] >= 0 && (p[e] >= dims.n_pages || map.ref_count[p[e]] <= 0))
+              if (p[e] < -1 || (p[e] >= 0 && (p[e] >= dims.n_pages || map.ref_count[p[e]] <= 0)))
                 err = max(err, static_cast<int>(BS_ERR_DEVICE_BOUNDS));
           }
           if (T % kPage != 0 && from[T / kPage] >= 0) need = 1;
@@ -511,8 +511,8 @@ __global__ void __launch_bounds__(kPgThreads) free_kernel(bs_dims dims, bs_page_
       }
 #pragma unroll
       for (int e = 0; e < kFreeBatch; ++e)
-        if (had[e] <= 0) {
-          if (p[e] < dims.n_pages) atomicAdd(map.ref_count + p[e], 1);
+        if (had[e] <= 0 || p[e] < -1) {
+          if (p[e] >= 0 && p[e] < dims.n_pages) atomicAdd(map.ref_count + p[e], 1);
           report(st, BS_ERR_DEVICE_BOUNDS);
         }
     }
@@ -566,8 +566,8 @@ __global__ void __launch_bounds__(kPgThreads) compact_apply(bs_dims dims, bs_pag
   for (int64_t i = static_cast<int64_t>(blockIdx.x - move_ctas) * kPgThreads + threadIdx.x; i < total;
        i += static_cast<int64_t>(gridDim.x - move_ctas) * kPgThreads) {
     const int p = map.page_table[i];
-    if (p < N) continue;
-    if (p >= n_pages || is_free(p)) {
+    if (p >= -1 && p < N) continue;
+    if (p < 0 || p >= n_pages || is_free(p)) {
       report(st, BS_ERR_DEVICE_BOUNDS);
       continue;
     }
