@@ -192,9 +192,21 @@ def _ptr(t) -> int | None:
     return t.ctypes.data          # a numpy array (host memory)
 
 
+def _current_stream():
+    """A function for the raw handle of the current stream. The handle alone, through torch's own
+    internals where it has them: a Stream object takes longer than a call's launches."""
+    raw, device = (getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+    if raw is None or device is None:
+        return lambda: torch.cuda.current_stream().cuda_stream
+    return lambda: raw(device())
+
+
+_current = _current_stream()
+
+
 def _stream(stream) -> int | None:
-    if stream is None:   # the handle alone: a Stream object takes longer than a call's launches
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    if stream is None:
+        return _current()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
