@@ -273,12 +273,13 @@ __device__ __forceinline__ void page_values(const unsigned char *slot, const Pag
   }
 }
 
-// exp(x) as 2^(x log2 e), results below 2^-126 as 0.
-__device__ __forceinline__ float exp_ftz(float x) {
+// 2^x, results below 2^-126 as 0; exp(x) as 2^(x log2 e).
+__device__ __forceinline__ float exp2_ftz(float x) {
   float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * kLog2e));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float exp_ftz(float x) { return exp2_ftz(x * kLog2e); }
 
 // Online softmax of this lane's head over the 32 tokens of two pages: x becomes the weights
 // exp(x - m), the running state is rescaled when the maximum rises.
@@ -325,15 +326,20 @@ __device__ __forceinline__ void softmax_pair(float (&x)[8], WarpState<D> &w, flo
   back[0] = make_float2(__uint_as_float(f0 << 23), __uint_as_float(f1 << 23));
   back[1] = make_float2(__uint_as_float(f0 << 7 & 0x7f800000u), __uint_as_float(f1 << 7 & 0x7f800000u));
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = exp_ftz(x[i] - base);   // (a weight below 2^-126 of the largest is 0)
+  for (int i = 0; i < 8; i += 2) {   // (a weight below 2^-126 of the largest is 0)
+    const float2 y = __fmul2_rn(__fadd2_rn(make_float2(x[i], x[i + 1]), make_float2(-base, -base)), make_float2(kLog2e, kLog2e));
+    x[i] = exp2_ftz(y.x);
+    x[i + 1] = exp2_ftz(y.y);
+  }
   w.l += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
 }
 __device__ __forceinline__ void split_weights(const float *x, float up, uint32_t (&h)[2], uint32_t (&l)[2]) {
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
-    const float a = x[2 * i] * up, b = x[2 * i + 1] * up;
-    h[i] = pack_f16(a, b);
-    l[i] = pack_f16(a - f16_lo_f(h[i]), b - f16_hi_f(h[i]));
+    const float2 a = __fmul2_rn(make_float2(x[2 * i], x[2 * i + 1]), make_float2(up, up));
+    h[i] = pack_f16(a.x, a.y);
+    const float2 rest = __fadd2_rn(a, make_float2(-f16_lo_f(h[i]), -f16_hi_f(h[i])));
+    l[i] = pack_f16(rest.x, rest.y);
   }
 }
 
