@@ -240,7 +240,8 @@ bs_status bs_select_topk(const bs_dims *dims, const bs_head_cfg *cfg, const int3
  * 8-bit caches: K[t] and V[t] are codes times their page's scale. Codes are exact in
  * fp16; queries and weights enter as fp16 parts hi + lo, a query element within 2^-22 of
  * itself or 2^-39 of its row's largest element, a weight within 2^-22 of itself or 2^-38
- * of its page's largest weight; sums and scales are fp32, whatever the scales. A
+ * of its page's largest weight (a page whose largest is below 2^-112 of the unit's: 2^-150
+ * of the unit's); sums and scales are fp32, whatever the scales. A
  * page whose block logit is -inf is not read; NaN codes in tokens past T do not count.
  * Their splits differ from the above: in cluster mode S is halved while a selection of
  * max_gather_pages_per_unit would leave a split fewer than 8 pages; in workspace mode up

@@ -224,10 +224,10 @@ __device__ __forceinline__ void page_scores(const unsigned char *slot, const Pag
 }
 
 // O^T += vs V8^T P^T of the page in `slot` (h, l: the page's weights at their power of two as
-// fp16 pairs, hi and lo; back: its reciprocal for heads 2 c and 2 c + 1). The products come back to their
-// size before the V scale enters: the two together may be subnormal. Two-wide fp32 makes that
-// free (the multiplication and the addition take the issue slots of one-wide additions). Codes
-// of tokens that do not count may be anything (NaN too) and are zeroed.
+// fp16 pairs, hi and lo; back: its reciprocal for heads 2 c and 2 c + 1). The products come back
+// to their size before the V scale enters: the two together may be subnormal. Two-wide fp32
+// makes that free (the multiplication and the addition take the issue slots of one-wide
+// additions). Codes of tokens that do not count may be anything (NaN too) and are zeroed.
 template <int D, bool I8>
 __device__ __forceinline__ void page_values(const unsigned char *slot, const PageMeta &t, const uint32_t (&h)[2],
                                             const uint32_t (&l)[2], float2 back, WarpState<D> &w) {
@@ -327,7 +327,8 @@ __device__ __forceinline__ void softmax_pair(float (&x)[8], WarpState<D> &w, flo
   back[1] = make_float2(__uint_as_float(f0 << 7 & 0x7f800000u), __uint_as_float(f1 << 7 & 0x7f800000u));
 #pragma unroll
   for (int i = 0; i < 8; i += 2) {   // (a weight below 2^-126 of the largest is 0)
-    const float2 y = __fmul2_rn(__fadd2_rn(make_float2(x[i], x[i + 1]), make_float2(-base, -base)), make_float2(kLog2e, kLog2e));
+    const float2 less = __fadd2_rn(make_float2(x[i], x[i + 1]), make_float2(-base, -base));
+    const float2 y = __fmul2_rn(less, make_float2(kLog2e, kLog2e));
     x[i] = exp2_ftz(y.x);
     x[i + 1] = exp2_ftz(y.y);
   }
