@@ -21,6 +21,13 @@
  *                             cache (BS_E4M3 or BS_INT8 codes, one scale per page)
  *   bs_pages_reserve, _fork,  pages of a cache handed out, shared between sequences,
  *   _free, _compact, _copy    taken back, and moved together, all on the device
+ *   bs_rope_append            queries and keys normalised per head and rotated to their
+ *                             positions; K and V written into the cache's pages
+ *   bs_prefill_attn           attention of new prompt tokens (or of single tokens) over
+ *                             the cache that holds them: dense, or sinks and a window
+ *   bs_tree_decode_attn       attention of a tree of drafted tokens over the selected
+ *                             blocks and their ancestors
+ *   bs_tree_commit            the accepted drafts' K and V appended to the cache
  *
  * Method sources: "Technisches Resümee: NOSA: Native und Offloadable Sparse
  * Attention" (section Methodik: "1. Algorithmus: NOSA" and "2. System: NOSI") and
@@ -578,6 +585,144 @@ bs_status bs_pages_compact(const bs_dims *dims, const bs_page_map *map, const bs
  * launch. */
 bs_status bs_pages_copy(const bs_dims *dims, const bs_pools *pools, const bs_page_copies *copies, int32_t *dev_status,
                         bs_stream_t stream);
+
+/* ------------------------------------------------------------------------------
+ * Prompts and drafted tokens. bs_rope_append turns a projection's rows into queries and
+ * keys; bs_prefill_attn attends new tokens to the cache that holds them; a tree of drafts
+ * is attended by bs_tree_decode_attn while its K and V stay outside the cache, and
+ * bs_tree_commit appends those that were accepted. (A draft enters no page before it is
+ * accepted: pages may be shared, and a page scale of an 8-bit cache only grows.)
+ * Rows. New tokens of all sequences are packed rows; those of sequence b start at row
+ * row_begin[b]. A row holds the heads of one token; row_stride (elements) lets q, k and v
+ * be columns of one fused projection's output. Rows that belong to no sequence are
+ * neither read for a result nor written.
+ * ------------------------------------------------------------------------------ */
+
+/* Norm and rotation of queries and keys (host struct; device pointers). Pair i, i <
+ * rot_dim / 2, of a head at position p turns by the angle p * inv_freq[i]; its elements are
+ * i and i + rot_dim / 2, or 2i and 2i + 1 (interleaved). Elements from rot_dim on are not
+ * rotated. */
+typedef struct {
+  const double *inv_freq;  /* [rot_dim / 2], radians a position, finite */
+  int32_t rot_dim;         /* 16 .. head_dim, a multiple of 16 */
+  int32_t interleaved;     /* 0 or 1 */
+  float magnitude;         /* cosines and sines are multiplied by it (1: a plain rotation) */
+  const float *q_weight, *k_weight;  /* norm weights [head_dim], or NULL: no norm of queries / keys */
+  float eps;               /* >= 0, finite */
+} bs_rope;
+
+/* For each row r and each query or key head x of it, in fp32:
+ *   x' = x * rsqrt(mean(x^2) + eps) * weight (x where the weight is NULL);
+ *   (a, b) of each pair -> m (a cos - b sin), m (b cos + a sin), m = magnitude;
+ * rounded once, to q_dtype in q_out and k_out, to kv_dtype in the cache. The angle keeps
+ * its fraction of a turn to 2^-24 whatever the position (below 2^24).
+ * q rows: n_q_heads * head_dim elements at q + r * row_stride; k and v rows likewise with
+ * n_kv_heads. positions int32 [n_rows], 0 .. 2^24 - 1. row_seq int32 [n_rows]: the row's
+ * sequence, < 0 for a padding row, which is skipped; NULL (only without pools): no
+ * padding. q_out [n_rows][n_q_heads][head_dim], k_out [n_rows][n_kv_heads][head_dim],
+ * q_dtype, packed, 16-byte aligned, apart from the inputs.
+ * With pools (kv_dtype BS_BF16 or BS_FP32; k_scale and v_scale not read) the rotated K and
+ * the V of a row go to slot position % 16 of the page that page_table names for position /
+ * 16 in the row's sequence; no two rows may name one slot. k_out may then be NULL. With
+ * pools NULL, k_out takes the keys, and v and page_table are not read (8-bit caches: follow
+ * with bs_quant_append; drafts: nothing is written to the cache yet).
+ * A row whose position is outside the range is skipped (BS_ERR_INVALID_ARG), and so is one
+ * whose row_seq >= batch (BS_ERR_DEVICE_BOUNDS) or whose position lies past the page table's
+ * row (BS_ERR_CAPACITY); a page outside the pool: that head's K and V are not written
+ * (BS_ERR_DEVICE_BOUNDS). One launch. */
+bs_status bs_rope_append(const bs_dims *dims, const bs_rope *rope, const void *q, const void *k, const void *v,
+                         int64_t row_stride, int64_t n_rows, const int32_t *positions, const int32_t *row_seq,
+                         const bs_pools *pools, const int32_t *page_table, void *q_out, void *k_out,
+                         int32_t *dev_status, bs_stream_t stream);
+
+/* Attention of new tokens over the cache that already holds them. Token p of sequence b,
+ * tok_begin[b] <= p < seq_lens[b] (kv->seq_lens), is row row_begin[b] + p - tok_begin[b] of
+ * q, out and lse. Over the tokens t of its unit that it sees:
+ *   out_h = sum_t softmax_t(x_h(t)) V[t],  lse_h = log sum_t exp(x_h(t)),  x_h(t) = q_h . K[t] / sqrt(d);
+ * it sees every t <= p (retrieval and dual units), or the t <= p with t < sink_tokens or
+ * t > p - local_tokens (streaming units: token for token, where selections cover both by
+ * whole blocks). A chunk may be a whole prompt, a piece of one behind a cached prefix, or
+ * one token; tok_begin[b] = seq_lens[b] has none for b.
+ * q_dtype BS_BF16; kv_dtype BS_BF16, BS_E4M3 or BS_INT8 (BS_ERR_INVALID_ARG otherwise).
+ * q: n_rows rows of q_stride elements, 16-byte aligned, q_stride a multiple of 8 and at least
+ * n_q_heads * head_dim. out bf16 [n_rows][n_q_heads][head_dim], 16-byte aligned; lse fp32
+ * [n_rows][n_q_heads], or NULL. Of cfg: cls, sink_tokens and local_tokens.
+ * Weights are rounded to bf16 (relative to a running maximum, at most 2^-9 each) before they
+ * meet V; logits, maxima, sums and outputs are fp32 until out's own rounding. A row that is
+ * not finite after that is computed again in fp32 throughout, without its unseen keys, so
+ * that an infinity or a NaN of a key it does not see cannot reach it.
+ * max_new_tokens (host): an upper bound on seq_lens[b] - tok_begin[b]. It and n_rows size the
+ * grid and choose the splits of long rows, and so the order of sums; a row's result does not
+ * depend on what other sequences hold.
+ * workspace: bs_prefill_workspace_size bytes, 16-byte aligned, overwritten by every call,
+ * needs no clearing (NULL when the size is 0). Calls that share one must not run
+ * concurrently.
+ * A sequence whose lengths or rows do not fit is skipped: tok_begin < 0 or above seq_lens
+ * (BS_ERR_INVALID_ARG); more tokens than max_new_tokens or more pages than a row
+ * (BS_ERR_CAPACITY); rows outside [0, n_rows) (BS_ERR_DEVICE_BOUNDS). A unit with a bad head
+ * configuration is skipped (BS_ERR_INVALID_ARG); a page outside the pool is left out
+ * (BS_ERR_DEVICE_BOUNDS). Sequences may not share rows. One launch, two where rows are
+ * split. */
+bs_status bs_prefill_attn(const bs_dims *dims, const void *q, int64_t q_stride, int64_t n_rows, const bs_kv *kv,
+                          const bs_head_cfg *cfg, const int32_t *tok_begin, const int32_t *row_begin,
+                          int32_t max_new_tokens, void *out, float *lse, void *workspace, size_t workspace_bytes,
+                          int32_t *dev_status, bs_stream_t stream);
+
+/* Bytes of workspace bs_prefill_attn needs (0 on bad arguments, or when it needs none). */
+size_t bs_prefill_workspace_size(const bs_dims *dims, int64_t n_rows, int32_t max_new_tokens);
+
+/* Largest tree of drafts of one sequence. */
+#define BS_MAX_DRAFT 64
+
+/* Drafted tokens (device pointers but for the sizes). Draft i of sequence b, i < n_draft[b],
+ * is row row_begin[b] + i of k_new, v_new (n_rows rows of row_stride elements, bf16, KV head
+ * h at [h * head_dim, (h + 1) * head_dim)) and of visible, whose bit j says that draft i
+ * attends draft j of the same sequence (its ancestors and itself; bits from n_draft[b] on do
+ * not count). */
+typedef struct {
+  const void *k_new, *v_new;    /* 16-byte aligned */
+  int64_t row_stride, n_rows;   /* row_stride: a multiple of 8, >= n_kv_heads * head_dim */
+  const int32_t *row_begin;     /* [batch] */
+  const int32_t *n_draft;       /* [batch], 0 .. max_draft */
+  const uint64_t *visible;      /* [n_rows] */
+  int32_t max_draft;            /* host value: 1 .. BS_MAX_DRAFT */
+} bs_drafts;
+
+/* Attention of a tree of drafted tokens: bs_sparse_decode_attn for every draft at once. Draft
+ * i of sequence b attends, with each query head h of a unit, the tokens t < T of the unit's
+ * selected blocks (sel_idx, sel_cnt; T = kv->seq_lens[b], which does not count the drafts) and
+ * the drafts j that visible names; out_h and lse_h as there, without block logits. A row that
+ * sees nothing gets zeros and lse = -inf. q, out, lse, types, rounding and non-finite keys as
+ * for bs_prefill_attn; rows are the drafts'. Of cfg: block_tokens. T may be 0 (no cache yet).
+ * Selections are those of bs_select_topk (for the root's query, say): ascending, at most
+ * max_sel_per_unit blocks and max_gather_pages_per_unit pages (BS_ERR_CAPACITY).
+ * workspace: bs_tree_workspace_size bytes, under the rules of bs_prefill_attn's.
+ * Skipped: a sequence with n_draft outside 0 .. max_draft or T < 0 (BS_ERR_INVALID_ARG), rows outside
+ * [0, n_rows) (BS_ERR_DEVICE_BOUNDS) or more pages than a row (BS_ERR_CAPACITY); a unit whose
+ * block_tokens is not a positive multiple of 16 (BS_ERR_INVALID_ARG). A block or page out of
+ * range is left out (BS_ERR_DEVICE_BOUNDS). One launch, two where rows are split. */
+bs_status bs_tree_decode_attn(const bs_dims *dims, const void *q, int64_t q_stride, const bs_kv *kv,
+                              const bs_head_cfg *cfg, const int32_t *sel_idx, const int32_t *sel_cnt,
+                              const bs_drafts *drafts, void *out, float *lse, void *workspace,
+                              size_t workspace_bytes, int32_t *dev_status, bs_stream_t stream);
+
+/* Bytes of workspace bs_tree_decode_attn needs (0 on bad arguments, or when it needs none). */
+size_t bs_tree_workspace_size(const bs_dims *dims, int32_t max_draft);
+
+/* Appends the accepted drafts. Token t of sequence b, tok_begin[b] <= t < seq_lens[b], is row
+ * row_begin[b] + path[b][t - tok_begin[b]] of k_new and v_new (layout and types as for
+ * bs_quant_append); it goes to slot t % 16 of the page that page_table names for t / 16: by
+ * the rule of bs_quant_append into an 8-bit cache, rounded to kv_dtype into a BS_BF16 or
+ * BS_FP32 one. path int32 [batch][path_stride], 1 <= path_stride <= BS_MAX_DRAFT; entries past
+ * the accepted ones are not read. tok_begin, seq_lens as for bs_quant_append: seq_lens counts
+ * the accepted tokens already, so that one path and one pair of lengths serve every layer.
+ * Errors as for bs_quant_append; a sequence with more tokens than path_stride
+ * (BS_ERR_CAPACITY) or a path entry whose row is outside [0, n_rows) (BS_ERR_DEVICE_BOUNDS) is
+ * skipped. One launch; bitwise reproducible. */
+bs_status bs_tree_commit(const bs_dims *dims, const bs_pools *pools, const int32_t *page_table,
+                         const int32_t *seq_lens, const int32_t *tok_begin, const int32_t *row_begin,
+                         const int32_t *path, int32_t path_stride, const void *k_new, const void *v_new,
+                         int64_t row_stride, int64_t n_rows, int32_t *dev_status, bs_stream_t stream);
 
 /* Bytes of workspace bs_sparse_decode_attn needs for these dims (0 on bad dims). */
 size_t bs_workspace_size(const bs_dims *dims);

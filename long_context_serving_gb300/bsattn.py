@@ -29,6 +29,7 @@ BS_ERR_TIMEOUT = 7
 BS_BF16, BS_FP32, BS_E4M3, BS_INT8 = 0, 1, 2, 3
 BS_STREAMING, BS_RETRIEVAL, BS_DUAL = 0, 1, 2
 BS_GROUP_MAX, BS_GROUP_MEAN = 0, 1
+BS_MAX_DRAFT = 64
 
 
 class Dims(ctypes.Structure):
@@ -91,6 +92,18 @@ class PageCopies(ctypes.Structure):
     _fields_ = [("pairs", ctypes.c_void_p), ("count", ctypes.c_void_p), ("capacity", ctypes.c_int32)]
 
 
+class Rope(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("magnitude", ctypes.c_float), ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+                ("eps", ctypes.c_float)]
+
+
+class Drafts(ctypes.Structure):
+    _fields_ = [("k_new", ctypes.c_void_p), ("v_new", ctypes.c_void_p), ("row_stride", ctypes.c_int64),
+                ("n_rows", ctypes.c_int64), ("row_begin", ctypes.c_void_p), ("n_draft", ctypes.c_void_p),
+                ("visible", ctypes.c_void_p), ("max_draft", ctypes.c_int32)]
+
+
 class BsError(RuntimeError):
     def __init__(self, call: str, status: int, text: str):
         super().__init__(f"{call} returned {status} ({text})")
@@ -139,6 +152,24 @@ _SIGS = {
     "bs_pages_compact": (ctypes.c_int, [_P(Dims), _P(PageMap), _P(PageCopies), ctypes.c_void_p, ctypes.c_void_p,
                                         ctypes.c_size_t, ctypes.c_void_p, ctypes.c_void_p]),
     "bs_pages_copy": (ctypes.c_int, [_P(Dims), _P(Pools), _P(PageCopies), ctypes.c_void_p, ctypes.c_void_p]),
+    "bs_rope_append": (ctypes.c_int, [_P(Dims), _P(Rope), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                      ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p, ctypes.c_void_p, _P(Pools),
+                                      ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                      ctypes.c_void_p]),
+    "bs_prefill_attn": (ctypes.c_int, [_P(Dims), ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64, _P(KV), _P(HeadCfg),
+                                       ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
+                                       ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p,
+                                       ctypes.c_void_p]),
+    "bs_prefill_workspace_size": (ctypes.c_size_t, [_P(Dims), ctypes.c_int64, ctypes.c_int32]),
+    "bs_tree_decode_attn": (ctypes.c_int, [_P(Dims), ctypes.c_void_p, ctypes.c_int64, _P(KV), _P(HeadCfg),
+                                           ctypes.c_void_p, ctypes.c_void_p, _P(Drafts), ctypes.c_void_p,
+                                           ctypes.c_void_p, ctypes.c_void_p, ctypes.c_size_t, ctypes.c_void_p,
+                                           ctypes.c_void_p]),
+    "bs_tree_workspace_size": (ctypes.c_size_t, [_P(Dims), ctypes.c_int32]),
+    "bs_tree_commit": (ctypes.c_int, [_P(Dims), _P(Pools), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                      ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p,
+                                      ctypes.c_void_p, ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p,
+                                      ctypes.c_void_p]),
     "bs_workspace_size": (ctypes.c_size_t, [_P(Dims)]),
     "bs_decode_step_launches": (ctypes.c_int, [_P(Dims)]),
     "bs_set_wait_limit_ns": (ctypes.c_int, [ctypes.c_uint64]),
@@ -339,6 +370,53 @@ def pages_copy(dims, pools: Pools, copies: PageCopies, dev_status, stream=None):
     _check("bs_pages_copy",
            lib().bs_pages_copy(ctypes.byref(dims), ctypes.byref(pools), ctypes.byref(copies), _ptr(dev_status),
                                _stream(stream)))
+
+
+def rope_append(dims, rope: Rope, q, k, v, row_stride: int, n_rows: int, positions, row_seq, pools, page_table, q_out,
+                k_out, dev_status, stream=None):
+    """Queries and keys normalised per head and rotated; with pools, K and V written into their pages."""
+    _check("bs_rope_append",
+           lib().bs_rope_append(ctypes.byref(dims), ctypes.byref(rope), _ptr(q), _ptr(k), _ptr(v), int(row_stride),
+                                int(n_rows), _ptr(positions), _ptr(row_seq),
+                                None if pools is None else ctypes.byref(pools), _ptr(page_table), _ptr(q_out),
+                                _ptr(k_out), _ptr(dev_status), _stream(stream)))
+
+
+def prefill_attn(dims, q, q_stride: int, n_rows: int, kv, cfg, tok_begin, row_begin, max_new_tokens: int, out, lse,
+                 workspace, dev_status, stream=None):
+    """New tokens attend the cache that holds them: everything before them, or sinks and a window."""
+    _check("bs_prefill_attn",
+           lib().bs_prefill_attn(ctypes.byref(dims), _ptr(q), int(q_stride), int(n_rows), ctypes.byref(kv),
+                                 ctypes.byref(cfg), _ptr(tok_begin), _ptr(row_begin), int(max_new_tokens), _ptr(out),
+                                 _ptr(lse), _ptr(workspace), 0 if workspace is None else _nbytes(workspace),
+                                 _ptr(dev_status), _stream(stream)))
+
+
+def tree_decode_attn(dims, q, q_stride: int, kv, cfg, sel_idx, sel_cnt, drafts: Drafts, out, lse, workspace, dev_status,
+                     stream=None):
+    """A tree of drafted tokens attends the selected blocks and its own ancestors."""
+    _check("bs_tree_decode_attn",
+           lib().bs_tree_decode_attn(ctypes.byref(dims), _ptr(q), int(q_stride), ctypes.byref(kv), ctypes.byref(cfg),
+                                     _ptr(sel_idx), _ptr(sel_cnt), ctypes.byref(drafts), _ptr(out), _ptr(lse),
+                                     _ptr(workspace), 0 if workspace is None else _nbytes(workspace),
+                                     _ptr(dev_status), _stream(stream)))
+
+
+def tree_commit(dims, pools: Pools, page_table, seq_lens, tok_begin, row_begin, path, path_stride: int, k_new, v_new,
+                row_stride: int, n_rows: int, dev_status, stream=None):
+    """The accepted drafts' K and V, along a path through each tree, appended to the cache."""
+    _check("bs_tree_commit",
+           lib().bs_tree_commit(ctypes.byref(dims), ctypes.byref(pools), _ptr(page_table), _ptr(seq_lens),
+                                _ptr(tok_begin), _ptr(row_begin), _ptr(path), int(path_stride), _ptr(k_new),
+                                _ptr(v_new), int(row_stride), int(n_rows), _ptr(dev_status), _stream(stream)))
+
+
+def prefill_workspace_size(dims, n_rows: int, max_new_tokens: int) -> int:
+    return int(lib().bs_prefill_workspace_size(ctypes.byref(dims), int(n_rows), int(max_new_tokens)))
+
+
+def tree_workspace_size(dims, max_draft: int) -> int:
+    return int(lib().bs_tree_workspace_size(ctypes.byref(dims), int(max_draft)))
 
 
 def pages_workspace_size(dims) -> int:

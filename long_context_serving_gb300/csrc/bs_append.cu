@@ -10,6 +10,7 @@
 // sequences of 8 heads: 2.9 us; one chain of lengths -> page index -> rows and old scale).
 #include "bs_attn_launch.cuh"
 #include "bs_quant.cuh"
+#include "bs_rows.cuh"
 
 namespace bsi {
 namespace {
@@ -27,7 +28,36 @@ struct AppendArgs {
   const void *k_new, *v_new;
   int64_t row_stride, n_rows;
   int32_t *st;
+  const int32_t *path;   // bs_tree_commit: [batch][path_stride], the row of each new token; else null
+  int32_t path_stride;
 };
+
+// The new tokens of a sequence. False: nothing to do (none, or they do not fit, which `first`
+// reports). All lanes of a warp call it together.
+template <bool kPath>
+__device__ __forceinline__ bool new_tokens(const AppendArgs &a, int b, bool first, int &T, int &t_begin, int64_t &row0) {
+  T = a.seq_lens[b];
+  t_begin = a.tok_begin[b];
+  row0 = a.row_begin[b];
+  int bad = 0;
+  if (t_begin < 0 || T < t_begin) bad = BS_ERR_INVALID_ARG;
+  else if (t_begin == T) return false;
+  else if ((static_cast<int64_t>(T) + kPage - 1) / kPage > a.dims.max_pages_per_unit) bad = BS_ERR_CAPACITY;
+  else if (kPath && T - t_begin > a.path_stride) bad = BS_ERR_CAPACITY;
+  else if (row0 < 0 || row0 + (kPath ? 0 : T - t_begin) > a.n_rows) bad = BS_ERR_DEVICE_BOUNDS;
+  if constexpr (kPath) {
+    if (bad == 0) {
+      bool out = false;
+      for (int i = threadIdx.x & 31; i < T - t_begin; i += 32) {
+        const int node = a.path[static_cast<int64_t>(b) * a.path_stride + i];
+        out |= node < 0 || row0 + node >= a.n_rows;
+      }
+      if (__any_sync(0xffffffffu, out)) bad = BS_ERR_DEVICE_BOUNDS;
+    }
+  }
+  if (bad != 0 && first) report(a.st, bad);
+  return bad == 0;
+}
 
 // Scale of a page whose largest finite magnitude is a.
 template <bool I8>
@@ -128,7 +158,8 @@ struct Encoder {
 // Eight CTAs an SM for bf16 rows: 64 registers, at d = 128 with 40 bytes of them spilled a
 // thread; seven CTAs (72 registers, 12 bytes spilled) took 65.9 us for the prompts above, six
 // 68.1. fp32 rows are twice the registers (166 at d = 128, none spilled); not timed.
-template <int D, bool I8, bool Q32>
+// kPath: new tokens' rows are those that the path names (bs_tree_commit).
+template <int D, bool I8, bool Q32, bool kPath>
 __global__ void __launch_bounds__(kAppendThreads, Q32 ? (D == 128 ? 3 : 5) : 8) append_kernel(const __grid_constant__ AppendArgs a, int per_warp) {
   constexpr int kLanesPerRow = D / 8;              // 8 dimensions a lane
   constexpr int kRowsPerIter = 32 / kLanesPerRow;
@@ -138,22 +169,9 @@ __global__ void __launch_bounds__(kAppendThreads, Q32 ? (D == 128 ? 3 : 5) : 8) 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();      // everything before this call has finished
   pdl_trigger();
-  const int T = a.seq_lens[b], t_begin = a.tok_begin[b];
-  const int64_t row0 = a.row_begin[b];
-  const bool first_thread = blockIdx.y == 0 && threadIdx.x == 0;
-  if (t_begin < 0 || T < t_begin) {
-    if (first_thread) report(a.st, BS_ERR_INVALID_ARG);
-    return;
-  }
-  if (t_begin == T) return;
-  if ((static_cast<int64_t>(T) + kPage - 1) / kPage > dims.max_pages_per_unit) {
-    if (first_thread) report(a.st, BS_ERR_CAPACITY);
-    return;
-  }
-  if (row0 < 0 || row0 + (T - t_begin) > a.n_rows) {
-    if (first_thread) report(a.st, BS_ERR_DEVICE_BOUNDS);
-    return;
-  }
+  int T, t_begin;
+  int64_t row0;
+  if (!new_tokens<kPath>(a, b, blockIdx.y == 0 && threadIdx.x == 0, T, t_begin, row0)) return;
   const int lp0 = t_begin / kPage;
   const int64_t n_items = 2ll * ((T - 1) / kPage - lp0 + 1);
   const int sub = lane / kLanesPerRow, col = lane % kLanesPerRow;
@@ -178,8 +196,9 @@ __global__ void __launch_bounds__(kAppendThreads, Q32 ? (D == 128 ? 3 : 5) : 8) 
     uint4 raw[kIters][kVecs];
     const int64_t first = row0 + (base - t_begin);                       // row of slot 0
     const char *src = static_cast<const char *>(is_v ? a.v_new : a.k_new) +
-                      ((first + sub) * a.row_stride + static_cast<int64_t>(h) * D + col * 8) * (Q32 ? 4 : 2);
+                      ((kPath ? row0 : first + sub) * a.row_stride + static_cast<int64_t>(h) * D + col * 8) * (Q32 ? 4 : 2);
     const int64_t step = kRowsPerIter * a.row_stride * (Q32 ? 4 : 2);
+    const int32_t *nodes = kPath ? a.path + static_cast<int64_t>(b) * a.path_stride + (base - t_begin) : nullptr;   // of slot 0
 #pragma unroll
     for (int i = 0; i < kIters; ++i) {
       const int slot = i * kRowsPerIter + sub;
@@ -187,7 +206,8 @@ __global__ void __launch_bounds__(kAppendThreads, Q32 ? (D == 128 ? 3 : 5) : 8) 
       for (int j = 0; j < kVecs; ++j) raw[i][j] = make_uint4(0u, 0u, 0u, 0u);
       if (slot >= s0 && slot < s1) {
 #pragma unroll
-        for (int j = 0; j < kVecs; ++j) raw[i][j] = ld_stream16(src + i * step + 16 * j);
+        for (int j = 0; j < kVecs; ++j)
+          raw[i][j] = ld_stream16(src + (kPath ? nodes[slot] * a.row_stride * (Q32 ? 4 : 2) : i * step) + 16 * j);
       }
     }
     auto values = [&](int i, float (&x)[8]) {
@@ -262,9 +282,38 @@ __global__ void __launch_bounds__(kAppendThreads, Q32 ? (D == 128 ? 3 : 5) : 8) 
   }
 }
 
+// Into a cache that is not quantised (bs_tree_commit): eight elements a thread, one CTA a unit.
+// A few rows; the launch and one chain of loads (lengths, path entry, page and row) are its time.
+template <int D, bool Q32, bool C32>
+__global__ void __launch_bounds__(kAppendThreads) commit_rows_kernel(const __grid_constant__ AppendArgs a) {
+  constexpr int kVecs = D / 8;
+  const int u = blockIdx.x, b = u / a.dims.n_kv_heads, h = u % a.dims.n_kv_heads;
+  pdl_wait();      // everything before this call has finished
+  pdl_trigger();
+  int T, t_begin;
+  int64_t row0;
+  if (!new_tokens<true>(a, b, threadIdx.x == 0, T, t_begin, row0)) return;
+  const int32_t *pt = a.page_table + static_cast<size_t>(u) * a.dims.max_pages_per_unit;
+  for (int i = threadIdx.x; i < (T - t_begin) * 2 * kVecs; i += kAppendThreads) {
+    const int n = i / (2 * kVecs), at = i % kVecs, t = t_begin + n;
+    const bool is_v = (i / kVecs) % 2 != 0;
+    const int phys = pt[t / kPage];
+    if (phys < 0 || phys >= a.dims.n_pages) {
+      report(a.st, BS_ERR_DEVICE_BOUNDS);
+      continue;
+    }
+    const int64_t row = row0 + a.path[static_cast<int64_t>(b) * a.path_stride + n];
+    Raw8<Q32> raw;
+    raw.load(is_v ? a.v_new : a.k_new, row * a.row_stride + static_cast<int64_t>(h) * D + at * 8);
+    float x[8];
+    raw.get(x);
+    store8<C32>(is_v ? a.pools.v_pool : a.pools.k_pool, (static_cast<int64_t>(phys) * kPage + t % kPage) * D + at * 8, x);
+  }
+}
+
 // Pages a warp takes in turn: one (K or V) while that keeps the launch short; four for long
 // prompts, where a CTA's start is worth several pages.
-template <int D, bool I8, bool Q32>
+template <int D, bool I8, bool Q32, bool kPath>
 bs_status launch_append(const AppendArgs &a, int max_new, cudaStream_t cs) {
   const int units = a.dims.batch * a.dims.n_kv_heads;
   const int64_t items = 2 * ((static_cast<int64_t>(max_new) + kPage - 2) / kPage + 1);   // pages that max_new tokens can touch
@@ -272,15 +321,39 @@ bs_status launch_append(const AppendArgs &a, int max_new, cudaStream_t cs) {
   const int64_t gy = (items + kAppendWarps * per_warp - 1) / (kAppendWarps * per_warp);
   // (a programmatic dependent: its CTAs are in place when the work before it ends)
   const dim3 grid(units, static_cast<unsigned>(gy < 65535 ? gy : 65535));
-  return launch_ex(append_kernel<D, I8, Q32>, grid, kAppendThreads, 0, cs, 0, true, a, per_warp) == cudaSuccess ? BS_OK
+  return launch_ex(append_kernel<D, I8, Q32, kPath>, grid, kAppendThreads, 0, cs, 0, true, a, per_warp) == cudaSuccess ? BS_OK
                                                                                                                 : BS_ERR_CUDA;
 }
 
-template <int D>
+template <int D, bool kPath>
 bs_status dispatch_types(const AppendArgs &a, int max_new, cudaStream_t cs) {
   const bool i8 = a.dims.kv_dtype == BS_INT8, q32 = a.dims.q_dtype == BS_FP32;
-  if (i8) return q32 ? launch_append<D, true, true>(a, max_new, cs) : launch_append<D, true, false>(a, max_new, cs);
-  return q32 ? launch_append<D, false, true>(a, max_new, cs) : launch_append<D, false, false>(a, max_new, cs);
+  if (i8) return q32 ? launch_append<D, true, true, kPath>(a, max_new, cs) : launch_append<D, true, false, kPath>(a, max_new, cs);
+  return q32 ? launch_append<D, false, true, kPath>(a, max_new, cs) : launch_append<D, false, false, kPath>(a, max_new, cs);
+}
+
+template <int D>
+bs_status commit_rows(const AppendArgs &a, cudaStream_t cs) {
+  const bool q32 = a.dims.q_dtype == BS_FP32, c32 = a.dims.kv_dtype == BS_FP32;
+  auto kernel = q32 ? (c32 ? commit_rows_kernel<D, true, true> : commit_rows_kernel<D, true, false>)
+                    : (c32 ? commit_rows_kernel<D, false, true> : commit_rows_kernel<D, false, false>);
+  const dim3 grid(a.dims.batch * a.dims.n_kv_heads);
+  return launch_ex(kernel, grid, kAppendThreads, 0, cs, 0, true, a) == cudaSuccess ? BS_OK : BS_ERR_CUDA;
+}
+
+// Host checks that both appends share (after those of the dims).
+bs_status check_append(const bs_dims *dims, const bs_pools *pools, const void *page_table, const void *seq_lens,
+                       const void *tok_begin, const void *row_begin, const void *k_new, const void *v_new,
+                       int64_t row_stride, int64_t n_rows, const void *dev_status) {
+  if (!pools || !pools->k_pool || !pools->v_pool || !page_table || !seq_lens || !tok_begin || !row_begin || !k_new ||
+      !v_new || !dev_status)
+    return BS_ERR_INVALID_ARG;
+  if (is_quant(dims->kv_dtype) && (!pools->k_scale || !pools->v_scale)) return BS_ERR_INVALID_ARG;
+  if (n_rows < 0 || row_stride < static_cast<int64_t>(dims->n_kv_heads) * dims->head_dim) return BS_ERR_INVALID_ARG;
+  if (!aligned16(pools->k_pool) || !aligned16(pools->v_pool) || !aligned16(k_new) || !aligned16(v_new) ||
+      row_stride % (dims->q_dtype == BS_FP32 ? 4 : 8) != 0)
+    return BS_ERR_ALIGN;
+  return BS_OK;
 }
 
 }  // namespace
@@ -294,15 +367,31 @@ extern "C" bs_status bs_quant_append(const bs_dims *dims, const bs_pools *pools,
   bs_status s = check_dims(dims);
   if (s != BS_OK) return s;
   if (!is_quant(dims->kv_dtype)) return BS_ERR_INVALID_ARG;
-  if (!pools || !pools->k_pool || !pools->v_pool || !pools->k_scale || !pools->v_scale || !page_table || !seq_lens ||
-      !tok_begin || !row_begin || !k_new || !v_new || !dev_status)
-    return BS_ERR_INVALID_ARG;
-  if (n_rows < 0 || max_new_tokens < 1) return BS_ERR_INVALID_ARG;
-  if (row_stride < static_cast<int64_t>(dims->n_kv_heads) * dims->head_dim) return BS_ERR_INVALID_ARG;
-  if (!aligned16(pools->k_pool) || !aligned16(pools->v_pool) || !aligned16(k_new) || !aligned16(v_new) ||
-      row_stride % (dims->q_dtype == BS_FP32 ? 4 : 8) != 0)
-    return BS_ERR_ALIGN;
-  AppendArgs a{*dims, *pools, page_table, seq_lens, tok_begin, row_begin, k_new, v_new, row_stride, n_rows, dev_status};
+  if (max_new_tokens < 1) return BS_ERR_INVALID_ARG;
+  s = check_append(dims, pools, page_table, seq_lens, tok_begin, row_begin, k_new, v_new, row_stride, n_rows, dev_status);
+  if (s != BS_OK) return s;
+  AppendArgs a{*dims, *pools, page_table, seq_lens, tok_begin, row_begin, k_new, v_new, row_stride, n_rows, dev_status, nullptr, 0};
   cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  return dims->head_dim == 128 ? dispatch_types<128>(a, max_new_tokens, cs) : dispatch_types<64>(a, max_new_tokens, cs);
+  return dims->head_dim == 128 ? dispatch_types<128, false>(a, max_new_tokens, cs) : dispatch_types<64, false>(a, max_new_tokens, cs);
+}
+
+extern "C" bs_status bs_tree_commit(const bs_dims *dims, const bs_pools *pools, const int32_t *page_table,
+                                    const int32_t *seq_lens, const int32_t *tok_begin, const int32_t *row_begin,
+                                    const int32_t *path, int32_t path_stride, const void *k_new, const void *v_new,
+                                    int64_t row_stride, int64_t n_rows, int32_t *dev_status, bs_stream_t stream) {
+  using namespace bsi;
+  bs_status s = check_dims(dims);
+  if (s != BS_OK) return s;
+  if (!path || path_stride < 1 || path_stride > BS_MAX_DRAFT) return BS_ERR_INVALID_ARG;
+  s = check_append(dims, pools, page_table, seq_lens, tok_begin, row_begin, k_new, v_new, row_stride, n_rows, dev_status);
+  if (s != BS_OK) return s;
+  // (the scales of a cache that has none are not the kernel's to see)
+  bs_pools to{pools->k_pool, pools->v_pool, nullptr, nullptr};
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  if (!is_quant(dims->kv_dtype)) {
+    AppendArgs a{*dims, to, page_table, seq_lens, tok_begin, row_begin, k_new, v_new, row_stride, n_rows, dev_status, path, path_stride};
+    return dims->head_dim == 128 ? commit_rows<128>(a, cs) : commit_rows<64>(a, cs);
+  }
+  AppendArgs a{*dims, *pools, page_table, seq_lens, tok_begin, row_begin, k_new, v_new, row_stride, n_rows, dev_status, path, path_stride};
+  return dims->head_dim == 128 ? dispatch_types<128, true>(a, path_stride, cs) : dispatch_types<64, true>(a, path_stride, cs);
 }

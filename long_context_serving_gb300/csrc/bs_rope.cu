@@ -1,0 +1,253 @@
+// Norm, rotation and cache write of new tokens' queries and keys (formulas with bs_rope_append
+// in bsattn.h), one pass: every element is read once and written once.
+//
+// A row is the heads of one token, and all of them turn by the same angles. A lane holds 16
+// elements of a head, the eight pairs that it turns, so a rotation needs no exchange and a norm
+// three shuffles (head_dim / 16 lanes a head); it keeps the pairs' cosines and sines in registers
+// while its warp walks the row's heads, four (d = 128) or eight (d = 64) at a time. Few rows are
+// split over several warps each.
+// Angles: position * inv_freq in turns, inv_freq / 2 pi held as two floats (high and low part,
+// from one fp64 product a frequency and block), the product's rounding error taken back by an
+// fma: the fraction of a turn is right to 2^-24 at any position below 2^24, without fp64 in the
+// loop (fp64 runs at 1/64 of fp32's rate here).
+#include "bs_attn_launch.cuh"
+#include "bs_rows.cuh"
+
+namespace bsi {
+namespace {
+
+constexpr int kRopeThreads = 256;
+constexpr int kRopeWarps = kRopeThreads / 32;
+constexpr int kMaxPosition = 1 << 24;   // positions are exact in fp32
+
+struct RopeArgs {
+  bs_dims dims;
+  bs_rope rope;
+  const void *q, *k, *v;
+  int64_t row_stride, n_rows;
+  const int32_t *positions, *row_seq;
+  void *k_pool, *v_pool;   // null: no cache
+  const int32_t *page_table;
+  void *q_out, *k_out;
+  int32_t parts;           // warps that share a row
+  int32_t *st;
+};
+
+// Q32, C32: rows and outputs, cache in fp32 (else bf16).
+template <int D, bool Q32, bool C32>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
+  constexpr int kLanes = D / 16;          // lanes a head
+  constexpr int kHeads = 32 / kLanes;     // heads a warp takes at once
+  const bs_dims &dims = a.dims;
+  const int lane = threadIdx.x & 31, l = lane % kLanes, sub = lane / kLanes;
+  const int rot = a.rope.rot_dim;
+  const bool inter = a.rope.interleaved != 0;
+  __shared__ float2 turns[D / 2];         // inv_freq / 2 pi: high part, low part
+  asm volatile("griddepcontrol.wait;" ::: "memory");      // everything before this call has finished
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (threadIdx.x < rot / 2) {
+    const double f = a.rope.inv_freq[threadIdx.x] * 0.15915494309189533577;   // 1 / (2 pi)
+    const float hi = static_cast<float>(f);
+    turns[threadIdx.x] = make_float2(hi, static_cast<float>(f - hi));
+  }
+  __syncthreads();
+  // This lane's elements of a head: [ea, ea + 8) and [eb, eb + 8); pairs 8l .. 8l + 7 where it
+  // lies in the rotated part.
+  const bool turning = l < rot / 16;
+  const int ea = turning && !inter ? 8 * l : 16 * l;
+  const int eb = turning && !inter ? rot / 2 + 8 * l : 16 * l + 8;
+  float wq_a[8], wq_b[8], wk_a[8], wk_b[8];
+  const bool norm_q = a.rope.q_weight != nullptr, norm_k = a.rope.k_weight != nullptr;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    wq_a[j] = norm_q ? a.rope.q_weight[ea + j] : 1.0f;
+    wq_b[j] = norm_q ? a.rope.q_weight[eb + j] : 1.0f;
+    wk_a[j] = norm_k ? a.rope.k_weight[ea + j] : 1.0f;
+    wk_b[j] = norm_k ? a.rope.k_weight[eb + j] : 1.0f;
+  }
+  const int Hq = dims.n_q_heads, Hkv = dims.n_kv_heads;
+  const bool cache = a.k_pool != nullptr;
+  const int n_heads = Hq + Hkv + (cache ? Hkv : 0);
+  const int64_t n_items = a.n_rows * a.parts;
+  const int64_t n_warps = static_cast<int64_t>(gridDim.x) * kRopeWarps;
+  for (int64_t item = static_cast<int64_t>(blockIdx.x) * kRopeWarps + (threadIdx.x >> 5); item < n_items; item += n_warps) {
+    const int64_t row = a.parts == 1 ? item : item / a.parts;
+    const int part = a.parts == 1 ? 0 : static_cast<int>(item - row * a.parts);
+    const int b = a.row_seq != nullptr ? a.row_seq[row] : 0;
+    if (b < 0) continue;   // padding
+    const int pos = a.positions[row];
+    int bad = 0;
+    if (pos < 0 || pos >= kMaxPosition) bad = BS_ERR_INVALID_ARG;
+    else if (a.row_seq != nullptr && b >= dims.batch) bad = BS_ERR_DEVICE_BOUNDS;
+    else if (cache && pos / kPage >= dims.max_pages_per_unit) bad = BS_ERR_CAPACITY;
+    if (bad != 0) {
+      if (lane == 0 && part == 0) report(a.st, bad);
+      continue;
+    }
+    float cs[8], sn[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      cs[j] = 1.0f;
+      sn[j] = 0.0f;
+    }
+    if (turning) {
+      const float p = static_cast<float>(pos);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float2 f = turns[8 * l + j];
+        const float t = p * f.x;
+        const float low = fmaf(p, f.y, fmaf(p, f.x, -t));
+        const float r = (t - rintf(t)) + low;
+        sincospif(2.0f * r, &sn[j], &cs[j]);
+        sn[j] *= a.rope.magnitude;
+        cs[j] *= a.rope.magnitude;
+      }
+    }
+    const int64_t row_at = row * a.row_stride;
+    for (int h0 = part * kHeads; h0 < n_heads; h0 += a.parts * kHeads) {
+      const int head = h0 + sub;
+      const bool live = head < n_heads;
+      const bool is_q = head < Hq, is_v = head >= Hq + Hkv;
+      const int hk = is_q ? 0 : (is_v ? head - Hq - Hkv : head - Hq);
+      Raw8<Q32> ra{}, rb{};
+      int page = 0;
+      if (live) {
+        const void *src = is_q ? a.q : (is_v ? a.v : a.k);
+        const int64_t at = row_at + static_cast<int64_t>(is_q ? head : hk) * D;
+        ra.load(src, at + ea);
+        rb.load(src, at + eb);
+        if (cache && !is_q)
+          page = a.page_table[(static_cast<int64_t>(b) * Hkv + hk) * dims.max_pages_per_unit + pos / kPage];
+      }
+      float xa[8], xb[8];
+      ra.get(xa);
+      rb.get(xb);
+      if (norm_q || norm_k) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum = fmaf(xa[j], xa[j], fmaf(xb[j], xb[j], sum));
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (is_q ? norm_q : (!is_v && norm_k)) {
+          const float inv = rsqrtf(fmaf(sum, 1.0f / D, a.rope.eps));
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            xa[j] = xa[j] * inv * (is_q ? wq_a[j] : wk_a[j]);
+            xb[j] = xb[j] * inv * (is_q ? wq_b[j] : wk_b[j]);
+          }
+        }
+      }
+      if (turning && !is_v) {
+        if (inter) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            float &x = j < 4 ? xa[2 * j] : xb[2 * j - 8];
+            float &y = j < 4 ? xa[2 * j + 1] : xb[2 * j - 7];
+            const float u = x, w = y;
+            x = fmaf(u, cs[j], -(w * sn[j]));
+            y = fmaf(w, cs[j], u * sn[j]);
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float u = xa[j], w = xb[j];
+            xa[j] = fmaf(u, cs[j], -(w * sn[j]));
+            xb[j] = fmaf(w, cs[j], u * sn[j]);
+          }
+        }
+      }
+      if (!live) continue;
+      if (is_q) {
+        const int64_t to = (row * Hq + head) * D;
+        store8<Q32>(a.q_out, to + ea, xa);
+        store8<Q32>(a.q_out, to + eb, xb);
+        continue;
+      }
+      if (!is_v && a.k_out != nullptr) {
+        const int64_t to = (row * Hkv + hk) * D;
+        store8<Q32>(a.k_out, to + ea, xa);
+        store8<Q32>(a.k_out, to + eb, xb);
+      }
+      if (cache) {
+        if (page < 0 || page >= dims.n_pages) {
+          if (l == 0) report(a.st, BS_ERR_DEVICE_BOUNDS);
+          continue;
+        }
+        const int64_t to = (static_cast<int64_t>(page) * kPage + pos % kPage) * D;
+        store8<C32>(is_v ? a.v_pool : a.k_pool, to + ea, xa);
+        store8<C32>(is_v ? a.v_pool : a.k_pool, to + eb, xb);
+      }
+    }
+  }
+}
+
+template <int D, bool Q32, bool C32>
+bs_status launch_rope(RopeArgs &a, cudaStream_t cs) {
+  constexpr int kHeads = 512 / D;
+  const int groups = (a.dims.n_q_heads + 2 * a.dims.n_kv_heads + kHeads - 1) / kHeads;
+  const int64_t most = static_cast<int64_t>(attn_target_ctas()) * 2;   // CTAs of a full grid: four an SM
+  // A row's angles are worth about one group of its heads: it is shared out only while warps lack work.
+  const int64_t spare = most * kRopeWarps / a.n_rows;
+  a.parts = static_cast<int>(spare < 1 ? 1 : spare < groups ? spare : groups);
+  const int64_t ctas = (a.n_rows * a.parts + kRopeWarps - 1) / kRopeWarps;
+  const dim3 grid(static_cast<unsigned>(ctas < most ? ctas : most));
+  return launch_ex(rope_kernel<D, Q32, C32>, grid, kRopeThreads, 0, cs, 0, true, a) == cudaSuccess ? BS_OK : BS_ERR_CUDA;
+}
+
+template <int D>
+bs_status dispatch_types(RopeArgs &a, cudaStream_t cs) {
+  const bool q32 = a.dims.q_dtype == BS_FP32, c32 = a.dims.kv_dtype == BS_FP32;
+  if (q32) return c32 ? launch_rope<D, true, true>(a, cs) : launch_rope<D, true, false>(a, cs);
+  return c32 ? launch_rope<D, false, true>(a, cs) : launch_rope<D, false, false>(a, cs);
+}
+
+}  // namespace
+}  // namespace bsi
+
+extern "C" bs_status bs_rope_append(const bs_dims *dims, const bs_rope *rope, const void *q, const void *k,
+                                    const void *v, int64_t row_stride, int64_t n_rows, const int32_t *positions,
+                                    const int32_t *row_seq, const bs_pools *pools, const int32_t *page_table,
+                                    void *q_out, void *k_out, int32_t *dev_status, bs_stream_t stream) {
+  using namespace bsi;
+  bs_status s = check_dims(dims);
+  if (s != BS_OK) return s;
+  if (!rope || !rope->inv_freq || !q || !k || !positions || !q_out || !dev_status) return BS_ERR_INVALID_ARG;
+  if (pools != nullptr) {
+    if (is_quant(dims->kv_dtype)) return BS_ERR_INVALID_ARG;
+    if (!pools->k_pool || !pools->v_pool || !page_table || !row_seq || !v) return BS_ERR_INVALID_ARG;
+  } else if (!k_out) {
+    return BS_ERR_INVALID_ARG;
+  }
+  if (rope->rot_dim < 16 || rope->rot_dim > dims->head_dim || rope->rot_dim % 16 != 0) return BS_ERR_SHAPE;
+  if (rope->interleaved != 0 && rope->interleaved != 1) return BS_ERR_INVALID_ARG;
+  // (written so that NaN fails too)
+  if (!(rope->eps >= 0.0f && rope->eps <= 3.4e38f) || !(rope->magnitude >= -3.4e38f && rope->magnitude <= 3.4e38f))
+    return BS_ERR_INVALID_ARG;
+  if (n_rows < 0 || n_rows > (int64_t(1) << 40)) return BS_ERR_INVALID_ARG;
+  if (row_stride < static_cast<int64_t>(dims->n_q_heads) * dims->head_dim) return BS_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k) || (pools && (!aligned16(v) || !aligned16(pools->k_pool) || !aligned16(pools->v_pool))) ||
+      !aligned16(q_out) || (k_out && !aligned16(k_out)) || row_stride % (dims->q_dtype == BS_FP32 ? 4 : 8) != 0 ||
+      reinterpret_cast<uintptr_t>(rope->inv_freq) % 8 != 0)
+    return BS_ERR_ALIGN;
+  if (n_rows == 0) return BS_OK;
+  RopeArgs a{};
+  a.dims = *dims;
+  a.rope = *rope;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.row_stride = row_stride;
+  a.n_rows = n_rows;
+  a.positions = positions;
+  a.row_seq = row_seq;
+  if (pools != nullptr) {
+    a.k_pool = pools->k_pool;
+    a.v_pool = pools->v_pool;
+    a.page_table = page_table;
+  }
+  a.q_out = q_out;
+  a.k_out = k_out;
+  a.st = dev_status;
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  return dims->head_dim == 128 ? dispatch_types<128>(a, cs) : dispatch_types<64>(a, cs);
+}
