@@ -15,7 +15,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libbsattn.so")
 SOURCES = ["bs_api.cu", "bs_summaries.cu", "bs_score.cu", "bs_select.cu", "bs_attn.cu", "bs_attn_bf16.cu",
            "bs_attn_f32.cu", "bs_attn_quant.cu", "bs_setdiff.cu", "bs_step.cu", "bs_swap.cu", "bs_split.cu",
-           "bs_append.cu", "bs_pages.cu", "bs_rope.cu", "bs_rows_attn.cu"]
+           "bs_append.cu", "bs_pages.cu", "bs_rope.cu", "bs_rows_attn.cu",
+           "bs_prefill_bf16.cu", "bs_prefill_quant.cu", "bs_tree_bf16.cu", "bs_tree_quant.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-I" + INCLUDE, "-I" + CSRC]
 

@@ -75,6 +75,24 @@ bs_status make_kv_tensor_maps(const bs_dims &d, const bs_kv &kv, CUtensorMap *tk
   return BS_OK;
 }
 
+bs_status make_bf16_map(CUtensorMap *map, const void *base, int rank, const uint64_t *size, const uint64_t *stride_bytes,
+                        const uint32_t *box) {
+  EncodeTiledFn enc = encode_tiled_fn();
+  if (enc == nullptr) return BS_ERR_CUDA;
+  cuuint64_t dims[3], strides[2];
+  cuuint32_t boxes[3], estr[3];
+  for (int i = 0; i < rank; ++i) {
+    dims[i] = size[i];
+    boxes[i] = box[i];
+    estr[i] = 1;
+    if (i > 0) strides[i - 1] = stride_bytes[i - 1];
+  }
+  const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, static_cast<cuuint32_t>(rank), const_cast<void *>(base), dims,
+                         strides, boxes, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? BS_OK : BS_ERR_CUDA;
+}
+
 }  // namespace bsi
 
 extern "C" {

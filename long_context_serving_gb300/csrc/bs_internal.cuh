@@ -199,6 +199,11 @@ uint64_t wait_limit_ns();
 // boxes of 16 rows x 64 columns (128 bytes) with 128-byte swizzle.
 bs_status make_kv_tensor_maps(const bs_dims &d, const bs_kv &kv, CUtensorMap *tk, CUtensorMap *tv);
 
+// A tiled tensor map over bf16 elements (rank 2 or 3, sizes and box fastest first, strides of the
+// outer dimensions), 128-byte swizzle.
+bs_status make_bf16_map(CUtensorMap *map, const void *base, int rank, const uint64_t *size, const uint64_t *stride_bytes,
+                        const uint32_t *box);
+
 // Dynamic shared memory is re-based to a 1024-byte boundary (the 128-byte swizzle
 // atom of TMA copies); kernels that need it allocate this much more.
 constexpr int kSmemAlignSlack = 1024;

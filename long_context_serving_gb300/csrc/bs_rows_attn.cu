@@ -1,51 +1,139 @@
-// Attention of new tokens over the paged cache: bs_prefill_attn and bs_tree_decode_attn.
-#include "bs_attn_launch.cuh"
-#include "bs_rows_attn.cuh"
+// Attention of new tokens over the paged cache: bs_prefill_attn and bs_tree_decode_attn, their
+// plans, and the merge of split rows.
+#include "bs_rows_mma.cuh"
 
 namespace bsi {
 namespace {
 
-constexpr int kRowWarps = 4;
+// ---------------------------------------------------------------------------------------
+// Plan: from host-known bounds only (n_rows, the most tokens of a sequence, the dims).
+// ---------------------------------------------------------------------------------------
+constexpr int kSms = 152;
 
-// A warp a row and query head.
+struct HostPlan {
+  RowsPlan p;
+  int tiles;               // row tiles of a CTA
+  int64_t items;
+  size_t rec_o_bytes, workspace_bytes;
+};
+
+HostPlan plan_rows(const bs_dims &d, int64_t n_rows, int max_new, bool tree) {
+  HostPlan h{};
+  const int G = d.n_q_heads / d.n_kv_heads;
+  h.p.tokens = 128 / G;
+  h.tiles = max_new <= h.p.tokens ? 1 : 2;
+  h.p.block_tokens = h.tiles * h.p.tokens;
+  const int64_t per_seq = (static_cast<int64_t>(max_new) + h.p.block_tokens - 1) / h.p.block_tokens;
+  int64_t key_tiles;       // of a block, at most
+  if (tree) {
+    h.p.n_blocks = static_cast<int>(per_seq);
+    h.items = static_cast<int64_t>(d.batch) * d.n_kv_heads * per_seq;
+    key_tiles = (static_cast<int64_t>(d.max_gather_pages_per_unit) + (max_new + kPage - 1) / kPage + kTileGroups - 1) / kTileGroups;
+  } else {
+    const int64_t by_seq = per_seq * d.batch, by_rows = n_rows / h.p.block_tokens + (n_rows < d.batch ? n_rows : d.batch);
+    const int64_t blocks = by_seq < by_rows ? by_seq : by_rows;
+    h.p.n_blocks = static_cast<int>(blocks < INT32_MAX ? blocks : INT32_MAX);
+    h.items = blocks * d.n_kv_heads;
+    key_tiles = (static_cast<int64_t>(d.max_pages_per_unit) + kTileGroups - 1) / kTileGroups;
+  }
+  h.p.record_rows = (max_new < h.p.block_tokens ? max_new : h.p.block_tokens) * G;
+  int64_t splits = 1;
+  if (h.items <= kSms) splits = kSms / h.items;                                   // one wave
+  else if (h.tiles == 1 && key_tiles > 32) splits = (key_tiles + 23) / 24;       // pieces of about 24 tiles
+  if (splits > key_tiles) splits = key_tiles;
+  const int64_t most = (int64_t(64) << 20) / (static_cast<int64_t>(h.p.record_rows) * d.head_dim * 4) / h.items;   // records of 64 MB
+  if (splits > most) splits = most;
+  h.p.splits = static_cast<int>(splits < 1 ? 1 : splits);
+  if (h.p.splits > 1) {
+    const size_t recs = static_cast<size_t>(h.items) * h.p.splits * h.p.record_rows;
+    h.rec_o_bytes = recs * d.head_dim * sizeof(float);
+    h.workspace_bytes = h.rec_o_bytes + (recs * sizeof(float2) + 15) / 16 * 16;
+  }
+  return h;
+}
+
+// ---------------------------------------------------------------------------------------
+// Merge of split rows: a warp a row, a lane D / 32 elements, records eight at a time in flight.
+// ---------------------------------------------------------------------------------------
+constexpr int kMergeWarps = 8;
+
 template <int D, bool kTree>
-__global__ void __launch_bounds__(kRowWarps * 32) rows_kernel(const __grid_constant__ RowsArgs a) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");      // everything before this call has finished
+__global__ void __launch_bounds__(kMergeWarps * 32) rows_merge_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ RowsPlan p) {
+  constexpr int E = D / 32;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  asm volatile("griddepcontrol.wait;" ::: "memory");      // the splits' records
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int G = a.dims.n_q_heads / a.dims.n_kv_heads, lane = threadIdx.x & 31;
-  const int64_t item = static_cast<int64_t>(blockIdx.x) * kRowWarps + (threadIdx.x >> 5);
-  const int64_t row = item / a.dims.n_q_heads;
-  const int head = static_cast<int>(item % a.dims.n_q_heads), h = head / G;
-  SeqRows r;
-  int b = 0;
-  for (; b < a.dims.batch; ++b) {
-    const int bad = seq_rows<kTree>(a, b, r);
-    if (bad != 0 && item == 0 && lane == 0) report(a.st, bad);
-    if (r.n > 0 && row >= r.row0 && row < r.row0 + r.n) break;
-  }
-  if (b == a.dims.batch) return;
-  const int i = static_cast<int>(row - r.row0);
-  Keys k;
-  const int bad = unit_keys<kTree>(a, r, b * a.dims.n_kv_heads + h, i, i + 1, k);
-  if (bad != 0) {
-    if (lane == 0) report(a.st, bad);
-    return;
-  }
-  float m, l, o[D / 32];
-  row_attend<D, kTree>(a, r, k, h, i, head % G, 0, k.n_groups, m, l, o);
-  __nv_bfloat16 *out = a.out + (row * a.dims.n_q_heads + head) * D + lane * (D / 32);
+  const int64_t index = blockIdx.x;
+  RowsItem it;
+  find_item<kTree>(a, p, index, 1, it);                    // (errors are the first kernel's to report)
+  if (it.n_splits <= 1) return;                            // nothing to do, or written already
+  const int G = a.dims.n_q_heads / a.dims.n_kv_heads;
+  const int row = blockIdx.y * kMergeWarps + warp;
+  if (row >= (it.i1 - it.i0) * G) return;
+  const float *o = p.rec_o + (index * p.splits * p.record_rows + row) * D + lane * E;
+  const float2 *ml = p.rec_ml + index * p.splits * p.record_rows + row;
+  const int64_t step = p.record_rows;
+  float m = -INFINITY;
+  for (int s = lane; s < it.n_splits; s += 32) m = fmaxf(m, ml[s * step].x);
 #pragma unroll
-  for (int e = 0; e < D / 32; ++e) out[e] = __float2bfloat16_rn(l == 0.0f ? 0.0f : o[e] / l);
-  if (lane == 0 && a.lse != nullptr) a.lse[row * a.dims.n_q_heads + head] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+  for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+  float l = 0.0f, acc[E] = {};
+  if (m != -INFINITY) {
+#pragma unroll 8
+    for (int s = 0; s < it.n_splits; ++s) {
+      const float2 x = ml[s * step];
+      const float w = x.x == -INFINITY ? 0.0f : exp2f(x.x - m);
+      l = fmaf(x.y, w, l);
+      const float *at = o + s * step * D;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = fmaf(at[e], w, acc[e]);
+    }
+  }
+  const int64_t out_row = (it.r.row0 + it.i0 + row / G) * a.dims.n_q_heads + it.h * G + row % G;
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+  uint32_t *to = reinterpret_cast<uint32_t *>(a.out + out_row * D + lane * E);
+#pragma unroll
+  for (int e = 0; e < E; e += 2) to[e / 2] = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
+  if (lane == 0 && a.lse != nullptr) a.lse[out_row] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 template <bool kTree>
-bs_status launch_rows(const RowsArgs &a, cudaStream_t cs) {
-  const int64_t warps = (kTree ? a.drafts.n_rows : a.n_rows) * a.dims.n_q_heads;
-  const int64_t ctas = (warps + kRowWarps - 1) / kRowWarps;
-  if (ctas > INT32_MAX) return BS_ERR_CAPACITY;
-  auto kernel = a.dims.head_dim == 128 ? rows_kernel<128, kTree> : rows_kernel<64, kTree>;
-  return launch_ex(kernel, dim3(static_cast<unsigned>(ctas)), kRowWarps * 32, 0, cs, 0, true, a) == cudaSuccess ? BS_OK : BS_ERR_CUDA;
+bs_status launch_rows(RowsArgs &a, void *workspace, size_t workspace_bytes, cudaStream_t cs) {
+  const bs_dims &d = a.dims;
+  HostPlan h = plan_rows(d, a.n_rows, a.max_new, kTree);
+  if (h.items * h.p.splits > INT32_MAX) return BS_ERR_CAPACITY;
+  if (h.p.splits > 1) {
+    if (workspace == nullptr) return BS_ERR_INVALID_ARG;
+    if (!aligned16(workspace)) return BS_ERR_ALIGN;
+    if (workspace_bytes < h.workspace_bytes) return BS_ERR_CAPACITY;
+    h.p.rec_o = static_cast<float *>(workspace);
+    h.p.rec_ml = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + h.rec_o_bytes);
+  }
+  h.p.wait_ns = wait_limit_ns();
+  const int G = d.n_q_heads / d.n_kv_heads;
+  const uint64_t D = static_cast<uint64_t>(d.head_dim);
+  RowsMaps maps{};
+  const uint64_t q_size[3] = {D, static_cast<uint64_t>(d.n_q_heads), static_cast<uint64_t>(a.n_rows)};
+  const uint64_t q_step[2] = {D * 2, static_cast<uint64_t>(a.q_stride) * 2};
+  const uint32_t q_box[3] = {64, static_cast<uint32_t>(G), static_cast<uint32_t>(h.p.tokens)};
+  bs_status s = make_bf16_map(&maps.q, a.q, 3, q_size, q_step, q_box);
+  if (s == BS_OK && d.kv_dtype == BS_BF16) {
+    s = make_kv_tensor_maps(d, a.kv, &maps.k, &maps.v);
+    if (kTree) {
+      const uint64_t size[2] = {D * d.n_kv_heads, static_cast<uint64_t>(a.drafts.n_rows)};
+      const uint64_t step[1] = {static_cast<uint64_t>(a.drafts.row_stride) * 2};
+      const uint32_t box[2] = {64, kPage};
+      if (s == BS_OK) s = make_bf16_map(&maps.k_new, a.drafts.k_new, 2, size, step, box);
+      if (s == BS_OK) s = make_bf16_map(&maps.v_new, a.drafts.v_new, 2, size, step, box);
+    }
+  }
+  if (s != BS_OK) return s;
+  s = d.kv_dtype == BS_BF16 ? launch_rows_bf16<kTree>(a, h.p, maps, h.items, h.tiles, cs)
+                            : launch_rows_quant<kTree>(a, h.p, maps, h.items, h.tiles, cs);
+  if (s != BS_OK || h.p.splits == 1) return s;
+  auto merge = d.head_dim == 128 ? rows_merge_kernel<128, kTree> : rows_merge_kernel<64, kTree>;
+  const dim3 grid(static_cast<unsigned>(h.items), static_cast<unsigned>((h.p.record_rows + kMergeWarps - 1) / kMergeWarps));
+  return launch_ex(merge, grid, kMergeWarps * 32, 0, cs, 0, true, a, h.p) == cudaSuccess ? BS_OK : BS_ERR_CUDA;
 }
 
 // Host checks that both calls share (after those of the dims).
@@ -65,10 +153,16 @@ bs_status check_rows(const bs_dims *dims, const void *q, int64_t q_stride, const
 }  // namespace bsi
 
 extern "C" size_t bs_prefill_workspace_size(const bs_dims *dims, int64_t n_rows, int32_t max_new_tokens) {
-  return 0;
+  using namespace bsi;
+  if (check_dims(dims) != BS_OK || n_rows < 1 || n_rows > INT32_MAX || max_new_tokens < 1) return 0;
+  return plan_rows(*dims, n_rows, max_new_tokens, false).workspace_bytes;
 }
 
-extern "C" size_t bs_tree_workspace_size(const bs_dims *dims, int32_t max_draft) { return 0; }
+extern "C" size_t bs_tree_workspace_size(const bs_dims *dims, int32_t max_draft) {
+  using namespace bsi;
+  if (check_dims(dims) != BS_OK || max_draft < 1 || max_draft > BS_MAX_DRAFT) return 0;
+  return plan_rows(*dims, 0, max_draft, true).workspace_bytes;
+}
 
 extern "C" bs_status bs_prefill_attn(const bs_dims *dims, const void *q, int64_t q_stride, int64_t n_rows,
                                      const bs_kv *kv, const bs_head_cfg *cfg, const int32_t *tok_begin,
@@ -99,7 +193,7 @@ extern "C" bs_status bs_prefill_attn(const bs_dims *dims, const void *q, int64_t
   a.out = static_cast<__nv_bfloat16 *>(out);
   a.lse = lse;
   a.st = dev_status;
-  return launch_rows<false>(a, reinterpret_cast<cudaStream_t>(stream));
+  return launch_rows<false>(a, workspace, workspace_bytes, reinterpret_cast<cudaStream_t>(stream));
 }
 
 extern "C" bs_status bs_tree_decode_attn(const bs_dims *dims, const void *q, int64_t q_stride, const bs_kv *kv,
@@ -136,5 +230,5 @@ extern "C" bs_status bs_tree_decode_attn(const bs_dims *dims, const void *q, int
   a.out = static_cast<__nv_bfloat16 *>(out);
   a.lse = lse;
   a.st = dev_status;
-  return launch_rows<true>(a, reinterpret_cast<cudaStream_t>(stream));
+  return launch_rows<true>(a, workspace, workspace_bytes, reinterpret_cast<cudaStream_t>(stream));
 }

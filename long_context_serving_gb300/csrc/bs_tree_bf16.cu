@@ -1,0 +1,11 @@
+// Trees of drafts over bf16 caches.
+#include "bs_rows_mma.cuh"
+
+namespace bsi {
+
+template <>
+bs_status launch_rows_bf16<true>(const RowsArgs &a, const RowsPlan &p, const RowsMaps &maps, int64_t items, int tiles, cudaStream_t cs) {
+  return dispatch_rows<0, true>(a, p, maps, items, tiles, cs);
+}
+
+}  // namespace bsi
