@@ -78,7 +78,11 @@ __global__ void __launch_bounds__(kMergeWarps * 32) rows_merge_kernel(const __gr
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
   float l = 0.0f, acc[E] = {};
-  if (m != -INFINITY) {
+  auto add = [&]() -> bool {        // false: a sum is not finite
+    l = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+    if (m == -INFINITY) return true;
 #pragma unroll 8
     for (int s = 0; s < it.n_splits; ++s) {
       const float2 x = ml[s * step];
@@ -88,6 +92,14 @@ __global__ void __launch_bounds__(kMergeWarps * 32) rows_merge_kernel(const __gr
 #pragma unroll
       for (int e = 0; e < E; ++e) acc[e] = fmaf(at[e], w, acc[e]);
     }
+    float big = fabsf(l);
+#pragma unroll
+    for (int e = 0; e < E; ++e) big = big + 0.0f * acc[e];
+    return __all_sync(0xffffffffu, big < INFINITY);
+  };
+  if (!add()) {                     // (sums of the largest values of bf16: 2^24 below)
+    m += 24.0f;
+    add();
   }
   const int64_t out_row = (it.r.row0 + it.i0 + row / G) * a.dims.n_q_heads + it.h * G + row % G;
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;

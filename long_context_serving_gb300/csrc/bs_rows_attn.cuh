@@ -152,7 +152,9 @@ __device__ __forceinline__ bool sees(const Keys &k, const Group &g, int c, int i
 // ---------------------------------------------------------------------------------------
 // One row by one warp, in fp32: lane l holds elements [l * D / 32, ...) of q and of the output.
 // x = q . K / sqrt(d) in log2 units, a running maximum m, sum l and unnormalised output o. A key
-// that the row does not see is not looked at.
+// that the row does not see is not looked at. Weights are relative to 2^24 times the largest, so
+// that sums of the largest values of bf16 stay finite (they are why a row comes here, as much as
+// infinities are); m counts that factor.
 // ---------------------------------------------------------------------------------------
 template <int D, bool kTree>
 __device__ __noinline__ void row_attend(const RowsArgs &a, const SeqRows &r, const Keys &k, int h, int i, int gq, int g_lo,
@@ -197,7 +199,7 @@ __device__ __noinline__ void row_attend(const RowsArgs &a, const SeqRows &r, con
 #pragma unroll
       for (int s = 16; s > 0; s >>= 1) x += __shfl_xor_sync(0xffffffffu, x, s);
       x = x * ks * sc;
-      const float top = fmaxf(m, x);   // (a NaN stays out of the maximum and enters the sum)
+      const float top = fmaxf(m, x + 24.0f);   // (a NaN stays out of the maximum and enters the sum)
       const float keep = m == -INFINITY ? 0.0f : exp2f(m - top), w = top == -INFINITY ? 0.0f : exp2f(x - top);
       m = top;
       l = fmaf(l, keep, w);
