@@ -3,20 +3,21 @@
 // One CTA takes one KV head's rows of a block of tokens (all query heads of the group: a K or V
 // tile is fetched once for all of them), packed as 128-row tiles of whole tokens, kTiles of them
 // (1 or 2), against a contiguous piece of the block's key groups:
-//   copy warps     fetch K and V tiles, 128 keys each, into a ring of shared-memory slots: bf16
-//                  pages by tiled copies (a warp for K, one for V); 8-bit pages as codes by plain
-//                  loads, written as the bf16 values they stand for (four warps);
+//   copy warps     one for K, one for V: fetch tiles of 128 keys into a ring of shared-memory slots,
+//                  bf16 pages by tiled copies; 8-bit pages by bulk copies into a ring of their own,
+//   (8-bit) four warps  write the bf16 values that the codes stand for into the ring's slots;
 //   product warp   S = Q K^T into tensor memory (one thread issues); O += P V with P from tensor
 //                  memory, page by page, so that a page that is not there takes no part;
 //   row warps      four a tile, a thread a row: logits from tensor memory, the running maximum and
 //                  sum in registers, weights back to tensor memory as bf16, over the logits.
 // S of the next key tile is issued behind O's update, so with two tiles one's products run beside
-// the other's softmax; weights are handed over 64 keys at a time, so that O's update starts while
-// the second half's are made. O is brought to a new maximum only when that has grown by more than 2^8
+// the other's softmax; weights are handed over in two parts, 96 keys and 32, so that O's update
+// starts while the last are made and the rest of it and S do not wait for much. O is brought to a new maximum only when that has grown by more than 2^8
 // (weights of at most 256 in between; the final division takes it back), at the start of a
 // tile, when the products in flight are done: O's rescaling through registers is rare and needs no
-// warps of its own. What the second half's maximum adds waits for the next tile (a weight too large
-// for its type meanwhile makes the row one of those that are computed again).
+// warps of its own. What the second half's maximum adds, which is taken once its weights are on their
+// way, waits for the next tile (a weight too large for its type meanwhile makes the row one of those
+// that are computed again).
 // Precision: products of bf16 in fp32; weights enter as bf16 (2^-9 of themselves), which is the
 // operand type of V; their sum is taken before that rounding. Page scales: K's multiplies logits
 // in fp32; V's is m * 2^e, 2^e goes into the bf16 values (exact), m into the weights, so that
@@ -30,10 +31,13 @@
 #include "bs_rows_attn.cuh"
 #include "bs_umma.cuh"
 
+#include <type_traits>
+
 namespace bsi {
 
 constexpr int kKeyTile = 128;                 // keys of a tile
 constexpr int kTileGroups = kKeyTile / kPage; // groups of a tile
+constexpr int kFirstKeys = 96;                // keys whose weights are handed over first
 constexpr int kInfos = 8;                     // tiles whose description is kept
 
 struct RowsPlan {
@@ -142,13 +146,17 @@ struct TileInfo {
   uint32_t flags;             // bits 0..7: rows differ in what they see of the group, or its end is
                               // past the cache's; 8..15: it is not there; 16..23: it is of drafts
   float ks[kTileGroups], vs[kTileGroups];   // 8-bit caches: K's scale, mantissa of V's
+  float ve[kTileGroups];                    // and its power of two
 };
+constexpr int kRawSlots = 4;  // K or V tiles in codes
 
 struct RowsShared {
   RowsItem item;
   TileInfo info[kInfos];
-  uint64_t full[12], empty[12];
-  uint64_t q_full, s_full[2], p_full[2][2], o_full[2], drained;   // (p_full: [row tile][half of the keys])
+  uint64_t empty[12];         // a slot's products are done
+  uint64_t raw_full[kRawSlots], raw_empty[kRawSlots];
+  uint64_t k0_full, full[kInfos];   // K of the first tile; V of a tile and K of the next one, have landed
+  uint64_t q_full, s_full[2], p_full[2][2], o_full[2], drained, never;   // (p_full: [row tile][part])
   uint32_t tmem;
 };
 
@@ -161,13 +169,17 @@ struct RowsTraits {
   static constexpr int kQBytes = kTiles * 128 * D * 2;
   static constexpr int kControl = 2048;                 // RowsShared
   static constexpr int kMaxDyn = 232448;                // shared memory of a CTA, at most
-  static constexpr int kRoom = (kMaxDyn - 1024 - kControl - kQBytes) / kSlotBytes;
+  static constexpr int kRawBytes = kQuant ? kKeyTile * D : 0;
+  static constexpr int kRoom = (kMaxDyn - 1024 - kControl - kQBytes - kRawSlots * kRawBytes) / kSlotBytes;
   static constexpr int kSlots = kRoom < 12 ? kRoom : 12;
   static constexpr int kRowWarps = 4 * kTiles;
-  static constexpr int kCopyWarps = kQuant ? 4 : 2;
-  static constexpr int kThreads = 32 * (kRowWarps + 1 + kCopyWarps);
+  static constexpr int kWriters = kQuant ? 4 : 1;      // warps that fill a slot
+  // Warp 0 issues products, warps 1 and 2 copy, (8-bit) warps 4 to 7 convert, one on each scheduler;
+  // the row warps start at a multiple of four.
+  static constexpr int kFirstRow = kQuant ? 8 : 4;
+  static constexpr int kThreads = 32 * (kFirstRow + kRowWarps);
   static constexpr int kColumns = kTiles == 1 ? 256 : 512;
-  static constexpr int kSmem = 1024 + kQBytes + kSlots * kSlotBytes + kControl;
+  static constexpr int kSmem = 1024 + kQBytes + kSlots * kSlotBytes + kRawSlots * kRawBytes + kControl;
   static_assert(sizeof(RowsShared) <= kControl, "control block");
   static_assert(kSlots >= 3 && kSmem <= kMaxDyn, "ring");
 };
@@ -186,49 +198,31 @@ __device__ __forceinline__ uint32_t group_flags(const Keys &k, const Group &g, i
   }
 }
 
-// Four codes as four bf16 (exact: E4M3 times 2^120 from the bits in place, INT8 by adding in the
-// low mantissa bits); with `scaled`, times 2^e.
+// Four codes, with `scaled` times a power of two, as four bf16: exact short of bf16's range. (Through fp16 and fp32:
+// 8 x 16 codes a lane 190 cycles more than their copy; placing the bits and multiplying by 2^120
+// took 400, and 1500 with a look for NaN codes, which come through here by themselves.)
 template <bool I8>
-__device__ __forceinline__ void codes_to_bf16(uint32_t w, bool scaled, __nv_bfloat162 two_e, uint32_t &lo, uint32_t &hi) {
-  __nv_bfloat162 v[2];
+__device__ __forceinline__ void codes_to_bf16(uint32_t w, bool scaled, float two_e, uint32_t &lo, uint32_t &hi) {
+  float f[4];
+  codes_to_f32<I8>(w, f);
+  if (scaled) {
 #pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    if constexpr (I8) {
-      const uint32_t x = __byte_perm(w, 0, j == 0 ? 0x4140 : 0x4342);
-      const uint32_t p = (x & 0x007f007fu) | 0x43004300u, n = (x & 0x00800080u) | 0x43004300u;
-      v[j] = __hsub2(*reinterpret_cast<const __nv_bfloat162 *>(&p), *reinterpret_cast<const __nv_bfloat162 *>(&n));
-    } else {
-      const uint32_t x = __byte_perm(w, 0, j == 0 ? 0x1404 : 0x3424);
-      const uint32_t y = (x & 0x80008000u) | ((x >> 4) & 0x07f007f0u);
-      const uint32_t up = 0x7b807b80u;   // 2^120
-      v[j] = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&y), *reinterpret_cast<const __nv_bfloat162 *>(&up));
-    }
-    if (scaled) v[j] = __hmul2(v[j], two_e);
+    for (int i = 0; i < 4; ++i) f[i] *= two_e;
   }
-  lo = *reinterpret_cast<const uint32_t *>(&v[0]);
-  hi = *reinterpret_cast<const uint32_t *>(&v[1]);
-  if constexpr (!I8) {
-    // 0x7f and 0xff are NaN
-    if ((((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0) {
-      if ((w & 0x7fu) == 0x7fu) lo |= 0x00007fffu;
-      if ((w & 0x7f00u) == 0x7f00u) lo |= 0x7fff0000u;
-      if ((w & 0x7f0000u) == 0x7f0000u) hi |= 0x00007fffu;
-      if ((w & 0x7f000000u) == 0x7f000000u) hi |= 0x7fff0000u;
-    }
-  }
+  lo = pack_bf16(f[0], f[1]);
+  hi = pack_bf16(f[2], f[3]);
 }
 
-// A scale as m * 2^e, 2^e a normal bf16 (returned twice in a word); m in [1, 2), smaller for a
-// subnormal scale, and what there is for 0, infinity and NaN.
-__device__ __forceinline__ uint32_t split_scale(float s, float &m) {
+// A scale as m * 2^e, 2^e returned; m in [1, 2), smaller for a subnormal scale, and what there is
+// for 0, infinity and NaN.
+__device__ __forceinline__ float split_scale(float s, float &m) {
   const uint32_t bits = __float_as_uint(s), e = (bits >> 23) & 0xffu;
   if (e == 0xffu || s == 0.0f) {
     m = s;
-    return 0x3f803f80u;
+    return 1.0f;
   }
-  const uint32_t ee = e == 0 ? 1u : e;   // subnormal: 2^-126
   m = e == 0 ? s * 8.507059173023462e37f : __uint_as_float((bits & 0x807fffffu) | 0x3f800000u);   // (2^126)
-  return ee << 7 | ee << 23;
+  return __uint_as_float((e == 0 ? 1u : e) << 23);
 }
 
 template <int D, int kKv, int kTiles, bool kTree>
@@ -239,16 +233,22 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kTiles>::kThreads, 1)
   extern __shared__ unsigned char raw_smem[];
   unsigned char *smem = align_smem_1024(raw_smem);
   unsigned char *q_smem = smem, *ring = smem + Tr::kQBytes;
-  RowsShared &sh = *reinterpret_cast<RowsShared *>(ring + kSlots * Tr::kSlotBytes);
+  unsigned char *raw_ring = ring + kSlots * Tr::kSlotBytes;
+  RowsShared &sh = *reinterpret_cast<RowsShared *>(raw_ring + kRawSlots * Tr::kRawBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = a.dims.n_q_heads / a.dims.n_kv_heads;
 
-  if (warp == Tr::kRowWarps) {
+  if (warp == 0) {
     tmem_alloc(&sh.tmem, Tr::kColumns);
     if (lane == 0) {
       for (int i = 0; i < kSlots; ++i) {
-        mbar_init(&sh.full[i], Tr::kQuant ? Tr::kCopyWarps : 1);
         mbar_init(&sh.empty[i], 1);
+      }
+      mbar_init(&sh.k0_full, Tr::kWriters);
+      for (int i = 0; i < kInfos; ++i) mbar_init(&sh.full[i], 2 * Tr::kWriters);
+      for (int i = 0; i < kRawSlots; ++i) {
+        mbar_init(&sh.raw_full[i], 1);
+        mbar_init(&sh.raw_empty[i], Tr::kWriters);
       }
       mbar_init(&sh.q_full, 1);
       for (int t = 0; t < kTiles; ++t) {
@@ -258,6 +258,7 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kTiles>::kThreads, 1)
         mbar_init(&sh.o_full[t], 1);
       }
       mbar_init(&sh.drained, 1);
+      mbar_init(&sh.never, 1);
       fence_mbar_init();
       fence_proxy_async_smem();
     }
@@ -265,7 +266,7 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kTiles>::kThreads, 1)
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");      // everything before this call has finished
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (warp == 0) {
+  if (warp == Tr::kFirstRow) {
     RowsItem it;
     const int64_t index = blockIdx.x / p.splits;
     find_item<kTree>(a, p, index, static_cast<int>(blockIdx.x - index * p.splits), it);
@@ -280,17 +281,22 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kTiles>::kThreads, 1)
   // Tiles that hold rows (a last block may have one only).
   const int live_tiles = kTiles == 1 || it.i1 - it.i0 <= p.tokens ? 1 : 2;
   // A whole warp waits; false (for every lane) when a wait ran out. Each role then leaves its loop.
+  // Barrier on which an item (K or V of key tile j) lands: K of a tile goes with V of the one before.
+  auto full_of = [&](int j, int kv) -> uint64_t * {
+    const int pair = j - t_lo - (kv == 0);
+    return pair < 0 ? &sh.k0_full : &sh.full[pair % kInfos];
+  };
   auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
     if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
     return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, a.st, p.wait_ns));
   };
 
   if (t_lo < t_hi) {
-    if (warp > Tr::kRowWarps) {
-      // ---- copy warps ----------------------------------------------------------------------
+    if (warp == 1 || warp == 2) {
+      // ---- copy warps: 1 K, 2 V -----------------------------------------------------------------
       const Keys k = it.k;
       const int64_t row0 = it.r.row0;
-      const int h = it.h;
+      const int h = it.h, kv = warp - 1;
       auto group_of = [&](int j) -> Group {     // lanes 0..7: a tile's groups
         const int i = j * kTileGroups + lane;
         if (lane < kTileGroups && j < t_hi && i < k.n_groups) return key_group<kTree>(a, k, i);
@@ -301,171 +307,154 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kTiles>::kThreads, 1)
         return __ballot_sync(0xffffffffu, f & 1u) | __ballot_sync(0xffffffffu, f & 0x100u) << 8 |
                __ballot_sync(0xffffffffu, f & 0x10000u) << 16;
       };
-      int item = 0;
-      if constexpr (!Tr::kQuant) {
-        // q rows of the block, tile by tile: [token][head of the group], 64 columns at a time
-        const int kv = warp - Tr::kRowWarps - 1;       // 0: K, 1: V
-        if (kv == 0 && lane == 0) {
-          mbar_arrive_expect_tx(&sh.q_full, static_cast<uint32_t>(live_tiles * Tr::kHalves * p.tokens * G * 128));
-          for (int t = 0; t < live_tiles; ++t)
-            for (int x = 0; x < Tr::kHalves; ++x)
-              tma_3d(q_smem + t * (128 * D * 2) + x * 16384, &maps.q, x * 64, h * G, static_cast<int>(row0) + it.i0 + t * p.tokens, &sh.q_full);
+      // q rows of the block, tile by tile: [token][head of the group], 64 columns at a time
+      if (kv == 0 && lane == 0) {
+        mbar_arrive_expect_tx(&sh.q_full, static_cast<uint32_t>(live_tiles * Tr::kHalves * p.tokens * G * 128));
+        for (int t = 0; t < live_tiles; ++t)
+          for (int x = 0; x < Tr::kHalves; ++x)
+            tma_3d(q_smem + t * (128 * D * 2) + x * 16384, &maps.q, x * 64, h * G, static_cast<int>(row0) + it.i0 + t * p.tokens, &sh.q_full);
+      }
+      const CUtensorMap *map = kv == 0 ? &maps.k : &maps.v, *map_new = kv == 0 ? &maps.k_new : &maps.v_new;
+      const int box_page = Tr::kQuant ? lane % kTileGroups : lane / Tr::kHalves % kTileGroups, half = lane % Tr::kHalves;
+      Group g = group_of(t_lo);
+      bool ok = true;
+      int item = kv;
+      for (int j = t_lo; j < t_hi; ++j, item += 2) {
+        const uint32_t flags = flags_of(g);
+        const int page = __shfl_sync(0xffffffffu, g.page, box_page), base = __shfl_sync(0xffffffffu, g.base, box_page);
+        const int my_base = g.base;
+        float ks = 1.0f, vs = 1.0f;
+        if (Tr::kQuant && kv == 0 && g.page >= 0) {
+          ks = a.kv.k_scale[g.page];
+          vs = a.kv.v_scale[g.page];
         }
-        const CUtensorMap *map = kv == 0 ? &maps.k : &maps.v, *map_new = kv == 0 ? &maps.k_new : &maps.v_new;
-        const int box_page = lane / Tr::kHalves % kTileGroups, half = lane % Tr::kHalves;
-        Group g = group_of(t_lo);
-        bool ok = true;
-        item = kv;
-        for (int j = t_lo; j < t_hi; ++j, item += 2) {
-          const uint32_t flags = flags_of(g);
-          const int boxes = __popc(~(flags >> 8) & 0xffu) * Tr::kHalves;
-          const int page = __shfl_sync(0xffffffffu, g.page, box_page), base = __shfl_sync(0xffffffffu, g.base, box_page);
-          const int my_base = g.base;
-          g = group_of(j + 1);     // (its loads fly beside this tile's copies)
-          const int slot = item % kSlots;
-          ok = wait(&sh.empty[slot], (item / kSlots & 1) ^ 1);
-          if (!ok) break;
-          if (kv == 0) {
-            TileInfo &info = sh.info[(j - t_lo) % kInfos];
-            if (lane < kTileGroups) info.base[lane] = my_base;
-            if (lane == 0) info.flags = flags;
-            __syncwarp();
+        g = group_of(j + 1);     // (its loads fly beside this tile's copies)
+        const int slot = item % (Tr::kQuant ? kRawSlots : kSlots), turn = item / (Tr::kQuant ? kRawSlots : kSlots);
+        ok = wait(Tr::kQuant ? &sh.raw_empty[slot] : &sh.empty[slot], (turn & 1) ^ 1);
+        if (!ok) break;
+        if (kv == 0) {
+          TileInfo &info = sh.info[(j - t_lo) % kInfos];
+          if (lane < kTileGroups) {
+            info.base[lane] = my_base;
+            if constexpr (Tr::kQuant) {
+              float m;
+              info.ve[lane] = split_scale(vs, m);
+              info.ks[lane] = ks;
+              info.vs[lane] = m;
+            }
           }
-          if (lane == 0) mbar_arrive_expect_tx(&sh.full[slot], static_cast<uint32_t>(boxes * kPage * 128));
+          if (lane == 0) info.flags = flags;
+          __syncwarp();
+        }
+        if constexpr (Tr::kQuant) {
+          const int pages = __popc(~((flags >> 8) | (flags >> 16)) & 0xffu);
+          if (lane == 0) mbar_arrive_expect_tx(&sh.raw_full[slot], static_cast<uint32_t>(pages * kPage * D));
+          __syncwarp();
+          if (lane < kTileGroups && page >= 0)
+            bulk_g2s(raw_ring + slot * Tr::kRawBytes + lane * (kPage * D),
+                     static_cast<const uint8_t *>(kv == 0 ? a.kv.k_pool : a.kv.v_pool) + static_cast<int64_t>(page) * (kPage * D), kPage * D,
+                     &sh.raw_full[slot]);
+        } else {
+          uint64_t *bar = full_of(j, kv);
+          const int boxes = __popc(~(flags >> 8) & 0xffu) * Tr::kHalves;
+          if (lane == 0) mbar_arrive_expect_tx(bar, static_cast<uint32_t>(boxes * kPage * 128));
+          if (kv == 1 && j == t_hi - 1 && lane == 0) mbar_arrive(bar);     // (there is no next K)
           __syncwarp();
           if (lane < kTileGroups * Tr::kHalves && page != -2) {
             unsigned char *dst = ring + slot * Tr::kSlotBytes + half * Tr::kHalfBytes + box_page * (kPage * 128);
-            if (kTree && page == -1) tma_2d(dst, map_new, h * D + half * 64, static_cast<int>(row0) + base, &sh.full[slot]);
-            else tma_2d(dst, map, half * 64, page * kPage, &sh.full[slot]);
+            if (kTree && page == -1) tma_2d(dst, map_new, h * D + half * 64, static_cast<int>(row0) + base, bar);
+            else tma_2d(dst, map, half * 64, page * kPage, bar);
           }
         }
-        // (after a wait that ran out: the copies in flight land before the CTA leaves)
-        if (!ok)
-          for (int i = item - 2; i >= 0 && i > item - kSlots; i -= 2) mbar_wait_bounded(&sh.full[i % kSlots], i / kSlots & 1, a.st, p.wait_ns);
-      } else {
-        constexpr int kChunks = kPage * D / 16 / 32;     // 16-code loads of a lane and page
-        constexpr int kPerRow = D / 16;
-        const int cw = warp - Tr::kRowWarps - 1;         // takes groups 2 cw, 2 cw + 1 of a tile
-        if (cw == 0 && lane == 0) {
-          mbar_arrive_expect_tx(&sh.q_full, static_cast<uint32_t>(live_tiles * Tr::kHalves * p.tokens * G * 128));
-          for (int t = 0; t < live_tiles; ++t)
-            for (int x = 0; x < Tr::kHalves; ++x)
-              tma_3d(q_smem + t * (128 * D * 2) + x * 16384, &maps.q, x * 64, h * G, static_cast<int>(row0) + it.i0 + t * p.tokens, &sh.q_full);
-        }
-        struct Pages {
-          int page[2], base[2];
-        };
-        auto my_pages = [&](const Group &g) {
-          Pages x;
+      }
+      // (After a wait that ran out, copies in flight land before the CTA leaves. Their barriers may
+      // lack the other copy warp's arrival: this takes as long as a wait may last.)
+      if (!ok) wait(&sh.never, 0);
+    } else if (Tr::kQuant && warp >= 4 && warp < 8) {
+      // ---- conversion warps: groups 2 cw and 2 cw + 1 of every tile -----------------------------------
+      constexpr int kPieces = kPage * D / 16 / 32;       // 16-code pieces of a lane and page
+      constexpr int kRowStep = kPage / kPieces;          // a lane's pieces lie this many rows apart
+      const int cw = warp - 4;
+      const Keys &k = it.k;
+      const int64_t row0 = it.r.row0;
+      // A piece is two of a slot row's 16-byte chunks, so four lanes have 64 columns of one parity of
+      // chunks; the other four of a group of eight take the next row, whose swizzle has the other
+      // parity (and for d = 128 the other 64 columns, whose codes lie on the other banks).
+      const int sub = lane % 8, up = sub / 4;
+      const int row = Tr::kHalves == 2 ? lane / 16 * 2 + up : lane / 4;
+      const int column = Tr::kHalves == 2 ? (up ^ (lane / 8 & 1)) * 64 : 0, col = column + sub % 4 * 16;
+      const uint32_t at0 = (column / 64) * Tr::kHalfBytes + row * 128 + ((sub % 4 * 2) ^ (row & 7)) * 16;
+      // Piece c of the lane into the group whose rows begin at `rows` in the slot.
+      auto put = [&](unsigned char *rows, int c, uint4 lo, uint4 hi) {
+        const uint32_t at = (at0 ^ (c * kRowStep & 7) * 16) + c * (kRowStep * 128);
+        *reinterpret_cast<uint4 *>(rows + at) = lo;
+        *reinterpret_cast<uint4 *>(rows + (at ^ 16)) = hi;
+      };
+      int item = 0;
+      bool ok = true;
+      for (int j = t_lo; j < t_hi && ok; ++j) {
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv, ++item) {
+          const int slot = item % kSlots, raw = item % kRawSlots;
+          ok = wait(&sh.raw_full[raw], item / kRawSlots & 1) && wait(&sh.empty[slot], (item / kSlots & 1) ^ 1);
+          if (!ok) break;
+          const TileInfo &info = sh.info[(j - t_lo) % kInfos];
+          uint4 codes[2][kPieces];                       // (all on their way before the first store)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int c = 0; c < kPieces; ++c)
+              codes[i][c] = *reinterpret_cast<const uint4 *>(raw_ring + raw * Tr::kRawBytes + (2 * cw + i) * (kPage * D) + (c * kRowStep + row) * D + col);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            x.page[i] = __shfl_sync(0xffffffffu, g.page, 2 * cw + i);
-            x.base[i] = __shfl_sync(0xffffffffu, g.base, 2 * cw + i);
-          }
-          return x;
-        };
-        auto chunk_of = [&](int page, bool is_v, int c) -> uint4 {
-          const uint8_t *pool = static_cast<const uint8_t *>(is_v ? a.kv.v_pool : a.kv.k_pool);
-          return page >= 0 ? ld_stream16(pool + static_cast<int64_t>(page) * (kPage * D) + (c * 32 + lane) * 16) : make_uint4(0u, 0u, 0u, 0u);
-        };
-        // two bf16 chunks of 16 bytes at the place of a row's 16 elements from col on
-        auto put = [&](unsigned char *slot, int row, int col, uint4 lo, uint4 hi) {
-          unsigned char *at = slot + (col / 64) * Tr::kHalfBytes + row * 128;
-          const int c = col % 64 / 8;
-          *reinterpret_cast<uint4 *>(at + ((c ^ (row & 7)) * 16)) = lo;
-          *reinterpret_cast<uint4 *>(at + (((c + 1) ^ (row & 7)) * 16)) = hi;
-        };
-        // Writes an item (K or V of a tile) from the codes in raw, and loads the next one's behind them.
-        auto store = [&](const Pages &x, bool is_v, uint4 (&raw)[2][kChunks], const uint32_t (&two_e)[2], unsigned char *slot, const Pages &then) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int g_row = (2 * cw + i) * kPage;
-            if (kTree && x.page[i] == -1) {              // drafts are bf16 already
-              const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(is_v ? a.drafts.v_new : a.drafts.k_new) + static_cast<int64_t>(h) * D;
+            const int gi = 2 * cw + i, base = info.base[gi];
+            const uint32_t flags = info.flags >> gi;
+            unsigned char *rows = ring + slot * Tr::kSlotBytes + gi * (kPage * 128);
+            if (flags & 0x100u) continue;
+            if (kTree && (flags & 0x10000u)) {           // drafts are bf16 already
+              const __nv_bfloat16 *src = static_cast<const __nv_bfloat16 *>(kv == 0 ? a.drafts.k_new : a.drafts.v_new) + static_cast<int64_t>(it.h) * D + col;
 #pragma unroll 1
-              for (int c = lane; c < kPage * kPerRow; c += 32) {
-                const int row = c / kPerRow, col = c % kPerRow * 16;
+              for (int c = 0; c < kPieces; ++c) {
+                const int draft = base + c * kRowStep + row;
                 uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
-                if (x.base[i] + row < k.n_draft) {
-                  const __nv_bfloat16 *at = src + (row0 + x.base[i] + row) * a.drafts.row_stride + col;
+                if (draft < k.n_draft) {
+                  const __nv_bfloat16 *at = src + (row0 + draft) * a.drafts.row_stride;
                   lo = ld_stream16(at);
                   hi = ld_stream16(at + 8);
                 }
-                put(slot, g_row + row, col, lo, hi);
+                put(rows, c, lo, hi);
               }
+              continue;
             }
-            const __nv_bfloat162 e = *reinterpret_cast<const __nv_bfloat162 *>(&two_e[i]);
+            const float two_e = info.ve[gi];
 #pragma unroll
-            for (int c = 0; c < kChunks; ++c) {
-              const uint4 w = raw[i][c];
-              raw[i][c] = chunk_of(then.page[i], !is_v, c);
-              if (x.page[i] >= 0) {
-                const int chunk = c * 32 + lane, row = chunk / kPerRow, col = chunk % kPerRow * 16;
-                uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
-                if (x.base[i] + row < k.T) {
-                  codes_to_bf16<kKv == 2>(w.x, is_v, e, lo.x, lo.y);
-                  codes_to_bf16<kKv == 2>(w.y, is_v, e, lo.z, lo.w);
-                  codes_to_bf16<kKv == 2>(w.z, is_v, e, hi.x, hi.y);
-                  codes_to_bf16<kKv == 2>(w.w, is_v, e, hi.z, hi.w);
-                }
-                put(slot, g_row + row, col, lo, hi);
-              }
+            for (int c = 0; c < kPieces; ++c) {
+              const uint4 w = codes[i][c];
+              uint4 lo, hi;
+              codes_to_bf16<kKv == 2>(w.x, kv == 1, two_e, lo.x, lo.y);
+              codes_to_bf16<kKv == 2>(w.y, kv == 1, two_e, lo.z, lo.w);
+              codes_to_bf16<kKv == 2>(w.z, kv == 1, two_e, hi.x, hi.y);
+              codes_to_bf16<kKv == 2>(w.w, kv == 1, two_e, hi.z, hi.w);
+              put(rows, c, lo, hi);
             }
+            if (base + kPage > k.T)                      // zeros behind the last token
+#pragma unroll 1
+              for (int c = 0; c < kPieces; ++c)
+                if (base + c * kRowStep + row >= k.T) put(rows, c, make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u));
           }
           fence_proxy_async_smem();
           __syncwarp();
-        };
-        // (pages and their scales one tile ahead, codes one item ahead)
-        struct Scales {
-          float k, v;
-        };
-        auto scales_of = [&](const Group &g) -> Scales {
-          return g.page >= 0 ? Scales{a.kv.k_scale[g.page], a.kv.v_scale[g.page]} : Scales{1.0f, 1.0f};
-        };
-        Group g = group_of(t_lo);
-        Scales sc = scales_of(g);
-        Pages now = my_pages(g);
-        uint4 raw[2][kChunks];
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int c = 0; c < kChunks; ++c) raw[i][c] = chunk_of(now.page[i], false, c);
-        for (int j = t_lo; j < t_hi; ++j) {
-          const uint32_t flags = flags_of(g);
-          float vm = 1.0f;
-          const uint32_t ve = split_scale(sc.v, vm);
-          const uint32_t two_e[2] = {__shfl_sync(0xffffffffu, ve, 2 * cw), __shfl_sync(0xffffffffu, ve, 2 * cw + 1)};
-          const int my_base = g.base;
-          const float ks = sc.k;
-          g = group_of(j + 1);
-          const Pages next = my_pages(g);
-          int slot = item % kSlots;
-          if (!wait(&sh.empty[slot], (item / kSlots & 1) ^ 1)) break;
-          if (cw == 0) {
-            TileInfo &info = sh.info[(j - t_lo) % kInfos];
-            if (lane < kTileGroups) {
-              info.base[lane] = my_base;
-              info.ks[lane] = ks;
-              info.vs[lane] = vm;
-            }
-            if (lane == 0) info.flags = flags;
+          if (lane == 0) {
+            mbar_arrive(&sh.raw_empty[raw]);
+            mbar_arrive(full_of(j, kv));
+            if (kv == 1 && j == t_hi - 1) mbar_arrive(full_of(j, kv));     // (there is no next K)
           }
-          store(now, false, raw, two_e, ring + slot * Tr::kSlotBytes, now);
-          if (lane == 0) mbar_arrive(&sh.full[slot]);
-          ++item;
-          sc = scales_of(g);
-          slot = item % kSlots;
-          if (!wait(&sh.empty[slot], (item / kSlots & 1) ^ 1)) break;
-          store(now, true, raw, two_e, ring + slot * Tr::kSlotBytes, next);
-          if (lane == 0) mbar_arrive(&sh.full[slot]);
-          ++item;
-          now = next;
         }
       }
-    } else if (warp == Tr::kRowWarps) {
+    } else if (warp == 0) {
       // ---- product warp ------------------------------------------------------------------------
       constexpr uint32_t kShapeS = umma_shape(kKeyTile, false), kShapeO = umma_shape(D, true);
-      const int n = t_hi - t_lo, T = it.k.T;
+      const int n = t_hi - t_lo;
       const uint32_t lead = elect_lane();
       // Operands of the first slot and the first row tile; others lie at whole steps of the address field.
       const uint64_t q_op = umma_operand(smem_u32(q_smem), 16, 1024), k_op = umma_operand(smem_u32(ring), 16, 1024);
@@ -481,7 +470,7 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kTiles>::kThreads, 1)
         }
       };
       uint32_t started = 0;      // bit t: O of row tile t has been written
-      bool ok = wait(&sh.q_full, 0) && wait(&sh.full[0], 0);
+      bool ok = wait(&sh.q_full, 0) && wait(&sh.k0_full, 0);
       if (ok) {
         tmem_fence_after();
 #pragma unroll
@@ -493,33 +482,31 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kTiles>::kThreads, 1)
         umma_commit(lead, &sh.empty[0]);
       }
       for (int j = 0; j < n && ok; ++j) {
-        const int v_item = 2 * j + 1, v_slot = v_item % kSlots;
-        const int k_item = 2 * j + 2, k_slot = k_item % kSlots;
-        const TileInfo &info = sh.info[j % kInfos];
-        ok = wait(&sh.full[v_slot], v_item / kSlots & 1);
-        if (!ok) break;
+        const int v_slot = (2 * j + 1) % kSlots, k_slot = (2 * j + 2) % kSlots;
+        const uint64_t vd = v_op + static_cast<uint32_t>(v_slot * (Tr::kSlotBytes / 16));
+        const TileInfo &info = sh.info[j % kInfos];     // (it came with the tile's K)
         const uint32_t flags = info.flags;
+        const uint32_t pages = __reduce_or_sync(0xffffffffu, ~(flags >> 8) & 0xffu);
+        ok = wait(&sh.full[j % kInfos], j / kInfos & 1);      // V, and K of the next tile
+        if (!ok) break;
         if constexpr (!Tr::kQuant) {
           // rows of V past the cache's end or the drafts' are not zero by themselves
           uint32_t marked = flags & ~(flags >> 8) & 0xffu;
-          bool wrote = false;
-          while (marked != 0) {
-            const int i = __ffs(marked) - 1;
-            marked &= marked - 1;
-            const int end = (kTree && (flags >> (16 + i) & 1u)) ? it.k.n_draft : T;
-            const int kept = end - info.base[i];
-            if (kept >= kPage) continue;
-            wrote = true;
-            unsigned char *at = ring + v_slot * Tr::kSlotBytes + i * (kPage * 128);
-            for (int c = lane; c < (kPage - kept) * 8 * Tr::kHalves; c += 32)
-              *reinterpret_cast<uint4 *>(at + (c % Tr::kHalves) * Tr::kHalfBytes + kept * 128 + c / Tr::kHalves * 16) = make_uint4(0u, 0u, 0u, 0u);
+          if (marked != 0) {
+            while (marked != 0) {
+              const int i = __ffs(marked) - 1;
+              marked &= marked - 1;
+              const int end = (kTree && (flags >> (16 + i) & 1u)) ? it.k.n_draft : it.k.T;
+              const int kept = end - info.base[i];
+              if (kept >= kPage) continue;
+              unsigned char *at = ring + v_slot * Tr::kSlotBytes + i * (kPage * 128);
+              for (int c = lane; c < (kPage - kept) * 8 * Tr::kHalves; c += 32)
+                *reinterpret_cast<uint4 *>(at + (c % Tr::kHalves) * Tr::kHalfBytes + kept * 128 + c / Tr::kHalves * 16) = make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
           }
-          if (wrote) fence_proxy_async_smem();
-          __syncwarp();
         }
-        if (j + 1 < n) ok = wait(&sh.full[k_slot], k_item / kSlots & 1);
-        const uint64_t vd = v_op + static_cast<uint32_t>(v_slot * (Tr::kSlotBytes / 16));
-        const uint32_t there = __reduce_or_sync(0xffffffffu, ~(flags >> 8) & 0xffu);     // pages of the tile
 #pragma unroll
         for (int t = 0; t < kTiles; ++t) {
           if (t >= live_tiles || !ok) break;
@@ -528,17 +515,19 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kTiles>::kThreads, 1)
             ok = wait(&sh.p_full[t][part], j & 1);
             if (!ok) break;
             tmem_fence_after();
-            const uint32_t here = there >> (4 * part) & 0xfu;
-            if (here == 0xfu) {
+            constexpr int kFirst = kFirstKeys / kPage;
+            const int lo = part * kFirst, hi = part == 0 ? kFirst : kTileGroups;
+            const uint32_t all = (1u << hi) - (1u << lo), here = pages & all;
+            if (here == all) {
 #pragma unroll
-              for (int i = 4 * part; i < 4 * part + 4; ++i)
+              for (int i = lo; i < hi; ++i)
                 umma_ts(lead, o_tm[t], s_tm[t] + i * 8, vd + static_cast<uint32_t>(i * (kPage * 128 / 16)), kShapeO,
-                        i > 4 * part || (started >> t & 1u));
+                        i > lo || (started >> t & 1u));
               started |= 1u << t;
             } else {
 #pragma unroll 1
               for (uint32_t left = here; left != 0; left &= left - 1) {
-                const int i = 4 * part + __ffs(left) - 1;
+                const int i = __ffs(left) - 1;
                 umma_ts(lead, o_tm[t], s_tm[t] + i * 8, vd + static_cast<uint32_t>(i * (kPage * 128 / 16)), kShapeO,
                         (started >> t & 1u) != 0);
                 started |= 1u << t;
@@ -560,9 +549,9 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kTiles>::kThreads, 1)
         umma_commit(lead, &sh.drained);
         wait(&sh.drained, 0);
       }
-    } else {
+    } else if (warp >= Tr::kFirstRow) {
       // ---- row warps -----------------------------------------------------------------------------
-      const int t = warp / 4;
+      const int t = (warp - Tr::kFirstRow) / 4;
       if (t < live_tiles) {
         const int row = (warp % 4) * 32 + lane;
         const int i = it.i0 + t * p.tokens + row / G, gq = row % G;
@@ -589,87 +578,82 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kTiles>::kThreads, 1)
           if (any) {
             const TileInfo &info = sh.info[j % kInfos];
             const uint32_t flags = info.flags;
-            // bf16: the tile's logits stay in registers. 8-bit (whose copy warps need registers too):
-            // they are read twice, 32 at a time, for the maximum and for the weights.
-            constexpr bool kKeep = !Tr::kQuant;
-            float s[kKeep ? 128 : 32];
-            auto fetch = [&](int c32) {
-              tmem_ld32(s_at + c32 * 32, s);
-              tmem_wait_ld();
-            };
-            if constexpr (kKeep) {
-#pragma unroll
-              for (int c = 0; c < 4; ++c) tmem_ld32(s_at + c * 32, s + c * 32);
-            }
-            // What the row sees, a bit a key.
-            uint32_t seen[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
-            const bool masked = (flags & 0xffffu) != 0;
-            if (masked) {
-#pragma unroll
-              for (int gi = 0; gi < kTileGroups; ++gi) {
-                if ((flags >> gi | flags >> (8 + gi)) & 1u) {
-                  const int base = info.base[gi];
-                  uint32_t bits;
-                  if (flags >> (8 + gi) & 1u) {
-                    bits = 0;
-                  } else if constexpr (kTree) {
-                    if (flags >> (16 + gi) & 1u) {
-                      bits = static_cast<uint32_t>(mask >> base) & 0xffffu;
-                    } else {
-                      bits = (1u << min(k.T - base, kPage)) - 1u;
-                    }
-                  } else {
-                    // t <= p: keys [0, p - base]; t > p - local or t < sink: all but [sink - base, p - local - base]
-                    auto below = [](int x) -> uint32_t { return x <= 0 ? 0u : x >= 16 ? 0xffffu : (1u << x) - 1u; };
-                    bits = below(pos - base + 1);
-                    if (k.windowed) bits &= below(k.sink - base) | ~below(pos - k.local - base + 1);
-                  }
-                  seen[gi / 2] &= gi % 2 == 0 ? 0xffff0000u | bits : 0xffffu | bits << 16;
-                }
-              }
-            }
+            // Half a tile's logits are in registers at a time; the other half flies ahead of its use
+            // where the registers are there (bf16: fewer warps, more of them each).
+            constexpr bool kAhead = !Tr::kQuant;
             auto largest = [&](const float *x) -> float {      // of 16
               float top[4];
 #pragma unroll
               for (int c = 0; c < 4; ++c) top[c] = fmaxf(fmaxf(x[c], x[4 + c]), fmaxf(x[8 + c], x[12 + c]));
               return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
             };
-            if constexpr (kKeep) tmem_wait_ld();
-            auto half_max = [&](int half) -> float {
-              float mx = -INFINITY;
+            float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+            // The tile, with or without a look at what the row sees (a copy of the code each: the
+            // selections would otherwise be executed, switched off, for every tile).
+            auto tile = [&](auto with_mask) {
+              constexpr bool kMasked = decltype(with_mask)::value;
+              float first[64], ahead[kAhead ? 64 : 1];
+              float *const second = kAhead ? ahead : first;
+              uint32_t seen[4];            // a bit a key
+              auto read = [&](int half, float *to) {
+                tmem_ld32(s_at + half * 64, to);
+                tmem_ld32(s_at + half * 64 + 32, to + 32);
+              };
+              read(0, first);
+              if constexpr (kMasked) {
 #pragma unroll
-              for (int c32 = 2 * half; c32 < 2 * half + 2; ++c32) {
-                if constexpr (!kKeep) fetch(c32);
-                float *x = kKeep ? s + c32 * 32 : s;
-                if (masked) {
-#pragma unroll
-                  for (int c = 0; c < 32; ++c)
-                    if (!(seen[c32] >> c & 1u)) x[c] = -INFINITY;
-                }
-#pragma unroll
-                for (int gi = 0; gi < 2; ++gi) {
-                  float of = largest(x + gi * 16);
-                  if (Tr::kQuant && of != -INFINITY) of *= info.ks[c32 * 2 + gi];
-                  mx = fmaxf(mx, of);
+                for (int gi = 0; gi < kTileGroups; ++gi) {
+                  uint32_t bits = 0xffffu;
+                  if ((flags >> gi | flags >> (8 + gi)) & 1u) {
+                    const int base = info.base[gi];
+                    if (flags >> (8 + gi) & 1u) {
+                      bits = 0;
+                    } else if constexpr (kTree) {
+                      if (flags >> (16 + gi) & 1u) {
+                        bits = static_cast<uint32_t>(mask >> base) & 0xffffu;
+                      } else {
+                        bits = (1u << min(k.T - base, kPage)) - 1u;
+                      }
+                    } else {
+                      // t <= p: keys [0, p - base]; t > p - local or t < sink: all but [sink - base, p - local - base]
+                      auto below = [](int x) -> uint32_t { return x <= 0 ? 0u : x >= 16 ? 0xffffu : (1u << x) - 1u; };
+                      bits = below(pos - base + 1);
+                      if (k.windowed) bits &= below(k.sink - base) | ~below(pos - k.local - base + 1);
+                    }
+                  }
+                  if (gi % 2 == 0) seen[gi / 2] = bits & 0xffffu;
+                  else seen[gi / 2] |= bits << 16;
                 }
               }
-              return mx;
-            };
-            float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-            auto half_weights = [&](int half) {
-              const float base_m = m == -INFINITY ? 0.0f : -m * sc;
-              const float2 m2 = make_float2(base_m, base_m);
+              // Logits that the row does not see, of 64 keys, become -inf.
+              auto blank = [&](int half, float *x) {
+                if constexpr (kMasked) {
 #pragma unroll
-              for (int c32 = 2 * half; c32 < 2 * half + 2; ++c32) {
-                if constexpr (!kKeep) fetch(c32);
-                const float *from = kKeep ? s + c32 * 32 : s;
+                  for (int c = 0; c < 64; ++c)
+                    if (!(seen[2 * half + c / 32] >> (c % 32) & 1u)) x[c] = -INFINITY;
+                }
+              };
+              auto max_of = [&](int half, const float *x) -> float {
+                float mx = -INFINITY;
+#pragma unroll
+                for (int gi = 0; gi < 4; ++gi) {
+                  float of = largest(x + gi * 16);
+                  if (Tr::kQuant && of != -INFINITY) of *= info.ks[half * 4 + gi];
+                  mx = fmaxf(mx, of);
+                }
+                return mx;
+              };
+              // Weights of keys [32 c32, + 32), over the first logits.
+              auto weigh = [&](int c32, const float *x32) {
+                const float base_m = m == -INFINITY ? 0.0f : -m * sc;
+                const float2 m2 = make_float2(base_m, base_m);
                 uint32_t w[16];
 #pragma unroll
                 for (int x = 0; x < 16; ++x) {
                   const int gi = c32 * 2 + x / 8;
                   const float to_log2 = Tr::kQuant ? info.ks[gi] * sc : sc;
-                  float2 y = __ffma2_rn(make_float2(from[2 * x], from[2 * x + 1]), make_float2(to_log2, to_log2), m2);
-                  if (!kKeep && masked) {
+                  float2 y = __ffma2_rn(make_float2(x32[2 * x], x32[2 * x + 1]), make_float2(to_log2, to_log2), m2);
+                  if constexpr (Tr::kQuant && kMasked) {      // (a K scale of 0 makes a NaN of -inf)
                     if (!(seen[c32] >> (2 * x) & 1u)) y.x = -INFINITY;
                     if (!(seen[c32] >> (2 * x + 1) & 1u)) y.y = -INFINITY;
                   }
@@ -682,37 +666,66 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kTiles>::kThreads, 1)
                   w[x] = pack_bf16(e.x, e.y);
                 }
                 tmem_st16(s_at + c32 * 16, w);
+              };
+              auto hand_over = [&](int part) {
+                tmem_wait_st();
+                tmem_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.p_full[t][part]);
+              };
+              tmem_wait_ld<64>(first);
+              if constexpr (kAhead) read(1, ahead);
+              blank(0, first);
+              const float mx = fmaxf(max_of(0, first), pend);
+              bool late = false;
+              if (m == -INFINITY) {            // (nothing seen before: O's row is zero)
+                m = mx;
+                late = valid && m == -INFINITY;
               }
-              tmem_wait_st();
-              tmem_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&sh.p_full[t][half]);
-            };
-            const float mx = fmaxf(half_max(0), pend);
-            if (m == -INFINITY) m = mx;      // (nothing seen before: O's row is zero)
-            const bool grow = valid && (mx - m) * sc > 8.0f;
-            if (__any_sync(0xffffffffu, grow)) {
-              const float to = grow ? mx : m;
-              const float f = grow ? exp2_approx((m - to) * sc) : 1.0f;
-              m = to;
-              l *= f;
-              if (j > 0) {
-#pragma unroll 1
-                for (int c = 0; c < D / 16; ++c) {
-                  float o[16];
-                  tmem_ld16(o_at + c * 16, o);
-                  tmem_wait_ld();
-                  uint32_t w[16];
-#pragma unroll
-                  for (int x = 0; x < 16; ++x) w[x] = __float_as_uint(o[x] * f);
-                  tmem_st16(o_at + c * 16, w);
+              if (__any_sync(0xffffffffu, late)) {      // a row's first keys are in the second half
+                if constexpr (!kAhead) read(1, first);
+                tmem_wait_ld<64>(second);
+                blank(1, second);
+                const float then = max_of(1, second);
+                if (m == -INFINITY) m = then;
+                if constexpr (!kAhead) {
+                  read(0, first);
+                  tmem_wait_ld<64>(first);
+                  blank(0, first);
                 }
               }
-            }
-            half_weights(0);
-            pend = half_max(1);
-            if (m == -INFINITY) m = pend;    // (its row of O is still zero, its first half's weights too)
-            half_weights(1);
+              const bool grow = valid && (mx - m) * sc > 8.0f;
+              if (__any_sync(0xffffffffu, grow)) {
+                const float to = grow ? mx : m;
+                const float f = grow ? exp2_approx((m - to) * sc) : 1.0f;
+                m = to;
+                l *= f;
+                if (j > 0) {
+#pragma unroll 1
+                  for (int c = 0; c < D / 16; ++c) {
+                    float o[16];
+                    tmem_ld16(o_at + c * 16, o);
+                    tmem_wait_ld<16>(o);
+                    uint32_t w[16];
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) w[x] = __float_as_uint(o[x] * f);
+                    tmem_st16(o_at + c * 16, w);
+                  }
+                }
+              }
+              weigh(0, first);
+              weigh(1, first + 32);
+              if constexpr (!kAhead) read(1, first);
+              tmem_wait_ld<64>(second);
+              blank(1, second);
+              weigh(2, second);
+              hand_over(0);
+              weigh(3, second + 32);
+              hand_over(1);
+              pend = max_of(1, second);
+            };
+            if ((flags & 0xffffu) != 0) tile(std::true_type{});
+            else tile(std::false_type{});
             l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
           } else if (lane == 0) {
             mbar_arrive(&sh.p_full[t][0]);
@@ -732,7 +745,7 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kTiles>::kThreads, 1)
           for (int c = 0; c < D / 32; ++c) {
             float o[32];
             tmem_ld32(o_at + c * 32, o);
-            tmem_wait_ld();
+            tmem_wait_ld<32>(o);
 #pragma unroll
             for (int x = 0; x < 32; ++x) {
               if (l == 0.0f) o[x] = 0.0f;      // (a row that has seen nothing: no product may have written its O)
@@ -782,7 +795,7 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kTiles>::kThreads, 1)
   }
   tmem_fence_before();
   __syncthreads();
-  if (warp == Tr::kRowWarps) {
+  if (warp == 0) {
     tmem_fence_after();
     tmem_free(tmem, Tr::kColumns);
   }
