@@ -12,96 +12,118 @@ constexpr int kSms = 152;
 
 struct HostPlan {
   RowsPlan p;
-  int tiles;               // row tiles of a CTA
+  int rows;                // rows of a CTA: 32, 128 or 256
   int64_t items;
-  size_t rec_o_bytes, workspace_bytes;
+  size_t ml_at, heads_at, workspace_bytes;
 };
 
 HostPlan plan_rows(const bs_dims &d, int64_t n_rows, int max_new, bool tree) {
   HostPlan h{};
   const int G = d.n_q_heads / d.n_kv_heads;
-  h.p.tokens = 128 / G;
-  h.tiles = max_new <= h.p.tokens ? 1 : 2;
-  h.p.block_tokens = h.tiles * h.p.tokens;
+  h.rows = static_cast<int64_t>(max_new) * G <= 32 ? 32 : max_new <= 128 / G ? 128 : 256;
+  h.p.tokens = (h.rows == 32 ? 32 : 128) / G;
+  h.p.block_tokens = h.rows == 256 ? 2 * h.p.tokens : h.p.tokens;
   const int64_t per_seq = (static_cast<int64_t>(max_new) + h.p.block_tokens - 1) / h.p.block_tokens;
-  int64_t key_tiles;       // of a block, at most
+  int64_t tiles;           // key tiles of a block, at most
   if (tree) {
     h.p.n_blocks = static_cast<int>(per_seq);
     h.items = static_cast<int64_t>(d.batch) * d.n_kv_heads * per_seq;
-    key_tiles = (static_cast<int64_t>(d.max_gather_pages_per_unit) + (max_new + kPage - 1) / kPage + kTileGroups - 1) / kTileGroups;
+    tiles = (static_cast<int64_t>(d.max_gather_pages_per_unit) + (max_new + kPage - 1) / kPage + kTileGroups - 1) / kTileGroups;
   } else {
     const int64_t by_seq = per_seq * d.batch, by_rows = n_rows / h.p.block_tokens + (n_rows < d.batch ? n_rows : d.batch);
     const int64_t blocks = by_seq < by_rows ? by_seq : by_rows;
     h.p.n_blocks = static_cast<int>(blocks < INT32_MAX ? blocks : INT32_MAX);
     h.items = blocks * d.n_kv_heads;
-    key_tiles = (static_cast<int64_t>(d.max_pages_per_unit) + kTileGroups - 1) / kTileGroups;
+    tiles = (static_cast<int64_t>(d.max_pages_per_unit) + kTileGroups - 1) / kTileGroups;
   }
   h.p.record_rows = (max_new < h.p.block_tokens ? max_new : h.p.block_tokens) * G;
+  const int at_once = h.rows == 32 && d.kv_dtype == BS_BF16 ? 2 * kSms : kSms;   // CTAs
   int64_t splits = 1;
-  if (h.items <= kSms) splits = kSms / h.items;                                   // one wave
-  else if (h.tiles == 1 && key_tiles > 32) splits = (key_tiles + 23) / 24;       // pieces of about 24 tiles
-  if (splits > key_tiles) splits = key_tiles;
-  const int64_t most = (int64_t(64) << 20) / (static_cast<int64_t>(h.p.record_rows) * d.head_dim * 4) / h.items;   // records of 64 MB
-  if (splits > most) splits = most;
+  if (tree && h.items <= kSms) {                                      // a wave of CTAs over the units' own tiles
+    if (tiles > 1) h.p.even = at_once;
+    splits = tiles;
+  } else {
+    splits = at_once / h.items;                                       // what one wave has room for
+    if (h.rows < 256 && tiles > 32 && splits < (tiles + 23) / 24) splits = (tiles + 23) / 24;   // pieces of about 24 tiles
+  }
+  if (splits > tiles) splits = tiles;
+  const int64_t row_bytes = static_cast<int64_t>(h.p.record_rows) * d.head_dim * 4;
+  if (h.p.even == 0) {
+    const int64_t most = (int64_t(64) << 20) / row_bytes / h.items;   // records of 64 MB
+    if (splits > most) splits = most;
+  }
   h.p.splits = static_cast<int>(splits < 1 ? 1 : splits);
   if (h.p.splits > 1) {
-    const size_t recs = static_cast<size_t>(h.items) * h.p.splits * h.p.record_rows;
-    h.rec_o_bytes = recs * d.head_dim * sizeof(float);
-    h.workspace_bytes = h.rec_o_bytes + (recs * sizeof(float2) + 15) / 16 * 16;
+    const size_t recs = h.p.even > 0 ? h.p.even : static_cast<size_t>(h.items) * h.p.splits;
+    h.ml_at = recs * row_bytes;
+    h.heads_at = h.ml_at + (recs * h.p.record_rows * sizeof(float2) + 15) / 16 * 16;
+    h.workspace_bytes = h.heads_at + static_cast<size_t>(h.items) * sizeof(int4);
   }
   return h;
 }
 
 // ---------------------------------------------------------------------------------------
-// Merge of split rows: a warp a row, a lane D / 32 elements, records eight at a time in flight.
+// Merge of split rows: a warp a row, a lane D / 32 elements. Two loads one after the other (what the
+// item is; its records, eight of them at a time in flight beside the maxima).
 // ---------------------------------------------------------------------------------------
-constexpr int kMergeWarps = 8;
+constexpr int kMergeWarps = 4;
 
 template <int D, bool kTree>
 __global__ void __launch_bounds__(kMergeWarps * 32) rows_merge_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ RowsPlan p) {
-  constexpr int E = D / 32;
+  constexpr int E = D / 32, kAtOnce = 8;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.wait;" ::: "memory");      // the splits' records
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int64_t index = blockIdx.x;
-  RowsItem it;
-  find_item<kTree>(a, p, index, 1, it);                    // (errors are the first kernel's to report)
-  if (it.n_splits <= 1) return;                            // nothing to do, or written already
-  const int G = a.dims.n_q_heads / a.dims.n_kv_heads;
-  const int row = blockIdx.y * kMergeWarps + warp;
-  if (row >= (it.i1 - it.i0) * G) return;
-  const float *o = p.rec_o + (index * p.splits * p.record_rows + row) * D + lane * E;
-  const float2 *ml = p.rec_ml + index * p.splits * p.record_rows + row;
-  const int64_t step = p.record_rows;
+  const int item = blockIdx.x, row = blockIdx.y * kMergeWarps + warp;
+  const int4 head = p.heads[item];                         // CTAs, the first, first row, rows
+  const int G = a.dims.n_q_heads / a.dims.n_kv_heads, n = head.x;
+  if (n <= 1 || row >= head.w * G) return;                 // nothing to do, or written already
+  const int h = (kTree ? item / p.n_blocks : item) % a.dims.n_kv_heads;
+  const int64_t rec = static_cast<int64_t>(head.y) * p.record_rows + row, step = p.record_rows;
+  float o[kAtOnce][E];
+  auto load = [&](int s0) {
+#pragma unroll
+    for (int s = 0; s < kAtOnce; ++s)
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[s][e] = s0 + s < n ? p.rec_o[(rec + (s0 + s) * step) * D + lane * E + e] : 0.0f;
+  };
+  load(0);
   float m = -INFINITY;
-  for (int s = lane; s < it.n_splits; s += 32) m = fmaxf(m, ml[s * step].x);
+  for (int s = lane; s < n; s += 32) m = fmaxf(m, p.rec_ml[rec + s * step].x);
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
   float l = 0.0f, acc[E] = {};
-  auto add = [&]() -> bool {        // false: a sum is not finite
+  auto add = [&](bool again) -> bool {        // false: a sum is not finite
     l = 0.0f;
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.0f;
     if (m == -INFINITY) return true;
-#pragma unroll 8
-    for (int s = 0; s < it.n_splits; ++s) {
-      const float2 x = ml[s * step];
-      const float w = x.x == -INFINITY ? 0.0f : exp2f(x.x - m);
-      l = fmaf(x.y, w, l);
-      const float *at = o + s * step * D;
+    for (int s0 = 0; s0 < n; s0 += kAtOnce) {
+      float w = 0.0f, part = 0.0f;            // lane s: weight and sum of record s0 + s
+      if (lane < kAtOnce && s0 + lane < n) {
+        const float2 x = p.rec_ml[rec + (s0 + lane) * step];
+        w = x.x == -INFINITY ? 0.0f : exp2f(x.x - m);
+        part = x.y;
+      }
+      if (s0 > 0 || again) load(s0);
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] = fmaf(at[e], w, acc[e]);
+      for (int s = 0; s < kAtOnce; ++s) {
+        const float ws = __shfl_sync(0xffffffffu, w, s);
+        l = fmaf(__shfl_sync(0xffffffffu, part, s), ws, l);
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = fmaf(o[s][e], ws, acc[e]);
+      }
     }
-    float big = fabsf(l);
+    float odd = fabsf(l);
 #pragma unroll
-    for (int e = 0; e < E; ++e) big = big + 0.0f * acc[e];
-    return __all_sync(0xffffffffu, big < INFINITY);
+    for (int e = 0; e < E; ++e) odd = odd + 0.0f * acc[e];
+    return __all_sync(0xffffffffu, odd < INFINITY);
   };
-  if (!add()) {                     // (sums of the largest values of bf16: 2^24 below)
+  if (!add(false)) {                          // (sums of the largest values of bf16: 2^24 below)
     m += 24.0f;
-    add();
+    add(true);
   }
-  const int64_t out_row = (it.r.row0 + it.i0 + row / G) * a.dims.n_q_heads + it.h * G + row % G;
+  const int64_t out_row = (static_cast<int64_t>(head.z) + row / G) * a.dims.n_q_heads + h * G + row % G;
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   uint32_t *to = reinterpret_cast<uint32_t *>(a.out + out_row * D + lane * E);
 #pragma unroll
@@ -113,13 +135,15 @@ template <bool kTree>
 bs_status launch_rows(RowsArgs &a, void *workspace, size_t workspace_bytes, cudaStream_t cs) {
   const bs_dims &d = a.dims;
   HostPlan h = plan_rows(d, a.n_rows, a.max_new, kTree);
-  if (h.items * h.p.splits > INT32_MAX) return BS_ERR_CAPACITY;
+  if (h.items > INT32_MAX || h.items * h.p.splits > INT32_MAX) return BS_ERR_CAPACITY;
+  h.p.items = static_cast<int>(h.items);
   if (h.p.splits > 1) {
     if (workspace == nullptr) return BS_ERR_INVALID_ARG;
     if (!aligned16(workspace)) return BS_ERR_ALIGN;
     if (workspace_bytes < h.workspace_bytes) return BS_ERR_CAPACITY;
     h.p.rec_o = static_cast<float *>(workspace);
-    h.p.rec_ml = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + h.rec_o_bytes);
+    h.p.rec_ml = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + h.ml_at);
+    h.p.heads = reinterpret_cast<int4 *>(static_cast<char *>(workspace) + h.heads_at);
   }
   h.p.wait_ns = wait_limit_ns();
   const int G = d.n_q_heads / d.n_kv_heads;
@@ -140,8 +164,8 @@ bs_status launch_rows(RowsArgs &a, void *workspace, size_t workspace_bytes, cuda
     }
   }
   if (s != BS_OK) return s;
-  s = d.kv_dtype == BS_BF16 ? launch_rows_bf16<kTree>(a, h.p, maps, h.items, h.tiles, cs)
-                            : launch_rows_quant<kTree>(a, h.p, maps, h.items, h.tiles, cs);
+  s = d.kv_dtype == BS_BF16 ? launch_rows_bf16<kTree>(a, h.p, maps, h.rows, cs)
+                            : launch_rows_quant<kTree>(a, h.p, maps, h.rows, cs);
   if (s != BS_OK || h.p.splits == 1) return s;
   auto merge = d.head_dim == 128 ? rows_merge_kernel<128, kTree> : rows_merge_kernel<64, kTree>;
   const dim3 grid(static_cast<unsigned>(h.items), static_cast<unsigned>((h.p.record_rows + kMergeWarps - 1) / kMergeWarps));

@@ -41,13 +41,16 @@ constexpr int kFirstKeys = 96;                // keys whose weights are handed o
 constexpr int kInfos = 8;                     // tiles whose description is kept
 
 struct RowsPlan {
-  int tokens;         // tokens of a row tile: 128 / G
+  int tokens;         // tokens of a row tile: its rows / G
   int block_tokens;   // of a CTA
   int n_blocks;       // prefill: blocks of all sequences, at most; tree: of a sequence
-  int splits;         // CTAs a block's keys are split over, at most
+  int items;          // blocks of all units, at most
+  int splits;         // CTAs a block's keys are split over, at most (1: records unused)
+  int even;           // > 0: that many CTAs share all items' key tiles (tree_share)
   int record_rows;    // rows of a block, at most
-  float *rec_o;       // [item][split][record_rows][D], when splits > 1
-  float2 *rec_ml;     // [item][split][record_rows]: maximum (log2 units), sum
+  float *rec_o;       // [CTA][record_rows][D]: unnormalised outputs
+  float2 *rec_ml;     // [CTA][record_rows]: maximum (log2 units), sum
+  int4 *heads;        // [item]: CTAs that took part, the first of them, first row, rows
   uint64_t wait_ns;
 };
 
@@ -60,43 +63,106 @@ struct RowsItem {
   SeqRows r;
   Keys k;
   int b, h, i0, i1;       // tokens [i0, i1) of the sequence
-  int64_t index;          // item (for the records)
-  int t_lo, t_hi;         // key tiles of this split; empty: nothing to do
-  int n_splits;           // splits that have work
+  int item;
+  int t_lo, t_hi;         // key tiles of this CTA; empty: nothing to do
+  int n_splits, first;    // CTAs that share the item, the first of them
 };
 
-// Key tiles of split s of an item.
-__device__ __forceinline__ void split_tiles(const RowsPlan &p, int n_groups, int s, RowsItem &it) {
-  const int n = (n_groups + kTileGroups - 1) / kTileGroups;
-  const int per = max(1, (n + p.splits - 1) / p.splits);
-  it.n_splits = (n + per - 1) / per;
-  it.t_lo = min(s * per, n);
-  it.t_hi = min(it.t_lo + per, n);
+__device__ __forceinline__ int key_tiles(const Keys &k) { return (k.n_groups + kTileGroups - 1) / kTileGroups; }
+
+// Rows and keys of an item (tree): 0, or the status of a sequence or unit that does not fit (no tokens then).
+__device__ __forceinline__ int tree_item(const RowsArgs &a, const RowsPlan &p, int item, RowsItem &it) {
+  const int u = item / p.n_blocks, block = item - u * p.n_blocks;
+  it.b = u / a.dims.n_kv_heads;
+  it.h = u - it.b * a.dims.n_kv_heads;
+  it.i0 = it.i1 = 0;
+  int bad = seq_rows<true>(a, it.b, it.r);
+  if (bad != 0) return bad;
+  if (it.r.n <= block * p.block_tokens) return 0;
+  const int i0 = block * p.block_tokens, i1 = min(i0 + p.block_tokens, it.r.n);
+  bad = unit_keys<true>(a, it.r, u, i0, i1, it.k);
+  if (bad != 0) return bad;
+  it.i0 = i0;
+  it.i1 = i1;
+  return 0;
 }
 
-// Item of a CTA index, by a whole warp (every lane gets it). Errors are reported once.
-template <bool kTree>
-__device__ __forceinline__ void find_item(const RowsArgs &a, const RowsPlan &p, int64_t index, int split, RowsItem &it) {
+// The tree's few items (at most kShareItems) over p.even CTAs: pieces of `per` tiles, the smallest
+// number that does not ask for more CTAs, whatever the units' own sizes. Every CTA works this out by
+// itself (a warp; a lane looks at every 32nd item).
+constexpr int kShareItems = 160, kLaneItems = kShareItems / 32;
+__device__ __forceinline__ void tree_share(const RowsArgs &a, const RowsPlan &p, int cta, RowsItem &it) {
   const int lane = threadIdx.x & 31;
-  it.index = index;
+  int n[kLaneItems], total = 0;
+#pragma unroll
+  for (int q = 0; q < kLaneItems; ++q) {
+    const int item = q * 32 + lane;
+    n[q] = 0;
+    if (item < p.items) {
+      RowsItem x;
+      const int bad = tree_item(a, p, item, x);
+      if (bad != 0 && cta == 0) report(a.st, bad);
+      n[q] = x.i1 > x.i0 ? key_tiles(x.k) : 0;
+      if (n[q] == 0 && cta == 0) p.heads[item] = make_int4(0, 0, 0, 0);
+    }
+    total += n[q];
+  }
+  total = __reduce_add_sync(0xffffffffu, total);
+  int per = max(1, (total + p.even - 1) / p.even);
+  for (;; per += max(1, per / 16)) {
+    int ctas = 0;
+#pragma unroll
+    for (int q = 0; q < kLaneItems; ++q) ctas += (n[q] + per - 1) / per;
+    if (static_cast<int>(__reduce_add_sync(0xffffffffu, ctas)) <= p.even) break;   // (items are no more than CTAs)
+  }
+  int before = 0;
+  it.item = -1;
+#pragma unroll
+  for (int q = 0; q < kLaneItems; ++q) {
+    const int mine = (n[q] + per - 1) / per;
+    int sum = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += x;
+    }
+    const unsigned here = __ballot_sync(0xffffffffu, before + sum > cta);
+    if (it.item < 0 && here != 0) {
+      const int src = __ffs(here) - 1, tiles = __shfl_sync(0xffffffffu, n[q], src);
+      it.item = q * 32 + src;
+      it.n_splits = __shfl_sync(0xffffffffu, mine, src);
+      it.first = before + __shfl_sync(0xffffffffu, sum, src) - it.n_splits;
+      const int even = (tiles + it.n_splits - 1) / it.n_splits, s = cta - it.first;   // (pieces of a unit alike)
+      it.t_lo = min(s * even, tiles);
+      it.t_hi = min(it.t_lo + even, tiles);
+    }
+    before += __shfl_sync(0xffffffffu, sum, 31);
+  }
+  if (it.item >= 0) tree_item(a, p, it.item, it);
+}
+
+// Item of a CTA, by a whole warp (every lane gets it). Errors are reported once.
+template <bool kTree>
+__device__ __forceinline__ void find_item(const RowsArgs &a, const RowsPlan &p, int cta, RowsItem &it) {
+  const int lane = threadIdx.x & 31;
   it.t_lo = it.t_hi = it.n_splits = 0;
   it.i0 = it.i1 = 0;
-  int block;
+  if (kTree && p.even > 0) {
+    tree_share(a, p, cta, it);
+    return;
+  }
+  it.item = cta / p.splits;
+  it.first = it.item * p.splits;
+  const int split = cta - it.first;
   if constexpr (kTree) {
-    const int64_t u = index / p.n_blocks;
-    block = static_cast<int>(index - u * p.n_blocks);
-    it.b = static_cast<int>(u / a.dims.n_kv_heads);
-    it.h = static_cast<int>(u % a.dims.n_kv_heads);
-    const int bad = seq_rows<kTree>(a, it.b, it.r);
-    if (bad != 0 && lane == 0 && block == 0 && split == 0 && it.h == 0) report(a.st, bad);
-    if (it.r.n <= block * p.block_tokens) return;
+    const int bad = tree_item(a, p, it.item, it);
+    if (bad != 0 && lane == 0 && split == 0) report(a.st, bad);
   } else {
-    it.h = static_cast<int>(index % a.dims.n_kv_heads);
-    int at = static_cast<int>(index / a.dims.n_kv_heads);   // blocks before this one
-    const bool first = index == 0 && split == 0;            // looks at every sequence, and reports
+    it.h = it.item % a.dims.n_kv_heads;
+    int at = it.item / a.dims.n_kv_heads;                   // blocks before this one
+    const bool first = cta == 0;                            // looks at every sequence, and reports
     it.b = -1;
-    block = 0;
-    int total = 0;
+    int block = 0, total = 0;
     for (int b0 = 0; b0 < a.dims.batch && (it.b < 0 || first); b0 += 32) {
       SeqRows r;
       r.n = 0;
@@ -128,16 +194,23 @@ __device__ __forceinline__ void find_item(const RowsArgs &a, const RowsPlan &p, 
       total += all;
     }
     if (first && lane == 0 && total > p.n_blocks) report(a.st, BS_ERR_CAPACITY);   // sequences that share rows
-    if (it.b < 0) return;
+    if (it.b >= 0) {
+      it.i0 = block * p.block_tokens;
+      it.i1 = min(it.i0 + p.block_tokens, it.r.n);
+      const int bad = unit_keys<kTree>(a, it.r, it.b * a.dims.n_kv_heads + it.h, it.i0, it.i1, it.k);
+      if (bad != 0) {
+        if (lane == 0 && split == 0) report(a.st, bad);
+        it.i1 = it.i0;
+      }
+    }
   }
-  it.i0 = block * p.block_tokens;
-  it.i1 = min(it.i0 + p.block_tokens, it.r.n);
-  const int bad = unit_keys<kTree>(a, it.r, it.b * a.dims.n_kv_heads + it.h, it.i0, it.i1, it.k);
-  if (bad != 0) {
-    if (lane == 0 && split == 0) report(a.st, bad);
-    return;
+  if (it.i1 > it.i0) {
+    const int n = key_tiles(it.k), per = max(1, (n + p.splits - 1) / p.splits);
+    it.n_splits = (n + per - 1) / per;
+    it.t_lo = min(split * per, n);
+    it.t_hi = min(it.t_lo + per, n);
   }
-  split_tiles(p, it.k.n_groups, split, it);
+  if (p.splits > 1 && split == 0 && it.n_splits == 0 && lane == 0) p.heads[it.item] = make_int4(0, 0, 0, 0);
 }
 
 // Description of a key tile, written by the copy warps.
@@ -148,40 +221,51 @@ struct TileInfo {
   float ks[kTileGroups], vs[kTileGroups];   // 8-bit caches: K's scale, mantissa of V's
   float ve[kTileGroups];                    // and its power of two
 };
-constexpr int kRawSlots = 4;  // K or V tiles in codes
 
 struct RowsShared {
   RowsItem item;
   TileInfo info[kInfos];
   uint64_t empty[12];         // a slot's products are done
-  uint64_t raw_full[kRawSlots], raw_empty[kRawSlots];
+  uint64_t raw_full[8], raw_empty[8];
   uint64_t k0_full, full[kInfos];   // K of the first tile; V of a tile and K of the next one, have landed
   uint64_t q_full, s_full[2], p_full[2][2], o_full[2], drained, never;   // (p_full: [row tile][part])
   uint32_t tmem;
 };
 
-template <int D, int kKv, int kTiles>
+// kRows: rows of a CTA, 256 (two row tiles), 128 or 32. With 32 (single tokens, small trees) one row
+// warp and the first quarter of a tile do; the products' other rows are whatever lies behind the
+// queries, in rows of S and O that nobody reads. bf16: two such CTAs an SM, one's start beside the
+// other's keys (32 sequences' single tokens: 200 us with one, see the launcher for both).
+template <int D, int kKv, int kRows>
 struct RowsTraits {
   static constexpr bool kQuant = kKv != 0;              // 1: E4M3, 2: INT8
+  static constexpr int kTiles = kRows == 256 ? 2 : 1;
+  static constexpr int kPerSm = kRows == 32 && !kQuant ? 2 : 1;
   static constexpr int kHalves = D / 64;                // 128-byte columns of a row
   static constexpr int kSlotBytes = kKeyTile * D * 2;
   static constexpr int kHalfBytes = kKeyTile * 128;
-  static constexpr int kQBytes = kTiles * 128 * D * 2;
+  static constexpr int kQHalf = (kRows == 32 ? 32 : 128) * 128;   // 64 columns of a row tile's queries
+  static constexpr int kQTile = kQHalf * kHalves;
+  static constexpr int kQBytes = kTiles * kQTile;
   static constexpr int kControl = 2048;                 // RowsShared
-  static constexpr int kMaxDyn = 232448;                // shared memory of a CTA, at most
+  static constexpr int kMaxDyn = kPerSm == 2 ? 233472 / 2 - 1024 : 232448;   // shared memory of a CTA, at most
+  static constexpr int kRaw = !kQuant ? 0 : kRows == 32 ? 6 : 4;  // K or V tiles in codes
   static constexpr int kRawBytes = kQuant ? kKeyTile * D : 0;
-  static constexpr int kRoom = (kMaxDyn - 1024 - kControl - kQBytes - kRawSlots * kRawBytes) / kSlotBytes;
+  static constexpr int kRoom = (kMaxDyn - 1024 - kControl - kQBytes - kRaw * kRawBytes) / kSlotBytes;
   static constexpr int kSlots = kRoom < 12 ? kRoom : 12;
-  static constexpr int kRowWarps = 4 * kTiles;
-  static constexpr int kWriters = kQuant ? 4 : 1;      // warps that fill a slot
-  // Warp 0 issues products, warps 1 and 2 copy, (8-bit) warps 4 to 7 convert, one on each scheduler;
-  // the row warps start at a multiple of four.
-  static constexpr int kFirstRow = kQuant ? 8 : 4;
-  static constexpr int kThreads = 32 * (kFirstRow + kRowWarps);
+  static constexpr int kTileWarps = kRows == 32 ? 1 : 4;          // row warps of a tile
+  static constexpr int kRowWarps = kTileWarps * kTiles;
+  static constexpr int kWriters = kQuant ? 4 : 1;       // warps that fill a slot
+  // Product warp, two copy warps, (8-bit) conversion warps, one on each scheduler, row warps from a
+  // multiple of four.
+  static constexpr int kProduct = kRows == 32 ? 1 : 0, kCopy = kProduct + 1, kConvert = 4;
+  static constexpr int kFirstRow = kRows == 32 ? 0 : kQuant ? 8 : 4;
+  static constexpr int kThreads = 32 * (kRows == 32 ? (kQuant ? 8 : 4) : kFirstRow + kRowWarps);
   static constexpr int kColumns = kTiles == 1 ? 256 : 512;
-  static constexpr int kSmem = 1024 + kQBytes + kSlots * kSlotBytes + kRawSlots * kRawBytes + kControl;
+  static constexpr int kSmem = 1024 + kQBytes + kSlots * kSlotBytes + kRaw * kRawBytes + kControl;
   static_assert(sizeof(RowsShared) <= kControl, "control block");
-  static_assert(kSlots >= 3 && kSmem <= kMaxDyn, "ring");
+  static_assert(kSlots >= 3 && kRaw <= 8 && kSmem <= kMaxDyn, "ring");
+  static_assert(kQBytes + kSlots * kSlotBytes >= kQTile - kQHalf + 16384, "products read 128 rows");
 };
 
 // Flags of a group for the rows of tokens [i0, i1).
@@ -225,20 +309,20 @@ __device__ __forceinline__ float split_scale(float s, float &m) {
   return __uint_as_float((e == 0 ? 1u : e) << 23);
 }
 
-template <int D, int kKv, int kTiles, bool kTree>
-__global__ void __launch_bounds__(RowsTraits<D, kKv, kTiles>::kThreads, 1)
+template <int D, int kKv, int kRows, bool kTree>
+__global__ void __launch_bounds__(RowsTraits<D, kKv, kRows>::kThreads, RowsTraits<D, kKv, kRows>::kPerSm)
     rows_mma_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ RowsPlan p, const __grid_constant__ RowsMaps maps) {
-  using Tr = RowsTraits<D, kKv, kTiles>;
-  constexpr int kSlots = Tr::kSlots;
+  using Tr = RowsTraits<D, kKv, kRows>;
+  constexpr int kTiles = Tr::kTiles, kSlots = Tr::kSlots, kRaw = Tr::kQuant ? Tr::kRaw : 1;
   extern __shared__ unsigned char raw_smem[];
   unsigned char *smem = align_smem_1024(raw_smem);
   unsigned char *q_smem = smem, *ring = smem + Tr::kQBytes;
   unsigned char *raw_ring = ring + kSlots * Tr::kSlotBytes;
-  RowsShared &sh = *reinterpret_cast<RowsShared *>(raw_ring + kRawSlots * Tr::kRawBytes);
+  RowsShared &sh = *reinterpret_cast<RowsShared *>(raw_ring + Tr::kRaw * Tr::kRawBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = a.dims.n_q_heads / a.dims.n_kv_heads;
 
-  if (warp == 0) {
+  if (warp == Tr::kProduct) {
     tmem_alloc(&sh.tmem, Tr::kColumns);
     if (lane == 0) {
       for (int i = 0; i < kSlots; ++i) {
@@ -246,15 +330,15 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kTiles>::kThreads, 1)
       }
       mbar_init(&sh.k0_full, Tr::kWriters);
       for (int i = 0; i < kInfos; ++i) mbar_init(&sh.full[i], 2 * Tr::kWriters);
-      for (int i = 0; i < kRawSlots; ++i) {
+      for (int i = 0; i < kRaw; ++i) {
         mbar_init(&sh.raw_full[i], 1);
         mbar_init(&sh.raw_empty[i], Tr::kWriters);
       }
       mbar_init(&sh.q_full, 1);
       for (int t = 0; t < kTiles; ++t) {
         mbar_init(&sh.s_full[t], 1);
-        mbar_init(&sh.p_full[t][0], 4);
-        mbar_init(&sh.p_full[t][1], 4);
+        mbar_init(&sh.p_full[t][0], Tr::kTileWarps);
+        mbar_init(&sh.p_full[t][1], Tr::kTileWarps);
         mbar_init(&sh.o_full[t], 1);
       }
       mbar_init(&sh.drained, 1);
@@ -268,9 +352,12 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kTiles>::kThreads, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (warp == Tr::kFirstRow) {
     RowsItem it;
-    const int64_t index = blockIdx.x / p.splits;
-    find_item<kTree>(a, p, index, static_cast<int>(blockIdx.x - index * p.splits), it);
-    if (lane == 0) sh.item = it;
+    find_item<kTree>(a, p, static_cast<int>(blockIdx.x), it);
+    if (lane == 0) {
+      sh.item = it;
+      if (it.n_splits > 0 && it.first == static_cast<int>(blockIdx.x) && p.splits > 1)
+        p.heads[it.item] = make_int4(it.n_splits, it.first, static_cast<int>(it.r.row0) + it.i0, it.i1 - it.i0);
+    }
   }
   __syncthreads();
   tmem_fence_after();
@@ -292,11 +379,11 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kTiles>::kThreads, 1)
   };
 
   if (t_lo < t_hi) {
-    if (warp == 1 || warp == 2) {
-      // ---- copy warps: 1 K, 2 V -----------------------------------------------------------------
+    if (warp == Tr::kCopy || warp == Tr::kCopy + 1) {
+      // ---- copy warps: K, V -----------------------------------------------------------------
       const Keys k = it.k;
       const int64_t row0 = it.r.row0;
-      const int h = it.h, kv = warp - 1;
+      const int h = it.h, kv = warp - Tr::kCopy;
       auto group_of = [&](int j) -> Group {     // lanes 0..7: a tile's groups
         const int i = j * kTileGroups + lane;
         if (lane < kTileGroups && j < t_hi && i < k.n_groups) return key_group<kTree>(a, k, i);
@@ -312,7 +399,7 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kTiles>::kThreads, 1)
         mbar_arrive_expect_tx(&sh.q_full, static_cast<uint32_t>(live_tiles * Tr::kHalves * p.tokens * G * 128));
         for (int t = 0; t < live_tiles; ++t)
           for (int x = 0; x < Tr::kHalves; ++x)
-            tma_3d(q_smem + t * (128 * D * 2) + x * 16384, &maps.q, x * 64, h * G, static_cast<int>(row0) + it.i0 + t * p.tokens, &sh.q_full);
+            tma_3d(q_smem + t * Tr::kQTile + x * Tr::kQHalf, &maps.q, x * 64, h * G, static_cast<int>(row0) + it.i0 + t * p.tokens, &sh.q_full);
       }
       const CUtensorMap *map = kv == 0 ? &maps.k : &maps.v, *map_new = kv == 0 ? &maps.k_new : &maps.v_new;
       const int box_page = Tr::kQuant ? lane % kTileGroups : lane / Tr::kHalves % kTileGroups, half = lane % Tr::kHalves;
@@ -329,7 +416,7 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kTiles>::kThreads, 1)
           vs = a.kv.v_scale[g.page];
         }
         g = group_of(j + 1);     // (its loads fly beside this tile's copies)
-        const int slot = item % (Tr::kQuant ? kRawSlots : kSlots), turn = item / (Tr::kQuant ? kRawSlots : kSlots);
+        const int slot = item % (Tr::kQuant ? kRaw : kSlots), turn = item / (Tr::kQuant ? kRaw : kSlots);
         ok = wait(Tr::kQuant ? &sh.raw_empty[slot] : &sh.empty[slot], (turn & 1) ^ 1);
         if (!ok) break;
         if (kv == 0) {
@@ -370,11 +457,11 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kTiles>::kThreads, 1)
       // (After a wait that ran out, copies in flight land before the CTA leaves. Their barriers may
       // lack the other copy warp's arrival: this takes as long as a wait may last.)
       if (!ok) wait(&sh.never, 0);
-    } else if (Tr::kQuant && warp >= 4 && warp < 8) {
+    } else if (Tr::kQuant && warp >= Tr::kConvert && warp < Tr::kConvert + 4) {
       // ---- conversion warps: groups 2 cw and 2 cw + 1 of every tile -----------------------------------
       constexpr int kPieces = kPage * D / 16 / 32;       // 16-code pieces of a lane and page
       constexpr int kRowStep = kPage / kPieces;          // a lane's pieces lie this many rows apart
-      const int cw = warp - 4;
+      const int cw = warp - Tr::kConvert;
       const Keys &k = it.k;
       const int64_t row0 = it.r.row0;
       // A piece is two of a slot row's 16-byte chunks, so four lanes have 64 columns of one parity of
@@ -395,8 +482,8 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kTiles>::kThreads, 1)
       for (int j = t_lo; j < t_hi && ok; ++j) {
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv, ++item) {
-          const int slot = item % kSlots, raw = item % kRawSlots;
-          ok = wait(&sh.raw_full[raw], item / kRawSlots & 1) && wait(&sh.empty[slot], (item / kSlots & 1) ^ 1);
+          const int slot = item % kSlots, raw = item % kRaw;
+          ok = wait(&sh.raw_full[raw], item / kRaw & 1) && wait(&sh.empty[slot], (item / kSlots & 1) ^ 1);
           if (!ok) break;
           const TileInfo &info = sh.info[(j - t_lo) % kInfos];
           uint4 codes[2][kPieces];                       // (all on their way before the first store)
@@ -451,7 +538,7 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kTiles>::kThreads, 1)
           }
         }
       }
-    } else if (warp == 0) {
+    } else if (warp == Tr::kProduct) {
       // ---- product warp ------------------------------------------------------------------------
       constexpr uint32_t kShapeS = umma_shape(kKeyTile, false), kShapeO = umma_shape(D, true);
       const int n = t_hi - t_lo;
@@ -462,11 +549,11 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kTiles>::kThreads, 1)
       const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
       const uint32_t s_tm[2] = {tm, tm + 128}, o_tm[2] = {tm + 128 * kTiles, tm + 128 * kTiles + 128};
       auto logits = [&](int t, int slot) {      // S of row tile t
-        const uint64_t kd = k_op + static_cast<uint32_t>(slot * (Tr::kSlotBytes / 16)), qd = q_op + static_cast<uint32_t>(t * (128 * D * 2 / 16));
+        const uint64_t kd = k_op + static_cast<uint32_t>(slot * (Tr::kSlotBytes / 16)), qd = q_op + static_cast<uint32_t>(t * (Tr::kQTile / 16));
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t off = (kk / 4) * (16384 / 16) + (kk % 4) * (32 / 16);
-          umma_ss(lead, s_tm[t], qd + off, kd + off, kShapeS, kk > 0);
+          const uint32_t in = (kk % 4) * (32 / 16);
+          umma_ss(lead, s_tm[t], qd + (kk / 4) * (Tr::kQHalf / 16) + in, kd + (kk / 4) * (Tr::kHalfBytes / 16) + in, kShapeS, kk > 0);
         }
       };
       uint32_t started = 0;      // bit t: O of row tile t has been written
@@ -549,9 +636,9 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kTiles>::kThreads, 1)
         umma_commit(lead, &sh.drained);
         wait(&sh.drained, 0);
       }
-    } else if (warp >= Tr::kFirstRow) {
+    } else if (warp >= Tr::kFirstRow && warp < Tr::kFirstRow + Tr::kRowWarps) {
       // ---- row warps -----------------------------------------------------------------------------
-      const int t = (warp - Tr::kFirstRow) / 4;
+      const int t = (warp - Tr::kFirstRow) / Tr::kTileWarps;
       if (t < live_tiles) {
         const int row = (warp % 4) * 32 + lane;
         const int i = it.i0 + t * p.tokens + row / G, gq = row % G;
@@ -795,34 +882,40 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kTiles>::kThreads, 1)
   }
   tmem_fence_before();
   __syncthreads();
-  if (warp == 0) {
+  if (warp == Tr::kProduct) {
     tmem_fence_after();
     tmem_free(tmem, Tr::kColumns);
   }
 }
 
-template <int D, int kKv, int kTiles, bool kTree>
-bs_status launch_rows_mma(const RowsArgs &a, const RowsPlan &p, const RowsMaps &maps, int64_t items, cudaStream_t cs) {
-  using Tr = RowsTraits<D, kKv, kTiles>;
-  auto kernel = rows_mma_kernel<D, kKv, kTiles, kTree>;
+template <int D, int kKv, int kRows, bool kTree>
+bs_status launch_rows_mma(const RowsArgs &a, const RowsPlan &p, const RowsMaps &maps, cudaStream_t cs) {
+  using Tr = RowsTraits<D, kKv, kRows>;
+  auto kernel = rows_mma_kernel<D, kKv, kRows, kTree>;
   static OncePerDevice attrs;
   if (!attrs([&] { return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Tr::kSmem) == cudaSuccess; }))
     return BS_ERR_CUDA;
-  const dim3 grid(static_cast<unsigned>(items * p.splits));
+  const dim3 grid(static_cast<unsigned>(p.even > 0 ? p.even : p.items * p.splits));
   return launch_ex(kernel, grid, Tr::kThreads, Tr::kSmem, cs, 0, true, a, p, maps) == cudaSuccess ? BS_OK : BS_ERR_CUDA;
 }
 
-// By the row tiles of a CTA (1 or 2) and the cache's type; each in a file of its own.
+// By the rows of a CTA (32, 128 or 256) and the cache's type; each in a file of its own.
 template <bool kTree>
-bs_status launch_rows_bf16(const RowsArgs &a, const RowsPlan &p, const RowsMaps &maps, int64_t items, int tiles, cudaStream_t cs);
+bs_status launch_rows_bf16(const RowsArgs &a, const RowsPlan &p, const RowsMaps &maps, int rows, cudaStream_t cs);
 template <bool kTree>
-bs_status launch_rows_quant(const RowsArgs &a, const RowsPlan &p, const RowsMaps &maps, int64_t items, int tiles, cudaStream_t cs);
+bs_status launch_rows_quant(const RowsArgs &a, const RowsPlan &p, const RowsMaps &maps, int rows, cudaStream_t cs);
 
+template <int D, int kKv, bool kTree>
+bs_status dispatch_rows(const RowsArgs &a, const RowsPlan &p, const RowsMaps &maps, int rows, cudaStream_t cs) {
+  switch (rows) {
+    case 32: return launch_rows_mma<D, kKv, 32, kTree>(a, p, maps, cs);
+    case 128: return launch_rows_mma<D, kKv, 128, kTree>(a, p, maps, cs);
+    default: return launch_rows_mma<D, kKv, 256, kTree>(a, p, maps, cs);
+  }
+}
 template <int kKv, bool kTree>
-bs_status dispatch_rows(const RowsArgs &a, const RowsPlan &p, const RowsMaps &maps, int64_t items, int tiles, cudaStream_t cs) {
-  if (a.dims.head_dim == 128)
-    return tiles == 1 ? launch_rows_mma<128, kKv, 1, kTree>(a, p, maps, items, cs) : launch_rows_mma<128, kKv, 2, kTree>(a, p, maps, items, cs);
-  return tiles == 1 ? launch_rows_mma<64, kKv, 1, kTree>(a, p, maps, items, cs) : launch_rows_mma<64, kKv, 2, kTree>(a, p, maps, items, cs);
+bs_status dispatch_rows(const RowsArgs &a, const RowsPlan &p, const RowsMaps &maps, int rows, cudaStream_t cs) {
+  return a.dims.head_dim == 128 ? dispatch_rows<128, kKv, kTree>(a, p, maps, rows, cs) : dispatch_rows<64, kKv, kTree>(a, p, maps, rows, cs);
 }
 
 }  // namespace bsi

@@ -4,8 +4,8 @@
 namespace bsi {
 
 template <>
-bs_status launch_rows_bf16<true>(const RowsArgs &a, const RowsPlan &p, const RowsMaps &maps, int64_t items, int tiles, cudaStream_t cs) {
-  return dispatch_rows<0, true>(a, p, maps, items, tiles, cs);
+bs_status launch_rows_bf16<true>(const RowsArgs &a, const RowsPlan &p, const RowsMaps &maps, int rows, cudaStream_t cs) {
+  return dispatch_rows<0, true>(a, p, maps, rows, cs);
 }
 
 }  // namespace bsi

@@ -4,9 +4,9 @@
 namespace bsi {
 
 template <>
-bs_status launch_rows_quant<true>(const RowsArgs &a, const RowsPlan &p, const RowsMaps &maps, int64_t items, int tiles, cudaStream_t cs) {
-  return a.dims.kv_dtype == BS_INT8 ? dispatch_rows<2, true>(a, p, maps, items, tiles, cs)
-                                    : dispatch_rows<1, true>(a, p, maps, items, tiles, cs);
+bs_status launch_rows_quant<true>(const RowsArgs &a, const RowsPlan &p, const RowsMaps &maps, int rows, cudaStream_t cs) {
+  return a.dims.kv_dtype == BS_INT8 ? dispatch_rows<2, true>(a, p, maps, rows, cs)
+                                    : dispatch_rows<1, true>(a, p, maps, rows, cs);
 }
 
 }  // namespace bsi
