@@ -35,19 +35,28 @@ struct SeqRows {
   int64_t row0;
 };
 
+// What is told of a sequence: tokens, drafts or first new token, first row.
+struct SeqWords {
+  int T, x;
+  int64_t row0;
+};
+template <bool kTree>
+__device__ __forceinline__ SeqWords seq_words(const RowsArgs &a, int b) {
+  return SeqWords{a.kv.seq_lens[b], kTree ? a.drafts.n_draft[b] : a.tok_begin[b], a.row_begin[b]};
+}
+
 // 0, or the status of a sequence that does not fit (its n is then 0).
 template <bool kTree>
-__device__ __forceinline__ int seq_rows(const RowsArgs &a, int b, SeqRows &r) {
+__device__ __forceinline__ int seq_rows(const RowsArgs &a, const SeqWords &w, SeqRows &r) {
+  const int T = w.T, x = w.x;
   r.n = 0;
-  const int T = a.kv.seq_lens[b];
-  const int x = kTree ? a.drafts.n_draft[b] : a.tok_begin[b];
-  r.row0 = a.row_begin[b];
+  r.row0 = w.row0;
   r.T = T;
   r.p0 = kTree ? 0 : x;
   if (T < 0 || x < 0 || x > (kTree ? a.max_new : T)) return BS_ERR_INVALID_ARG;
   const int n = kTree ? x : T - x;
   if (n == 0) return 0;
-  if ((static_cast<int64_t>(T) + kPage - 1) / kPage > a.dims.max_pages_per_unit || n > a.max_new) return BS_ERR_CAPACITY;
+  if (T / kPage + (T % kPage != 0) > a.dims.max_pages_per_unit || n > a.max_new) return BS_ERR_CAPACITY;
   if (r.row0 < 0 || r.row0 + n > (kTree ? a.drafts.n_rows : a.n_rows)) return BS_ERR_DEVICE_BOUNDS;
   r.n = n;
   return 0;
@@ -66,8 +75,18 @@ struct Keys {
   const int32_t *table;      // its page table
 };
 
+// What is told of a unit: tree, tokens of a block and selected blocks; prefill, class, sink and window.
+struct UnitWords {
+  int x, y, z;
+};
 template <bool kTree>
-__device__ __forceinline__ int unit_keys(const RowsArgs &a, const SeqRows &r, int u, int i0, int i1, Keys &k) {
+__device__ __forceinline__ UnitWords unit_words(const RowsArgs &a, int u) {
+  if constexpr (kTree) return UnitWords{a.block_tokens[u], a.sel_cnt[u], 0};
+  else return UnitWords{a.cls[u], a.sink_tokens[u], a.local_tokens[u]};
+}
+
+template <bool kTree>
+__device__ __forceinline__ int unit_keys(const RowsArgs &a, const SeqRows &r, const UnitWords &w, int u, int i0, int i1, Keys &k) {
   k.T = r.T;
   k.p0 = r.p0;
   k.table = a.kv.page_table + static_cast<int64_t>(u) * a.dims.max_pages_per_unit;
@@ -77,7 +96,7 @@ __device__ __forceinline__ int unit_keys(const RowsArgs &a, const SeqRows &r, in
   k.sel = nullptr;
   k.n_cache = k.n_groups = 0;
   if constexpr (kTree) {
-    const int g = a.block_tokens[u], cnt = a.sel_cnt[u];
+    const int g = w.x, cnt = w.y;
     if (g <= 0 || g % kPage != 0 || cnt < 0) return BS_ERR_INVALID_ARG;
     k.ppb = g / kPage;
     if (cnt > a.dims.max_sel_per_unit || static_cast<int64_t>(cnt) * k.ppb > a.dims.max_gather_pages_per_unit)
@@ -87,13 +106,13 @@ __device__ __forceinline__ int unit_keys(const RowsArgs &a, const SeqRows &r, in
     k.n_cache = cnt * k.ppb;
     k.n_groups = k.n_cache + (r.n + kPage - 1) / kPage;
   } else {
-    const int cls = a.cls[u];
+    const int cls = w.x;
     if (cls < BS_STREAMING || cls > BS_DUAL) return BS_ERR_INVALID_ARG;
     const int pa = r.p0 + i0, pb = r.p0 + i1 - 1;
     if (cls == BS_STREAMING) {
       k.windowed = true;
-      k.sink = a.sink_tokens[u];
-      k.local = a.local_tokens[u];
+      k.sink = w.y;
+      k.local = w.z;
       if (k.sink < 0 || k.local < 1) return BS_ERR_INVALID_ARG;
       k.first = max(pa - k.local + 1, 0) / kPage;
       k.n_sink = min(k.sink / kPage + (k.sink % kPage != 0), k.first);

@@ -31,13 +31,12 @@
 #include "bs_rows_attn.cuh"
 #include "bs_umma.cuh"
 
-#include <type_traits>
-
 namespace bsi {
 
 constexpr int kKeyTile = 128;                 // keys of a tile
 constexpr int kTileGroups = kKeyTile / kPage; // groups of a tile
 constexpr int kFirstKeys = 96;                // keys whose weights are handed over first
+constexpr int kShareItems = 64;               // tree: items whose key tiles a wave of CTAs shares
 constexpr int kInfos = 8;                     // tiles whose description is kept
 
 struct RowsPlan {
@@ -58,6 +57,19 @@ struct RowsMaps {
   CUtensorMap q, k, v, k_new, v_new;
 };
 
+// 32 bytes, in one instruction where the address allows (a lane's row is far from the next lane's:
+// each store then fills the sectors it touches).
+__device__ __forceinline__ void store_sector(void *to, const uint32_t *w, bool aligned) {
+  if (aligned) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]),
+                 "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4 *>(to)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    reinterpret_cast<uint4 *>(to)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
 // What a CTA works on.
 struct RowsItem {
   SeqRows r;
@@ -70,29 +82,43 @@ struct RowsItem {
 
 __device__ __forceinline__ int key_tiles(const Keys &k) { return (k.n_groups + kTileGroups - 1) / kTileGroups; }
 
-// Rows and keys of an item (tree): 0, or the status of a sequence or unit that does not fit (no tokens then).
-__device__ __forceinline__ int tree_item(const RowsArgs &a, const RowsPlan &p, int item, RowsItem &it) {
+// Rows and keys of a tree's item from what is told of it: 0, or the status of a sequence or unit
+// that does not fit (no tokens then).
+struct ItemWords {
+  SeqWords seq;
+  UnitWords unit;
+};
+__device__ __forceinline__ ItemWords tree_words(const RowsArgs &a, const RowsPlan &p, int item) {
+  const int u = item / p.n_blocks;
+  return ItemWords{seq_words<true>(a, u / a.dims.n_kv_heads), unit_words<true>(a, u)};
+}
+__device__ __forceinline__ int tree_item(const RowsArgs &a, const RowsPlan &p, int item, const ItemWords &w, RowsItem &it) {
   const int u = item / p.n_blocks, block = item - u * p.n_blocks;
   it.b = u / a.dims.n_kv_heads;
   it.h = u - it.b * a.dims.n_kv_heads;
   it.i0 = it.i1 = 0;
-  int bad = seq_rows<true>(a, it.b, it.r);
+  int bad = seq_rows<true>(a, w.seq, it.r);
   if (bad != 0) return bad;
   if (it.r.n <= block * p.block_tokens) return 0;
   const int i0 = block * p.block_tokens, i1 = min(i0 + p.block_tokens, it.r.n);
-  bad = unit_keys<true>(a, it.r, u, i0, i1, it.k);
+  bad = unit_keys<true>(a, it.r, w.unit, u, i0, i1, it.k);
   if (bad != 0) return bad;
   it.i0 = i0;
   it.i1 = i1;
   return 0;
 }
 
-// The tree's few items (at most kShareItems) over p.even CTAs: pieces of `per` tiles, the smallest
-// number that does not ask for more CTAs, whatever the units' own sizes. Every CTA works this out by
-// itself (a warp; a lane looks at every 32nd item).
-constexpr int kShareItems = 160, kLaneItems = kShareItems / 32;
+// The tree's few items (at most kShareItems) over p.even CTAs: pieces of `per` tiles, about the
+// smallest number that does not ask for more CTAs, whatever the units' own sizes; a key tile against
+// two row tiles counts twice. Every CTA works this out by itself: a warp, a lane to every 32nd item,
+// one round of loads.
+constexpr int kLaneItems = kShareItems / 32;
 __device__ __forceinline__ void tree_share(const RowsArgs &a, const RowsPlan &p, int cta, RowsItem &it) {
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, used = (p.items + 31) / 32;
+  ItemWords w[kLaneItems];
+#pragma unroll
+  for (int q = 0; q < kLaneItems; ++q)
+    if (q < used) w[q] = tree_words(a, p, min(q * 32 + lane, p.items - 1));
   int n[kLaneItems], total = 0;
 #pragma unroll
   for (int q = 0; q < kLaneItems; ++q) {
@@ -100,9 +126,9 @@ __device__ __forceinline__ void tree_share(const RowsArgs &a, const RowsPlan &p,
     n[q] = 0;
     if (item < p.items) {
       RowsItem x;
-      const int bad = tree_item(a, p, item, x);
+      const int bad = tree_item(a, p, item, w[q], x);
       if (bad != 0 && cta == 0) report(a.st, bad);
-      n[q] = x.i1 > x.i0 ? key_tiles(x.k) : 0;
+      n[q] = x.i1 > x.i0 ? key_tiles(x.k) * (x.i1 - x.i0 > p.tokens ? 2 : 1) : 0;
       if (n[q] == 0 && cta == 0) p.heads[item] = make_int4(0, 0, 0, 0);
     }
     total += n[q];
@@ -112,13 +138,15 @@ __device__ __forceinline__ void tree_share(const RowsArgs &a, const RowsPlan &p,
   for (;; per += max(1, per / 16)) {
     int ctas = 0;
 #pragma unroll
-    for (int q = 0; q < kLaneItems; ++q) ctas += (n[q] + per - 1) / per;
+    for (int q = 0; q < kLaneItems; ++q)
+      if (q < used) ctas += (n[q] + per - 1) / per;
     if (static_cast<int>(__reduce_add_sync(0xffffffffu, ctas)) <= p.even) break;   // (items are no more than CTAs)
   }
   int before = 0;
   it.item = -1;
 #pragma unroll
   for (int q = 0; q < kLaneItems; ++q) {
+    if (q >= used) break;
     const int mine = (n[q] + per - 1) / per;
     int sum = mine;
 #pragma unroll
@@ -128,17 +156,27 @@ __device__ __forceinline__ void tree_share(const RowsArgs &a, const RowsPlan &p,
     }
     const unsigned here = __ballot_sync(0xffffffffu, before + sum > cta);
     if (it.item < 0 && here != 0) {
-      const int src = __ffs(here) - 1, tiles = __shfl_sync(0xffffffffu, n[q], src);
+      const int src = __ffs(here) - 1;
       it.item = q * 32 + src;
       it.n_splits = __shfl_sync(0xffffffffu, mine, src);
       it.first = before + __shfl_sync(0xffffffffu, sum, src) - it.n_splits;
-      const int even = (tiles + it.n_splits - 1) / it.n_splits, s = cta - it.first;   // (pieces of a unit alike)
+      ItemWords x;
+      x.seq.T = __shfl_sync(0xffffffffu, w[q].seq.T, src);
+      x.seq.x = __shfl_sync(0xffffffffu, w[q].seq.x, src);
+      x.seq.row0 = __shfl_sync(0xffffffffu, w[q].seq.row0, src);
+      x.unit.x = __shfl_sync(0xffffffffu, w[q].unit.x, src);
+      x.unit.y = __shfl_sync(0xffffffffu, w[q].unit.y, src);
+      x.unit.z = 0;
+      tree_item(a, p, it.item, x, it);
+      const int tiles = key_tiles(it.k), s = cta - it.first;
+      it.n_splits = min(it.n_splits, tiles);
+      const int even = (tiles + it.n_splits - 1) / it.n_splits;      // (pieces of a unit alike)
+      it.n_splits = (tiles + even - 1) / even;
       it.t_lo = min(s * even, tiles);
       it.t_hi = min(it.t_lo + even, tiles);
     }
     before += __shfl_sync(0xffffffffu, sum, 31);
   }
-  if (it.item >= 0) tree_item(a, p, it.item, it);
 }
 
 // Item of a CTA, by a whole warp (every lane gets it). Errors are reported once.
@@ -155,7 +193,7 @@ __device__ __forceinline__ void find_item(const RowsArgs &a, const RowsPlan &p, 
   it.first = it.item * p.splits;
   const int split = cta - it.first;
   if constexpr (kTree) {
-    const int bad = tree_item(a, p, it.item, it);
+    const int bad = tree_item(a, p, it.item, tree_words(a, p, it.item), it);
     if (bad != 0 && lane == 0 && split == 0) report(a.st, bad);
   } else {
     it.h = it.item % a.dims.n_kv_heads;
@@ -169,7 +207,7 @@ __device__ __forceinline__ void find_item(const RowsArgs &a, const RowsPlan &p, 
       r.p0 = r.T = 0;
       r.row0 = 0;
       const int b = b0 + lane;
-      const int bad = b < a.dims.batch ? seq_rows<kTree>(a, b, r) : 0;
+      const int bad = b < a.dims.batch ? seq_rows<kTree>(a, seq_words<kTree>(a, b), r) : 0;
       if (bad != 0 && first) report(a.st, bad);
       const int mine = (r.n + p.block_tokens - 1) / p.block_tokens;
       int sum = mine;
@@ -197,7 +235,8 @@ __device__ __forceinline__ void find_item(const RowsArgs &a, const RowsPlan &p, 
     if (it.b >= 0) {
       it.i0 = block * p.block_tokens;
       it.i1 = min(it.i0 + p.block_tokens, it.r.n);
-      const int bad = unit_keys<kTree>(a, it.r, it.b * a.dims.n_kv_heads + it.h, it.i0, it.i1, it.k);
+      const int u = it.b * a.dims.n_kv_heads + it.h;
+      const int bad = unit_keys<kTree>(a, it.r, unit_words<kTree>(a, u), u, it.i0, it.i1, it.k);
       if (bad != 0) {
         if (lane == 0 && split == 0) report(a.st, bad);
         it.i1 = it.i0;
@@ -675,21 +714,17 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kRows>::kThreads, RowsTrait
               return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
             };
             float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-            // The tile, with or without a look at what the row sees (a copy of the code each: the
-            // selections would otherwise be executed, switched off, for every tile).
-            auto tile = [&](auto with_mask) {
-              constexpr bool kMasked = decltype(with_mask)::value;
-              float first[64], ahead[kAhead ? 64 : 1];
-              float *const second = kAhead ? ahead : first;
-              uint32_t seen[4];            // a bit a key
-              auto read = [&](int half, float *to) {
-                tmem_ld32(s_at + half * 64, to);
-                tmem_ld32(s_at + half * 64 + 32, to + 32);
-              };
-              read(0, first);
-              if constexpr (kMasked) {
+            if ((flags & 0xffffu) != 0) {
+              // Logits of keys that the row does not see become -inf, in tensor memory: most tiles have
+              // none, and their code keeps its registers.
+#pragma unroll 1
+              for (int c32 = 0; c32 < 4; ++c32) {
+                float x[32];
+                tmem_ld32(s_at + c32 * 32, x);
+                uint32_t seen = 0;             // a bit a key
 #pragma unroll
-                for (int gi = 0; gi < kTileGroups; ++gi) {
+                for (int y = 0; y < 2; ++y) {
+                  const int gi = c32 * 2 + y;
                   uint32_t bits = 0xffffu;
                   if ((flags >> gi | flags >> (8 + gi)) & 1u) {
                     const int base = info.base[gi];
@@ -708,111 +743,107 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kRows>::kThreads, RowsTrait
                       if (k.windowed) bits &= below(k.sink - base) | ~below(pos - k.local - base + 1);
                     }
                   }
-                  if (gi % 2 == 0) seen[gi / 2] = bits & 0xffffu;
-                  else seen[gi / 2] |= bits << 16;
+                  seen |= (bits & 0xffffu) << (16 * y);
                 }
-              }
-              // Logits that the row does not see, of 64 keys, become -inf.
-              auto blank = [&](int half, float *x) {
-                if constexpr (kMasked) {
+                tmem_wait_ld<32>(x);
+                uint32_t w[32];
 #pragma unroll
-                  for (int c = 0; c < 64; ++c)
-                    if (!(seen[2 * half + c / 32] >> (c % 32) & 1u)) x[c] = -INFINITY;
-                }
-              };
-              auto max_of = [&](int half, const float *x) -> float {
-                float mx = -INFINITY;
-#pragma unroll
-                for (int gi = 0; gi < 4; ++gi) {
-                  float of = largest(x + gi * 16);
-                  if (Tr::kQuant && of != -INFINITY) of *= info.ks[half * 4 + gi];
-                  mx = fmaxf(mx, of);
-                }
-                return mx;
-              };
-              // Weights of keys [32 c32, + 32), over the first logits.
-              auto weigh = [&](int c32, const float *x32) {
-                const float base_m = m == -INFINITY ? 0.0f : -m * sc;
-                const float2 m2 = make_float2(base_m, base_m);
-                uint32_t w[16];
-#pragma unroll
-                for (int x = 0; x < 16; ++x) {
-                  const int gi = c32 * 2 + x / 8;
-                  const float to_log2 = Tr::kQuant ? info.ks[gi] * sc : sc;
-                  float2 y = __ffma2_rn(make_float2(x32[2 * x], x32[2 * x + 1]), make_float2(to_log2, to_log2), m2);
-                  if constexpr (Tr::kQuant && kMasked) {      // (a K scale of 0 makes a NaN of -inf)
-                    if (!(seen[c32] >> (2 * x) & 1u)) y.x = -INFINITY;
-                    if (!(seen[c32] >> (2 * x + 1) & 1u)) y.y = -INFINITY;
-                  }
-                  float2 e = make_float2(exp2_approx(y.x), exp2_approx(y.y));
-                  sum[x & 1] = __fadd2_rn(sum[x & 1], e);
-                  if constexpr (Tr::kQuant) {
-                    const float vs = info.vs[gi];
-                    e = __fmul2_rn(e, make_float2(vs, vs));
-                  }
-                  w[x] = pack_bf16(e.x, e.y);
-                }
-                tmem_st16(s_at + c32 * 16, w);
-              };
-              auto hand_over = [&](int part) {
-                tmem_wait_st();
-                tmem_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&sh.p_full[t][part]);
-              };
-              tmem_wait_ld<64>(first);
-              if constexpr (kAhead) read(1, ahead);
-              blank(0, first);
-              const float mx = fmaxf(max_of(0, first), pend);
-              bool late = false;
-              if (m == -INFINITY) {            // (nothing seen before: O's row is zero)
-                m = mx;
-                late = valid && m == -INFINITY;
+                for (int c = 0; c < 32; ++c) w[c] = seen >> c & 1u ? __float_as_uint(x[c]) : 0xff800000u;
+                tmem_st16(s_at + c32 * 32, w);
+                tmem_st16(s_at + c32 * 32 + 16, w + 16);
               }
-              if (__any_sync(0xffffffffu, late)) {      // a row's first keys are in the second half
-                if constexpr (!kAhead) read(1, first);
-                tmem_wait_ld<64>(second);
-                blank(1, second);
-                const float then = max_of(1, second);
-                if (m == -INFINITY) m = then;
-                if constexpr (!kAhead) {
-                  read(0, first);
-                  tmem_wait_ld<64>(first);
-                  blank(0, first);
-                }
-              }
-              const bool grow = valid && (mx - m) * sc > 8.0f;
-              if (__any_sync(0xffffffffu, grow)) {
-                const float to = grow ? mx : m;
-                const float f = grow ? exp2_approx((m - to) * sc) : 1.0f;
-                m = to;
-                l *= f;
-                if (j > 0) {
-#pragma unroll 1
-                  for (int c = 0; c < D / 16; ++c) {
-                    float o[16];
-                    tmem_ld16(o_at + c * 16, o);
-                    tmem_wait_ld<16>(o);
-                    uint32_t w[16];
+              tmem_wait_st();
+            }
+            float first[64], ahead[kAhead ? 64 : 1];
+            float *const second = kAhead ? ahead : first;
+            auto read = [&](int half, float *to) {
+              tmem_ld32(s_at + half * 64, to);
+              tmem_ld32(s_at + half * 64 + 32, to + 32);
+            };
+            read(0, first);
+            auto max_of = [&](int half, const float *x) -> float {
+              float mx = -INFINITY;
 #pragma unroll
-                    for (int x = 0; x < 16; ++x) w[x] = __float_as_uint(o[x] * f);
-                    tmem_st16(o_at + c * 16, w);
-                  }
-                }
+              for (int gi = 0; gi < 4; ++gi) {
+                float of = largest(x + gi * 16);
+                if (Tr::kQuant && of != -INFINITY) of *= info.ks[half * 4 + gi];
+                mx = fmaxf(mx, of);
               }
-              weigh(0, first);
-              weigh(1, first + 32);
+              return mx;
+            };
+            // Weights of keys [32 c32, + 32), over the first logits.
+            auto weigh = [&](int c32, const float *x32) {
+              const float base_m = m == -INFINITY ? 0.0f : -m * sc;
+              const float2 m2 = make_float2(base_m, base_m);
+              uint32_t w[16];
+#pragma unroll
+              for (int x = 0; x < 16; ++x) {
+                const int gi = c32 * 2 + x / 8;
+                // (a K scale of 0 must not make a NaN of -inf)
+                const float to_log2 = Tr::kQuant ? fmaxf(info.ks[gi] * sc, 1.17549435e-38f) : sc;
+                const float2 y = __ffma2_rn(make_float2(x32[2 * x], x32[2 * x + 1]), make_float2(to_log2, to_log2), m2);
+                float2 e = make_float2(exp2_approx(y.x), exp2_approx(y.y));
+                sum[x & 1] = __fadd2_rn(sum[x & 1], e);
+                if constexpr (Tr::kQuant) {
+                  const float vs = info.vs[gi];
+                  e = __fmul2_rn(e, make_float2(vs, vs));
+                }
+                w[x] = pack_bf16(e.x, e.y);
+              }
+              tmem_st16(s_at + c32 * 16, w);
+            };
+            auto hand_over = [&](int part) {
+              tmem_wait_st();
+              tmem_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&sh.p_full[t][part]);
+            };
+            tmem_wait_ld<64>(first);
+            if constexpr (kAhead) read(1, ahead);
+            const float mx = fmaxf(max_of(0, first), pend);
+            bool late = false;
+            if (m == -INFINITY) {            // (nothing seen before: O's row is zero)
+              m = mx;
+              late = valid && m == -INFINITY;
+            }
+            if (__any_sync(0xffffffffu, late)) {      // a row's first keys are in the second half
               if constexpr (!kAhead) read(1, first);
               tmem_wait_ld<64>(second);
-              blank(1, second);
-              weigh(2, second);
-              hand_over(0);
-              weigh(3, second + 32);
-              hand_over(1);
-              pend = max_of(1, second);
-            };
-            if ((flags & 0xffffu) != 0) tile(std::true_type{});
-            else tile(std::false_type{});
+              const float then = max_of(1, second);
+              if (m == -INFINITY) m = then;
+              if constexpr (!kAhead) {
+                read(0, first);
+                tmem_wait_ld<64>(first);
+              }
+            }
+            const bool grow = valid && (mx - m) * sc > 8.0f;
+            if (__any_sync(0xffffffffu, grow)) {
+              const float to = grow ? mx : m;
+              const float f = grow ? exp2_approx((m - to) * sc) : 1.0f;
+              m = to;
+              l *= f;
+              if (j > 0) {
+#pragma unroll 1
+                for (int c = 0; c < D / 16; ++c) {
+                  float o[16];
+                  tmem_ld16(o_at + c * 16, o);
+                  tmem_wait_ld<16>(o);
+                  uint32_t w[16];
+#pragma unroll
+                  for (int x = 0; x < 16; ++x) w[x] = __float_as_uint(o[x] * f);
+                  tmem_st16(o_at + c * 16, w);
+                }
+              }
+            }
+            weigh(0, first);
+            weigh(1, first + 32);
+            if constexpr (!kAhead) read(1, first);
+            tmem_wait_ld<64>(second);
+            weigh(2, second);
+            hand_over(0);
+            weigh(3, second + 32);
+            hand_over(1);
+            pend = max_of(1, second);
             l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
           } else if (lane == 0) {
             mbar_arrive(&sh.p_full[t][0]);
@@ -828,6 +859,7 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kRows>::kThreads, RowsTrait
           const int64_t rec = static_cast<int64_t>(blockIdx.x) * p.record_rows + (t * p.tokens * G + row);
           const float inv = l == 0.0f ? 0.0f : 1.0f / l;
           float odd = fabsf(l);
+          const bool aligned = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0, rec_aligned = (reinterpret_cast<uintptr_t>(p.rec_o) & 31) == 0;
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
             float o[32];
@@ -840,15 +872,18 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kRows>::kThreads, RowsTrait
             }
             if (valid) {
               if (last) {
-                uint4 *to = reinterpret_cast<uint4 *>(a.out + out_row * D + c * 32);
+                uint32_t w[16];
 #pragma unroll
-                for (int x = 0; x < 32; x += 8)
-                  to[x / 8] = make_uint4(pack_bf16(o[x] * inv, o[x + 1] * inv), pack_bf16(o[x + 2] * inv, o[x + 3] * inv),
-                                         pack_bf16(o[x + 4] * inv, o[x + 5] * inv), pack_bf16(o[x + 6] * inv, o[x + 7] * inv));
+                for (int x = 0; x < 16; ++x) w[x] = pack_bf16(o[2 * x] * inv, o[2 * x + 1] * inv);
+                __nv_bfloat16 *to = a.out + out_row * D + c * 32;
+                store_sector(to, w, aligned);
+                store_sector(to + 16, w + 8, aligned);
               } else {
-                float4 *to = reinterpret_cast<float4 *>(p.rec_o + rec * D + c * 32);
+                uint32_t w[32];
 #pragma unroll
-                for (int x = 0; x < 32; x += 4) to[x / 4] = make_float4(o[x], o[x + 1], o[x + 2], o[x + 3]);
+                for (int x = 0; x < 32; ++x) w[x] = __float_as_uint(o[x]);
+#pragma unroll
+                for (int x = 0; x < 32; x += 8) store_sector(p.rec_o + rec * D + c * 32 + x, w + x, rec_aligned);
               }
             }
           }
