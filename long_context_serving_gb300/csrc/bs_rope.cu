@@ -33,9 +33,9 @@ struct RopeArgs {
   int32_t *st;
 };
 
-// Q32, C32: rows and outputs, cache in fp32 (else bf16).
-template <int D, bool Q32, bool C32>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
+// Q32, C32: rows and outputs, cache in fp32 (else bf16). kNorm: with norms (of queries, keys or both).
+template <int D, bool Q32, bool C32, bool kNorm>
+__global__ void __launch_bounds__(kRopeThreads, kNorm || Q32 ? 2 : 3) rope_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int kLanes = D / 16;          // lanes a head
   constexpr int kHeads = 32 / kLanes;     // heads a warp takes at once
   const bs_dims &dims = a.dims;
@@ -50,32 +50,51 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
     const float hi = static_cast<float>(f);
     turns[threadIdx.x] = make_float2(hi, static_cast<float>(f - hi));
   }
-  __syncthreads();
   // This lane's elements of a head: [ea, ea + 8) and [eb, eb + 8); pairs 8l .. 8l + 7 where it
   // lies in the rotated part.
   const bool turning = l < rot / 16;
   const int ea = turning && !inter ? 8 * l : 16 * l;
   const int eb = turning && !inter ? rot / 2 + 8 * l : 16 * l + 8;
-  float wq_a[8], wq_b[8], wk_a[8], wk_b[8];
-  const bool norm_q = a.rope.q_weight != nullptr, norm_k = a.rope.k_weight != nullptr;
+  const bool norm_q = kNorm && a.rope.q_weight != nullptr, norm_k = kNorm && a.rope.k_weight != nullptr;
+  float wq[kNorm ? 16 : 1], wk[kNorm ? 16 : 1];
+  if constexpr (kNorm) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    wq_a[j] = norm_q ? a.rope.q_weight[ea + j] : 1.0f;
-    wq_b[j] = norm_q ? a.rope.q_weight[eb + j] : 1.0f;
-    wk_a[j] = norm_k ? a.rope.k_weight[ea + j] : 1.0f;
-    wk_b[j] = norm_k ? a.rope.k_weight[eb + j] : 1.0f;
+    for (int j = 0; j < 16; ++j) {
+      const int e = j < 8 ? ea + j : eb + j - 8;
+      wq[j] = norm_q ? a.rope.q_weight[e] : 1.0f;
+      wk[j] = norm_k ? a.rope.k_weight[e] : 1.0f;
+    }
   }
+  __syncthreads();
   const int Hq = dims.n_q_heads, Hkv = dims.n_kv_heads;
   const bool cache = a.k_pool != nullptr;
-  const int n_heads = Hq + Hkv + (cache ? Hkv : 0);
+  const int n_heads = Hq + Hkv + (cache ? Hkv : 0), step = a.parts * kHeads;
   const int64_t n_items = a.n_rows * a.parts;
   const int64_t n_warps = static_cast<int64_t>(gridDim.x) * kRopeWarps;
   for (int64_t item = static_cast<int64_t>(blockIdx.x) * kRopeWarps + (threadIdx.x >> 5); item < n_items; item += n_warps) {
     const int64_t row = a.parts == 1 ? item : item / a.parts;
     const int part = a.parts == 1 ? 0 : static_cast<int>(item - row * a.parts);
     const int b = a.row_seq != nullptr ? a.row_seq[row] : 0;
-    if (b < 0) continue;   // padding
     const int pos = a.positions[row];
+    const int64_t row_at = row * a.row_stride;
+    // The heads of one turn: this lane's, and its elements on their way.
+    struct Head {
+      int head;
+      Raw8<Q32> a, b;
+    };
+    auto fetch = [&](int h0) -> Head {
+      Head x{};
+      x.head = h0 + sub;
+      if (x.head < n_heads) {
+        const void *src = x.head < Hq ? a.q : x.head < Hq + Hkv ? a.k : a.v;
+        const int64_t at = row_at + static_cast<int64_t>(x.head < Hq ? x.head : x.head < Hq + Hkv ? x.head - Hq : x.head - Hq - Hkv) * D;
+        x.a.load(src, at + ea);
+        x.b.load(src, at + eb);
+      }
+      return x;
+    };
+    Head next = fetch(part * kHeads);     // (beside the row's position and its angles)
+    if (b < 0) continue;                  // padding
     int bad = 0;
     if (pos < 0 || pos >= kMaxPosition) bad = BS_ERR_INVALID_ARG;
     else if (a.row_seq != nullptr && b >= dims.batch) bad = BS_ERR_DEVICE_BOUNDS;
@@ -103,26 +122,19 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
         cs[j] *= a.rope.magnitude;
       }
     }
-    const int64_t row_at = row * a.row_stride;
-    for (int h0 = part * kHeads; h0 < n_heads; h0 += a.parts * kHeads) {
-      const int head = h0 + sub;
-      const bool live = head < n_heads;
-      const bool is_q = head < Hq, is_v = head >= Hq + Hkv;
-      const int hk = is_q ? 0 : (is_v ? head - Hq - Hkv : head - Hq);
-      Raw8<Q32> ra{}, rb{};
+    for (int h0 = part * kHeads; h0 < n_heads; h0 += step) {
+      const Head x = next;
+      next = fetch(h0 + step < n_heads ? h0 + step : n_heads);   // (past the last: nothing)
+      const int head = x.head;
+      const bool live = head < n_heads, is_q = head < Hq, is_v = head >= Hq + Hkv;
+      const int hk = is_q ? 0 : is_v ? head - Hq - Hkv : head - Hq;
       int page = 0;
-      if (live) {
-        const void *src = is_q ? a.q : (is_v ? a.v : a.k);
-        const int64_t at = row_at + static_cast<int64_t>(is_q ? head : hk) * D;
-        ra.load(src, at + ea);
-        rb.load(src, at + eb);
-        if (cache && !is_q)
-          page = a.page_table[(static_cast<int64_t>(b) * Hkv + hk) * dims.max_pages_per_unit + pos / kPage];
-      }
+      if (cache && live && !is_q)
+        page = a.page_table[(static_cast<int64_t>(b) * Hkv + hk) * dims.max_pages_per_unit + pos / kPage];
       float xa[8], xb[8];
-      ra.get(xa);
-      rb.get(xb);
-      if (norm_q || norm_k) {
+      x.a.get(xa);
+      x.b.get(xb);
+      if constexpr (kNorm) {
         float sum = 0.0f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) sum = fmaf(xa[j], xa[j], fmaf(xb[j], xb[j], sum));
@@ -132,8 +144,8 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
           const float inv = rsqrtf(fmaf(sum, 1.0f / D, a.rope.eps));
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            xa[j] = xa[j] * inv * (is_q ? wq_a[j] : wk_a[j]);
-            xb[j] = xb[j] * inv * (is_q ? wq_b[j] : wk_b[j]);
+            xa[j] = xa[j] * inv * (is_q ? wq[j] : wk[j]);
+            xb[j] = xb[j] * inv * (is_q ? wq[8 + j] : wk[8 + j]);
           }
         }
       }
@@ -141,11 +153,11 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constan
         if (inter) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
-            float &x = j < 4 ? xa[2 * j] : xb[2 * j - 8];
-            float &y = j < 4 ? xa[2 * j + 1] : xb[2 * j - 7];
-            const float u = x, w = y;
-            x = fmaf(u, cs[j], -(w * sn[j]));
-            y = fmaf(w, cs[j], u * sn[j]);
+            float &u = j < 4 ? xa[2 * j] : xb[2 * j - 8];
+            float &w = j < 4 ? xa[2 * j + 1] : xb[2 * j - 7];
+            const float u0 = u, w0 = w;
+            u = fmaf(u0, cs[j], -(w0 * sn[j]));
+            w = fmaf(w0, cs[j], u0 * sn[j]);
           }
         } else {
 #pragma unroll
@@ -185,13 +197,15 @@ template <int D, bool Q32, bool C32>
 bs_status launch_rope(RopeArgs &a, cudaStream_t cs) {
   constexpr int kHeads = 512 / D;
   const int groups = (a.dims.n_q_heads + 2 * a.dims.n_kv_heads + kHeads - 1) / kHeads;
-  const int64_t most = static_cast<int64_t>(attn_target_ctas()) * 2;   // CTAs of a full grid: four an SM
+  const bool norm = a.rope.q_weight != nullptr || a.rope.k_weight != nullptr;
+  const int64_t most = static_cast<int64_t>(attn_target_ctas()) / 2 * (norm || Q32 ? 2 : 3);   // CTAs that are on the GPU at once
   // A row's angles are worth about one group of its heads: it is shared out only while warps lack work.
   const int64_t spare = most * kRopeWarps / a.n_rows;
   a.parts = static_cast<int>(spare < 1 ? 1 : spare < groups ? spare : groups);
   const int64_t ctas = (a.n_rows * a.parts + kRopeWarps - 1) / kRopeWarps;
   const dim3 grid(static_cast<unsigned>(ctas < most ? ctas : most));
-  return launch_ex(rope_kernel<D, Q32, C32>, grid, kRopeThreads, 0, cs, 0, true, a) == cudaSuccess ? BS_OK : BS_ERR_CUDA;
+  auto kernel = norm ? rope_kernel<D, Q32, C32, true> : rope_kernel<D, Q32, C32, false>;
+  return launch_ex(kernel, grid, kRopeThreads, 0, cs, 0, true, a) == cudaSuccess ? BS_OK : BS_ERR_CUDA;
 }
 
 template <int D>
