@@ -423,15 +423,28 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kRows>::kThreads, RowsTrait
       const Keys k = it.k;
       const int64_t row0 = it.r.row0;
       const int h = it.h, kv = warp - Tr::kCopy;
-      auto group_of = [&](int j) -> Group {     // lanes 0..7: a tile's groups
-        const int i = j * kTileGroups + lane;
-        if (lane < kTileGroups && j < t_hi && i < k.n_groups) return key_group<kTree>(a, k, i);
-        return Group{0, -2};
+      // Pages (and scales) are looked up for four tiles at once, a lane each, four tiles ahead: two or
+      // three loads one behind another, mostly from memory.
+      struct Lookup {
+        Group g;
+        float ks, vs;
+        uint32_t differ, absent, drafts;     // of the 32 groups, as in TileInfo::flags
       };
-      auto flags_of = [&](const Group &g) -> uint32_t {
-        const uint32_t f = lane < kTileGroups ? group_flags<kTree>(k, g, it.i0, it.i1) : 0u;
-        return __ballot_sync(0xffffffffu, f & 1u) | __ballot_sync(0xffffffffu, f & 0x100u) << 8 |
-               __ballot_sync(0xffffffffu, f & 0x10000u) << 16;
+      auto look_up = [&](int j) -> Group {
+        const int i = j * kTileGroups + lane;
+        return i < min(k.n_groups, t_hi * kTileGroups) ? key_group<kTree>(a, k, i) : Group{0, -2};
+      };
+      auto complete = [&](const Group &g) -> Lookup {
+        Lookup x{g, 1.0f, 1.0f, 0u, 0u, 0u};
+        if (Tr::kQuant && kv == 0 && g.page >= 0) {
+          x.ks = a.kv.k_scale[g.page];
+          x.vs = a.kv.v_scale[g.page];
+        }
+        const uint32_t f = group_flags<kTree>(k, g, it.i0, it.i1);
+        x.differ = __ballot_sync(0xffffffffu, f & 1u);
+        x.absent = __ballot_sync(0xffffffffu, f & 0x100u);
+        x.drafts = __ballot_sync(0xffffffffu, f & 0x10000u);
+        return x;
       };
       // q rows of the block, tile by tile: [token][head of the group], 64 columns at a time
       if (kv == 0 && lane == 0) {
@@ -442,31 +455,27 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kRows>::kThreads, RowsTrait
       }
       const CUtensorMap *map = kv == 0 ? &maps.k : &maps.v, *map_new = kv == 0 ? &maps.k_new : &maps.v_new;
       const int box_page = Tr::kQuant ? lane % kTileGroups : lane / Tr::kHalves % kTileGroups, half = lane % Tr::kHalves;
-      Group g = group_of(t_lo);
+      Lookup now = complete(look_up(t_lo)), then{};
+      Group ahead{0, -2};
       bool ok = true;
       int item = kv;
       for (int j = t_lo; j < t_hi; ++j, item += 2) {
-        const uint32_t flags = flags_of(g);
-        const int page = __shfl_sync(0xffffffffu, g.page, box_page), base = __shfl_sync(0xffffffffu, g.base, box_page);
-        const int my_base = g.base;
-        float ks = 1.0f, vs = 1.0f;
-        if (Tr::kQuant && kv == 0 && g.page >= 0) {
-          ks = a.kv.k_scale[g.page];
-          vs = a.kv.v_scale[g.page];
-        }
-        g = group_of(j + 1);     // (its loads fly beside this tile's copies)
+        const int s = (j - t_lo) % 4 * kTileGroups;          // the tile's lanes
+        if (s == 0 && j > t_lo) now = then;
+        const uint32_t flags = (now.differ >> s & 0xffu) | (now.absent >> s & 0xffu) << 8 | (now.drafts >> s & 0xffu) << 16;
+        const int page = __shfl_sync(0xffffffffu, now.g.page, s + box_page), base = __shfl_sync(0xffffffffu, now.g.base, s + box_page);
         const int slot = item % (Tr::kQuant ? kRaw : kSlots), turn = item / (Tr::kQuant ? kRaw : kSlots);
         ok = wait(Tr::kQuant ? &sh.raw_empty[slot] : &sh.empty[slot], (turn & 1) ^ 1);
         if (!ok) break;
         if (kv == 0) {
           TileInfo &info = sh.info[(j - t_lo) % kInfos];
-          if (lane < kTileGroups) {
-            info.base[lane] = my_base;
+          if (lane >= s && lane < s + kTileGroups) {
+            info.base[lane - s] = now.g.base;
             if constexpr (Tr::kQuant) {
               float m;
-              info.ve[lane] = split_scale(vs, m);
-              info.ks[lane] = ks;
-              info.vs[lane] = m;
+              info.ve[lane - s] = split_scale(now.vs, m);
+              info.ks[lane - s] = now.ks;
+              info.vs[lane - s] = m;
             }
           }
           if (lane == 0) info.flags = flags;
@@ -492,6 +501,8 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kRows>::kThreads, RowsTrait
             else tma_2d(dst, map, half * 64, page * kPage, bar);
           }
         }
+        if (s == 0 && j + 4 < t_hi) ahead = look_up(j + 4);
+        if (s == 3 * kTileGroups && j + 1 < t_hi) then = complete(ahead);
       }
       // (After a wait that ran out, copies in flight land before the CTA leaves. Their barriers may
       // lack the other copy warp's arrival: this takes as long as a wait may last.)
