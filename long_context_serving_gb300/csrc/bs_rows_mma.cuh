@@ -288,7 +288,9 @@ struct RowsTraits {
   static constexpr int kQBytes = kTiles * kQTile;
   static constexpr int kControl = 2048;                 // RowsShared
   static constexpr int kMaxDyn = kPerSm == 2 ? 233472 / 2 - 1024 : 232448;   // shared memory of a CTA, at most
-  static constexpr int kRaw = !kQuant ? 0 : kRows == 32 ? 6 : 4;  // K or V tiles in codes
+  // K or V tiles in codes. (Two row tiles, d = 128: four slots and two of these rather than three and
+  // four, with which K's conversion waited for the products of the V before it.)
+  static constexpr int kRaw = !kQuant ? 0 : kRows == 32 ? 6 : kRows == 128 ? 4 : 2;
   static constexpr int kRawBytes = kQuant ? kKeyTile * D : 0;
   static constexpr int kRoom = (kMaxDyn - 1024 - kControl - kQBytes - kRaw * kRawBytes) / kSlotBytes;
   static constexpr int kSlots = kRoom < 12 ? kRoom : 12;
@@ -328,12 +330,13 @@ template <bool I8>
 __device__ __forceinline__ void codes_to_bf16(uint32_t w, bool scaled, float two_e, uint32_t &lo, uint32_t &hi) {
   float f[4];
   codes_to_f32<I8>(w, f);
+  float2 a = make_float2(f[0], f[1]), b = make_float2(f[2], f[3]);
   if (scaled) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] *= two_e;
+    a = __fmul2_rn(a, make_float2(two_e, two_e));
+    b = __fmul2_rn(b, make_float2(two_e, two_e));
   }
-  lo = pack_bf16(f[0], f[1]);
-  hi = pack_bf16(f[2], f[3]);
+  lo = pack_bf16(a.x, a.y);
+  hi = pack_bf16(b.x, b.y);
 }
 
 // A scale as m * 2^e, 2^e returned; m in [1, 2), smaller for a subnormal scale, and what there is
