@@ -37,7 +37,7 @@ HostPlan plan_rows(const bs_dims &d, int64_t n_rows, int max_new, bool tree) {
     tiles = (static_cast<int64_t>(d.max_pages_per_unit) + kTileGroups - 1) / kTileGroups;
   }
   h.p.record_rows = (max_new < h.p.block_tokens ? max_new : h.p.block_tokens) * G;
-  const int at_once = h.rows == 32 && d.kv_dtype == BS_BF16 ? 2 * kSms : kSms;   // CTAs
+  const int at_once = h.rows == 32 ? 2 * kSms : kSms;                  // CTAs
   int64_t splits = 1;
   if (tree && h.items <= kShareItems) {                                      // a wave of CTAs over the units' own tiles
     if (tiles > 1) h.p.even = at_once;

@@ -5,7 +5,7 @@
 // (1 or 2), against a contiguous piece of the block's key groups:
 //   copy warps     one for K, one for V: fetch tiles of 128 keys into a ring of shared-memory slots,
 //                  bf16 pages by tiled copies; 8-bit pages by bulk copies into a ring of their own,
-//   (8-bit) four warps  write the bf16 values that the codes stand for into the ring's slots;
+//   (8-bit) eight warps write the bf16 values that the codes stand for into the ring's slots;
 //   product warp   S = Q K^T into tensor memory (one thread issues); O += P V with P from tensor
 //                  memory, page by page, so that a page that is not there takes no part;
 //   row warps      four a tile, a thread a row: logits from tensor memory, the running maximum and
@@ -273,13 +273,13 @@ struct RowsShared {
 
 // kRows: rows of a CTA, 256 (two row tiles), 128 or 32. With 32 (single tokens, small trees) one row
 // warp and the first quarter of a tile do; the products' other rows are whatever lies behind the
-// queries, in rows of S and O that nobody reads. bf16: two such CTAs an SM, one's start beside the
-// other's keys (32 sequences' single tokens: 200 us with one, see the launcher for both).
+// queries, in rows of S and O that nobody reads. Two such CTAs an SM: one's start and softmax beside the
+// other's keys (32 sequences' single tokens, bf16: 164 us, with one 200).
 template <int D, int kKv, int kRows>
 struct RowsTraits {
   static constexpr bool kQuant = kKv != 0;              // 1: E4M3, 2: INT8
   static constexpr int kTiles = kRows == 256 ? 2 : 1;
-  static constexpr int kPerSm = kRows == 32 && !kQuant ? 2 : 1;
+  static constexpr int kPerSm = kRows == 32 ? 2 : 1;
   static constexpr int kHalves = D / 64;                // 128-byte columns of a row
   static constexpr int kSlotBytes = kKeyTile * D * 2;
   static constexpr int kHalfBytes = kKeyTile * 128;
@@ -290,22 +290,22 @@ struct RowsTraits {
   static constexpr int kMaxDyn = kPerSm == 2 ? 233472 / 2 - 1024 : 232448;   // shared memory of a CTA, at most
   // K or V tiles in codes. (Two row tiles, d = 128: four slots and two of these rather than three and
   // four, with which K's conversion waited for the products of the V before it.)
-  static constexpr int kRaw = !kQuant ? 0 : kRows == 32 ? 6 : kRows == 128 ? 4 : 2;
+  static constexpr int kRaw = !kQuant ? 0 : kRows == 128 ? 4 : 2;
   static constexpr int kRawBytes = kQuant ? kKeyTile * D : 0;
   static constexpr int kRoom = (kMaxDyn - 1024 - kControl - kQBytes - kRaw * kRawBytes) / kSlotBytes;
   static constexpr int kSlots = kRoom < 12 ? kRoom : 12;
   static constexpr int kTileWarps = kRows == 32 ? 1 : 4;          // row warps of a tile
   static constexpr int kRowWarps = kTileWarps * kTiles;
-  static constexpr int kWriters = kQuant ? 4 : 1;       // warps that fill a slot
+  static constexpr int kWriters = !kQuant ? 1 : kRows == 32 ? 4 : 8;       // warps that fill a slot
   // Product warp, two copy warps, (8-bit) conversion warps, one on each scheduler, row warps from a
   // multiple of four.
   static constexpr int kProduct = kRows == 32 ? 1 : 0, kCopy = kProduct + 1, kConvert = 4;
-  static constexpr int kFirstRow = kRows == 32 ? 0 : kQuant ? 8 : 4;
+  static constexpr int kFirstRow = kRows == 32 ? 0 : kQuant ? 4 + kWriters : 4;
   static constexpr int kThreads = 32 * (kRows == 32 ? (kQuant ? 8 : 4) : kFirstRow + kRowWarps);
   static constexpr int kColumns = kTiles == 1 ? 256 : 512;
   static constexpr int kSmem = 1024 + kQBytes + kSlots * kSlotBytes + kRaw * kRawBytes + kControl;
   static_assert(sizeof(RowsShared) <= kControl, "control block");
-  static_assert(kSlots >= 3 && kRaw <= 8 && kSmem <= kMaxDyn, "ring");
+  static_assert(kSlots >= 2 && kRaw <= 8 && kSmem <= kMaxDyn, "ring");
   static_assert(kQBytes + kSlots * kSlotBytes >= kQTile - kQHalf + 16384, "products read 128 rows");
 };
 
@@ -510,10 +510,11 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kRows>::kThreads, RowsTrait
       // (After a wait that ran out, copies in flight land before the CTA leaves. Their barriers may
       // lack the other copy warp's arrival: this takes as long as a wait may last.)
       if (!ok) wait(&sh.never, 0);
-    } else if (Tr::kQuant && warp >= Tr::kConvert && warp < Tr::kConvert + 4) {
-      // ---- conversion warps: groups 2 cw and 2 cw + 1 of every tile -----------------------------------
+    } else if (Tr::kQuant && warp >= Tr::kConvert && warp < Tr::kConvert + Tr::kWriters) {
+      // ---- conversion warps: one group of every tile each -----------------------------------------------
       constexpr int kPieces = kPage * D / 16 / 32;       // 16-code pieces of a lane and page
       constexpr int kRowStep = kPage / kPieces;          // a lane's pieces lie this many rows apart
+      constexpr int kMine = kTileGroups / Tr::kWriters;   // groups of a tile for each warp
       const int cw = warp - Tr::kConvert;
       const Keys &k = it.k;
       const int64_t row0 = it.r.row0;
@@ -539,15 +540,15 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kRows>::kThreads, RowsTrait
           ok = wait(&sh.raw_full[raw], item / kRaw & 1) && wait(&sh.empty[slot], (item / kSlots & 1) ^ 1);
           if (!ok) break;
           const TileInfo &info = sh.info[(j - t_lo) % kInfos];
-          uint4 codes[2][kPieces];                       // (all on their way before the first store)
+          uint4 codes[kMine][kPieces];                       // (all on their way before the first store)
 #pragma unroll
-          for (int i = 0; i < 2; ++i)
+          for (int i = 0; i < kMine; ++i)
 #pragma unroll
             for (int c = 0; c < kPieces; ++c)
-              codes[i][c] = *reinterpret_cast<const uint4 *>(raw_ring + raw * Tr::kRawBytes + (2 * cw + i) * (kPage * D) + (c * kRowStep + row) * D + col);
+              codes[i][c] = *reinterpret_cast<const uint4 *>(raw_ring + raw * Tr::kRawBytes + (kMine * cw + i) * (kPage * D) + (c * kRowStep + row) * D + col);
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const int gi = 2 * cw + i, base = info.base[gi];
+          for (int i = 0; i < kMine; ++i) {
+            const int gi = kMine * cw + i, base = info.base[gi];
             const uint32_t flags = info.flags >> gi;
             unsigned char *rows = ring + slot * Tr::kSlotBytes + gi * (kPage * 128);
             if (flags & 0x100u) continue;
