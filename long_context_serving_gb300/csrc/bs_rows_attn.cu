@@ -31,8 +31,8 @@ HostPlan plan_rows(const bs_dims &d, int64_t n_rows, int max_new, bool tree) {
     tiles = (static_cast<int64_t>(d.max_gather_pages_per_unit) + (max_new + kPage - 1) / kPage + kTileGroups - 1) / kTileGroups;
   } else {
     const int64_t by_seq = per_seq * d.batch, by_rows = n_rows / h.p.block_tokens + (n_rows < d.batch ? n_rows : d.batch);
-    const int64_t blocks = by_seq < by_rows ? by_seq : by_rows;
-    h.p.n_blocks = static_cast<int>(blocks < INT32_MAX ? blocks : INT32_MAX);
+    const int64_t blocks = per_seq == 1 || by_seq < by_rows ? by_seq : by_rows;
+    h.p.n_blocks = per_seq == 1 ? 0 : static_cast<int>(blocks < INT32_MAX ? blocks : INT32_MAX);
     h.items = blocks * d.n_kv_heads;
     tiles = (static_cast<int64_t>(d.max_pages_per_unit) + kTileGroups - 1) / kTileGroups;
   }

@@ -37,12 +37,13 @@ constexpr int kKeyTile = 128;                 // keys of a tile
 constexpr int kTileGroups = kKeyTile / kPage; // groups of a tile
 constexpr int kFirstKeys = 96;                // keys whose weights are handed over first
 constexpr int kShareItems = 64;               // tree: items whose key tiles a wave of CTAs shares
+constexpr uint64_t kInFlightNs = 10000000;    // longer than any copy or product takes
 constexpr int kInfos = 8;                     // tiles whose description is kept
 
 struct RowsPlan {
   int tokens;         // tokens of a row tile: its rows / G
   int block_tokens;   // of a CTA
-  int n_blocks;       // prefill: blocks of all sequences, at most; tree: of a sequence
+  int n_blocks;       // tree: blocks of a sequence; prefill: of all sequences, at most, or 0: one of each
   int items;          // blocks of all units, at most
   int splits;         // CTAs a block's keys are split over, at most (1: records unused)
   int even;           // > 0: that many CTAs share all items' key tiles (tree_share)
@@ -197,41 +198,62 @@ __device__ __forceinline__ void find_item(const RowsArgs &a, const RowsPlan &p, 
     if (bad != 0 && lane == 0 && split == 0) report(a.st, bad);
   } else {
     it.h = it.item % a.dims.n_kv_heads;
-    int at = it.item / a.dims.n_kv_heads;                   // blocks before this one
-    const bool first = cta == 0;                            // looks at every sequence, and reports
-    it.b = -1;
-    int block = 0, total = 0;
-    for (int b0 = 0; b0 < a.dims.batch && (it.b < 0 || first); b0 += 32) {
-      SeqRows r;
-      r.n = 0;
-      r.p0 = r.T = 0;
-      r.row0 = 0;
-      const int b = b0 + lane;
-      const int bad = b < a.dims.batch ? seq_rows<kTree>(a, seq_words<kTree>(a, b), r) : 0;
-      if (bad != 0 && first) report(a.st, bad);
-      const int mine = (r.n + p.block_tokens - 1) / p.block_tokens;
-      int sum = mine;
+    int block = 0;
+    if (p.n_blocks == 0) {
+      it.b = it.item / a.dims.n_kv_heads;
+      const int bad = seq_rows<kTree>(a, seq_words<kTree>(a, it.b), it.r);
+      if (bad != 0 && lane == 0 && split == 0 && it.h == 0) report(a.st, bad);
+      if (it.r.n == 0) it.b = -1;
+    } else {
+      // Blocks are numbered sequence by sequence, each sequence's last block (which has the most keys)
+      // first: 128 sequences at a time, a lane to four of them.
+      constexpr int kEach = 4;
+      int at = it.item / a.dims.n_kv_heads;                 // blocks before this one
+      const bool first = cta == 0;                          // looks at every sequence, and reports
+      int total = 0;
+      it.b = -1;
+      for (int b0 = 0; b0 < a.dims.batch && (it.b < 0 || first); b0 += 32 * kEach) {
+        SeqWords w[kEach];
+        int mine[kEach], sum = 0;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += x;
+        for (int i = 0; i < kEach; ++i) w[i] = seq_words<kTree>(a, min(b0 + lane * kEach + i, a.dims.batch - 1));
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+          SeqRows r;
+          r.n = 0;
+          const int bad = b0 + lane * kEach + i < a.dims.batch ? seq_rows<kTree>(a, w[i], r) : 0;
+          if (bad != 0 && first) report(a.st, bad);
+          mine[i] = (r.n + p.block_tokens - 1) / p.block_tokens;
+          sum += mine[i];
+        }
+        int end = sum;                                      // blocks of this lane's sequences and those before
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int x = __shfl_up_sync(0xffffffffu, end, o);
+          if (lane >= o) end += x;
+        }
+        const unsigned here = __ballot_sync(0xffffffffu, end > at);
+        if (it.b < 0 && here != 0) {
+          const int src = __ffs(here) - 1;
+          int i = 0, before = end - sum;                    // (meant for lane src)
+#pragma unroll
+          for (int x = 0; x < kEach - 1; ++x)
+            if (i == x && before + mine[x] <= at) {
+              before += mine[x];
+              ++i;
+            }
+          i = __shfl_sync(0xffffffffu, i, src);
+          before = __shfl_sync(0xffffffffu, before, src);
+          it.b = b0 + src * kEach + i;
+          seq_rows<kTree>(a, seq_words<kTree>(a, it.b), it.r);
+          block = before + (it.r.n + p.block_tokens - 1) / p.block_tokens - 1 - at;
+        }
+        const int all = __shfl_sync(0xffffffffu, end, 31);
+        at -= all;
+        total += all;
       }
-      const unsigned here = __ballot_sync(0xffffffffu, sum > at);
-      if (it.b < 0 && here != 0) {
-        const int src = __ffs(here) - 1;
-        it.b = b0 + src;
-        // (a sequence's last block first: it has the most keys)
-        block = __shfl_sync(0xffffffffu, sum, src) - 1 - at;
-        it.r.n = __shfl_sync(0xffffffffu, r.n, src);
-        it.r.p0 = __shfl_sync(0xffffffffu, r.p0, src);
-        it.r.T = __shfl_sync(0xffffffffu, r.T, src);
-        it.r.row0 = __shfl_sync(0xffffffffu, r.row0, src);
-      }
-      const int all = __shfl_sync(0xffffffffu, sum, 31);
-      at -= all;
-      total += all;
+      if (first && lane == 0 && total > p.n_blocks) report(a.st, BS_ERR_CAPACITY);   // sequences that share rows
     }
-    if (first && lane == 0 && total > p.n_blocks) report(a.st, BS_ERR_CAPACITY);   // sequences that share rows
     if (it.b >= 0) {
       it.i0 = block * p.block_tokens;
       it.i1 = min(it.i0 + p.block_tokens, it.r.n);
@@ -267,8 +289,9 @@ struct RowsShared {
   uint64_t empty[12];         // a slot's products are done
   uint64_t raw_full[8], raw_empty[8];
   uint64_t k0_full, full[kInfos];   // K of the first tile; V of a tile and K of the next one, have landed
-  uint64_t q_full, s_full[2], p_full[2][2], o_full[2], drained, never;   // (p_full: [row tile][part])
+  uint64_t q_full, s_full[2], p_full[2][2], o_full[2], never;   // (p_full: [row tile][part])
   uint32_t tmem;
+  int failed;                 // a wait ran out
 };
 
 // kRows: rows of a CTA, 256 (two row tiles), 128 or 32. With 32 (single tokens, small trees) one row
@@ -383,8 +406,8 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kRows>::kThreads, RowsTrait
         mbar_init(&sh.p_full[t][1], Tr::kTileWarps);
         mbar_init(&sh.o_full[t], 1);
       }
-      mbar_init(&sh.drained, 1);
       mbar_init(&sh.never, 1);
+      sh.failed = 0;
       fence_mbar_init();
       fence_proxy_async_smem();
     }
@@ -417,7 +440,9 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kRows>::kThreads, RowsTrait
   };
   auto wait = [&](uint64_t *bar, uint32_t parity) -> bool {
     if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
-    return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, a.st, p.wait_ns));
+    if (__all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, a.st, p.wait_ns))) return true;
+    *const_cast<volatile int *>(&sh.failed) = 1;
+    return false;
   };
 
   if (t_lo < t_hi) {
@@ -507,9 +532,6 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kRows>::kThreads, RowsTrait
         if (s == 0 && j + 4 < t_hi) ahead = look_up(j + 4);
         if (s == 3 * kTileGroups && j + 1 < t_hi) then = complete(ahead);
       }
-      // (After a wait that ran out, copies in flight land before the CTA leaves. Their barriers may
-      // lack the other copy warp's arrival: this takes as long as a wait may last.)
-      if (!ok) wait(&sh.never, 0);
     } else if (Tr::kQuant && warp >= Tr::kConvert && warp < Tr::kConvert + Tr::kWriters) {
       // ---- conversion warps: one group of every tile each -----------------------------------------------
       constexpr int kPieces = kPage * D / 16 / 32;       // 16-code pieces of a lane and page
@@ -685,10 +707,6 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kRows>::kThreads, RowsTrait
             umma_commit(lead, &sh.o_full[t]);
           }
         }
-      }
-      if (!ok) {     // products in flight end before the tensor memory is given back
-        umma_commit(lead, &sh.drained);
-        wait(&sh.drained, 0);
       }
     } else if (warp >= Tr::kFirstRow && warp < Tr::kFirstRow + Tr::kRowWarps) {
       // ---- row warps -----------------------------------------------------------------------------
@@ -933,6 +951,9 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kRows>::kThreads, RowsTrait
   tmem_fence_before();
   __syncthreads();
   if (warp == Tr::kProduct) {
+    // (After a wait that ran out, copies and products in flight, which take microseconds, end before
+    // the CTA gives its memory back.)
+    if (sh.failed != 0) mbar_wait_bounded(&sh.never, 0, a.st, kInFlightNs);
     tmem_fence_after();
     tmem_free(tmem, Tr::kColumns);
   }

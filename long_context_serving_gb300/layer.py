@@ -240,6 +240,56 @@ class PagedLayer:
                       stream)
         self.advance()
 
+    # -- prompts and drafts --------------------------------------------------------
+    def prefill_attend(self, q: torch.Tensor, lo, hi, stream=None):
+        """Tokens [lo[b], hi[b]) of every sequence, already in the cache, attend it: q bf16
+        [rows][Hq][d], the sequences' rows one behind another. Streaming heads look at their
+        sink and window, the others at everything. Returns out (like q) and lse."""
+        lo, hi = np.asarray(lo, np.int64), np.asarray(hi, np.int64)
+        n = hi - lo
+        i32 = lambda a: torch.as_tensor(np.ascontiguousarray(a, dtype=np.int32), device=self.device)  # noqa: E731
+        out = torch.zeros_like(q)
+        lse = torch.zeros(q.shape[:2], dtype=torch.float32, device=self.device)
+        self._rows_ws = self._rows_workspace(B.prefill_workspace_size(self.dims, q.shape[0], max(1, int(n.max()))))
+        self._rows_in = i32(hi), i32(lo), i32(np.cumsum(n) - n)
+        B.prefill_attn(self.dims, q, q.stride(0), q.shape[0], self.kv_at(self._rows_in[0]), self.cfg, self._rows_in[1],
+                       self._rows_in[2], max(1, int(n.max())), out, lse, self._rows_ws, self.status, stream)
+        return out, lse
+
+    def draft_attend(self, q: torch.Tensor, k_new, v_new, n_draft, visible, lens, stream=None):
+        """Trees of drafts, n_draft[b] of them for sequence b, attend the blocks of the last selection
+        (the one that became the previous) and the drafts that `visible` names; lens[b] tokens are in
+        the cache. k_new, v_new: rows of all KV heads. Returns out (like q) and lse."""
+        n = np.asarray(n_draft, np.int64)
+        i32 = lambda a: torch.as_tensor(np.ascontiguousarray(a, dtype=np.int32), device=self.device)  # noqa: E731
+        out = torch.zeros_like(q)
+        lse = torch.zeros(q.shape[:2], dtype=torch.float32, device=self.device)
+        most = max(1, int(n.max()))
+        self._rows_ws = self._rows_workspace(B.tree_workspace_size(self.dims, most))
+        self._rows_in = i32(lens), i32(np.cumsum(n) - n), i32(n)
+        drafts = B.Drafts(k_new=k_new.data_ptr(), v_new=v_new.data_ptr(), row_stride=k_new.stride(0), n_rows=q.shape[0],
+                          row_begin=self._rows_in[1].data_ptr(), n_draft=self._rows_in[2].data_ptr(),
+                          visible=visible.data_ptr(), max_draft=most)
+        last = 1 - self.cur
+        B.tree_decode_attn(self.dims, q, q.stride(0), self.kv_at(self._rows_in[0]), self.cfg, self.sel[last], self.cnt[last],
+                           drafts, out, lse, self._rows_ws, self.status, stream)
+        return out, lse
+
+    def commit_drafts(self, k_new, v_new, n_draft, path, lens, stream=None) -> None:
+        """The accepted drafts of each sequence, path[b] (node numbers, -1 behind the last), enter the
+        cache behind its lens[b] tokens."""
+        n, path, lens = np.asarray(n_draft, np.int64), np.asarray(path, np.int64), np.asarray(lens, np.int64)
+        i32 = lambda a: torch.as_tensor(np.ascontiguousarray(a, dtype=np.int32), device=self.device)  # noqa: E731
+        pools = self.pools if self.kv8 else B.Pools(k_pool=self.k_pool.data_ptr(), v_pool=self.v_pool.data_ptr())
+        self._rows_in = i32(lens + (path >= 0).sum(1)), i32(lens), i32(np.cumsum(n) - n), i32(path)
+        B.tree_commit(self.dims, pools, self.page_table, *self._rows_in, path.shape[1], k_new, v_new, k_new.stride(0),
+                      int(n.sum()), self.status, stream)
+
+    def _rows_workspace(self, size: int):
+        have = getattr(self, "_rows_ws", None)
+        return have if have is not None and have.numel() >= max(size, 16) else \
+            torch.empty(max(size, 16), dtype=torch.uint8, device=self.device)
+
     def advance(self) -> None:
         """The current selection becomes the previous one."""
         self.cur = 1 - self.cur

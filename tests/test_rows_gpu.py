@@ -276,6 +276,40 @@ def test_prefill_more_units_than_a_wave(units):
     p.check()
 
 
+def test_prefill_many_sequences():
+    """Blocks are found among hundreds of sequences, most of them with few or no new tokens."""
+    new = [(5 * i) % 4 if i % 97 else 90 + i // 97 for i in range(300)]
+    c = R.Cache(300, 1, 4, 64, [n + (3 * i) % 50 for i, n in enumerate(new)], "bf16")
+    p = Prefill(c, new)
+    p.run()
+    assert _sync_status(c) == 0
+    p.check(rows=12)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_waits_that_run_out_are_reported(kind):
+    """With a limit of a microsecond the waits for the first copies may run out: the call then says so,
+    ends, and the next one is right."""
+    c = R.Cache(2, 2, 4, 128, [3000, 900], kind, max_gather_pages_per_unit=192)
+    p, t = Prefill(c, [300, 40]), Tree(c, [9, 33], g=32)
+    limit = B.wait_limit_ns()
+    try:
+        B.set_wait_limit_ns(1000)
+        for x in (p, t):
+            x.run()
+            assert _sync_status(c) in (0, B.BS_ERR_TIMEOUT)
+            c.status.zero_()
+    finally:
+        B.set_wait_limit_ns(limit)
+    for x in (p, t):
+        x.out.fill_(7.0)
+        x.lse.fill_(7.0)
+        x.run()
+    assert _sync_status(c) == 0
+    p.check(rows=20)
+    t.check()
+
+
 def test_prefill_strides_and_no_lse():
     c = R.Cache(2, 2, 4, 128, [77, 20], "bf16")
     p = Prefill(c, [20, 20], stride_pad=8 * 128)
@@ -564,6 +598,17 @@ def test_tree_refusals_on_the_device():
             t.check(skip_units=(1,))
 
 
+@pytest.mark.parametrize("batch,n", [(33, 3), (70, 40)])
+def test_tree_many_units(batch, n):
+    """More units than share a wave's CTAs, and as many as just do."""
+    lens = [(37 * i) % 700 for i in range(batch)]
+    c = R.Cache(batch, 1, 8, 64, lens, "bf16", max_gather_pages_per_unit=300)
+    t = Tree(c, [(i * 7) % (n + 1) for i in range(batch)], g=16, sel="some")
+    t.run()
+    assert _sync_status(c) == 0
+    t.check()
+
+
 # ---------------------------------------------------------------------------------------
 # Commit
 # ---------------------------------------------------------------------------------------
@@ -655,6 +700,43 @@ def test_commit_skips_what_does_not_fit(kind, bad, code):
 # ---------------------------------------------------------------------------------------
 # Streams, graphs, and a run of them together
 # ---------------------------------------------------------------------------------------
+@pytest.mark.parametrize("kv8", [None, "e4m3"])
+def test_layer_attends_prompts_and_drafts(kv8):
+    """PagedLayer's own calls: a whole prompt against the float64 form over its logical K and V, then
+    drafts over the layer's selection, then their commit."""
+    from workloads import make_workload
+    from long_context_serving_gb300.layer import PagedLayer
+
+    wl = make_workload(2, seed=3, T=700)
+    layer = PagedLayer(wl, kv8=kv8)
+    layer.prefill()
+    layer.append(0)
+    layer.fused_step(0)                           # the selection that drafts attend
+    T = int(wl.T_prefill[0])
+    rng = np.random.default_rng(5)
+    lo, hi = np.array([T - 90]), np.array([T])
+    q = torch.as_tensor(R.bf16(rng.standard_normal((90, wl.Hq, wl.d)))).cuda().bfloat16()
+    out, lse = layer.prefill_attend(q, lo, hi)
+    if kv8 is None:                               # (8-bit values: the other tests')
+        for i, u in itertools.product((0, 40, 89), (0, 5)):
+            K, V = (x.astype(np.float64) for x in (wl.K64(u)[:T], wl.V64(u)[:T]))
+            s = R.prefill_seen(T - 90 + i, T, wl.cls[u] == B.BS_STREAMING, int(wl.sink[u]), int(wl.local[u]))
+            want = R.attend_row(q[i, u * wl.G].double().cpu().numpy(), K[s], V[s])
+            R.check_row(out[i, u * wl.G].double().cpu().numpy(), float(lse[i, u * wl.G]), want, (i, u))
+    n = 5
+    kv = torch.as_tensor(R.bf16(rng.standard_normal((n, 2 * wl.Hkv * wl.d)))).cuda().bfloat16()
+    visible = torch.tensor([(1 << (i + 1)) - 1 for i in range(n)], dtype=torch.int64, device="cuda")   # a chain
+    lens = np.array([T + 1])
+    d_out, d_lse = layer.draft_attend(q[:n].contiguous(), kv[:, :wl.Hkv * wl.d], kv[:, wl.Hkv * wl.d:], [n], visible, lens)
+    assert layer.read_status() == 0 and torch.isfinite(d_out.float()).all() and torch.isfinite(d_lse).all()
+    if T + 3 <= wl.page_table.shape[1] * 16:
+        layer.commit_drafts(kv[:, :wl.Hkv * wl.d], kv[:, wl.Hkv * wl.d:], [n], np.array([[0, 1]]), lens)
+        assert layer.read_status() == 0
+        ph = int(layer.page_table[0, (T + 1) // 16])
+        if kv8 is None:
+            assert torch.equal(layer.k_pool[ph, (T + 1) % 16], kv[0, :wl.d])
+
+
 def test_other_streams_and_graphs():
     """On a stream of the caller's, and captured once and replayed over new inputs; two captured graphs
     with a workspace each replay side by side."""
