@@ -35,7 +35,7 @@ struct RopeArgs {
 
 // Q32, C32: rows and outputs, cache in fp32 (else bf16). kNorm: with norms (of queries, keys or both).
 template <int D, bool Q32, bool C32, bool kNorm>
-__global__ void __launch_bounds__(kRopeThreads, kNorm || Q32 ? 2 : 3) rope_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kRopeThreads, Q32 ? 2 : 3) rope_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int kLanes = D / 16;          // lanes a head
   constexpr int kHeads = 32 / kLanes;     // heads a warp takes at once
   const bs_dims &dims = a.dims;
@@ -56,13 +56,11 @@ __global__ void __launch_bounds__(kRopeThreads, kNorm || Q32 ? 2 : 3) rope_kerne
   const int ea = turning && !inter ? 8 * l : 16 * l;
   const int eb = turning && !inter ? rot / 2 + 8 * l : 16 * l + 8;
   const bool norm_q = kNorm && a.rope.q_weight != nullptr, norm_k = kNorm && a.rope.k_weight != nullptr;
-  float wq[kNorm ? 16 : 1], wk[kNorm ? 16 : 1];
+  __shared__ __align__(16) float weights[kNorm ? 2 : 1][kNorm ? D : 4];   // of queries, of keys (registers hold no room for them)
   if constexpr (kNorm) {
-#pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      const int e = j < 8 ? ea + j : eb + j - 8;
-      wq[j] = norm_q ? a.rope.q_weight[e] : 1.0f;
-      wk[j] = norm_k ? a.rope.k_weight[e] : 1.0f;
+    for (int i = threadIdx.x; i < 2 * D; i += kRopeThreads) {
+      const float *w = i < D ? a.rope.q_weight : a.rope.k_weight;
+      weights[i / D][i % D] = w != nullptr ? w[i % D] : 1.0f;
     }
   }
   __syncthreads();
@@ -143,9 +141,11 @@ __global__ void __launch_bounds__(kRopeThreads, kNorm || Q32 ? 2 : 3) rope_kerne
         if (is_q ? norm_q : (!is_v && norm_k)) {
           const float inv = rsqrtf(fmaf(sum, 1.0f / D, a.rope.eps));
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            xa[j] = xa[j] * inv * (is_q ? wq[j] : wk[j]);
-            xb[j] = xb[j] * inv * (is_q ? wq[8 + j] : wk[8 + j]);
+          for (int j = 0; j < 8; j += 4) {
+            const float4 wa = *reinterpret_cast<const float4 *>(&weights[is_q ? 0 : 1][ea + j]);
+            const float4 wb = *reinterpret_cast<const float4 *>(&weights[is_q ? 0 : 1][eb + j]);
+            xa[j] *= inv * wa.x; xa[j + 1] *= inv * wa.y; xa[j + 2] *= inv * wa.z; xa[j + 3] *= inv * wa.w;
+            xb[j] *= inv * wb.x; xb[j + 1] *= inv * wb.y; xb[j + 2] *= inv * wb.z; xb[j + 3] *= inv * wb.w;
           }
         }
       }
@@ -198,7 +198,7 @@ bs_status launch_rope(RopeArgs &a, cudaStream_t cs) {
   constexpr int kHeads = 512 / D;
   const int groups = (a.dims.n_q_heads + 2 * a.dims.n_kv_heads + kHeads - 1) / kHeads;
   const bool norm = a.rope.q_weight != nullptr || a.rope.k_weight != nullptr;
-  const int64_t most = static_cast<int64_t>(attn_target_ctas()) / 2 * (norm || Q32 ? 2 : 3);   // CTAs that are on the GPU at once
+  const int64_t most = static_cast<int64_t>(attn_target_ctas()) / 2 * (Q32 ? 2 : 3);   // CTAs that are on the GPU at once
   // A row's angles are worth about one group of its heads: it is shared out only while warps lack work.
   const int64_t spare = most * kRopeWarps / a.n_rows;
   a.parts = static_cast<int>(spare < 1 ? 1 : spare < groups ? spare : groups);

@@ -64,13 +64,13 @@ HostPlan plan_rows(const bs_dims &d, int64_t n_rows, int max_new, bool tree) {
 
 // ---------------------------------------------------------------------------------------
 // Merge of split rows: a warp a row, a lane D / 32 elements. Two loads one after the other (what the
-// item is; its records, eight of them at a time in flight beside the maxima).
+// item is; its records, sixteen of them at a time in flight beside the maxima).
 // ---------------------------------------------------------------------------------------
 constexpr int kMergeWarps = 4;
 
 template <int D, bool kTree>
 __global__ void __launch_bounds__(kMergeWarps * 32) rows_merge_kernel(const __grid_constant__ RowsArgs a, const __grid_constant__ RowsPlan p) {
-  constexpr int E = D / 32, kAtOnce = 8;
+  constexpr int E = D / 32, kAtOnce = 16;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.wait;" ::: "memory");      // the splits' records
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");

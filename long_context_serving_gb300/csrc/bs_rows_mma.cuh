@@ -891,7 +891,7 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kRows>::kThreads, RowsTrait
           const int64_t out_row = (it.r.row0 + i) * a.dims.n_q_heads + it.h * G + gq;
           const int64_t rec = static_cast<int64_t>(blockIdx.x) * p.record_rows + (t * p.tokens * G + row);
           const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-          float odd = fabsf(l);
+          float odd[4] = {fabsf(l), 0.0f, 0.0f, 0.0f};     // NaN or infinite when the row's sums are
           const bool aligned = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0, rec_aligned = (reinterpret_cast<uintptr_t>(p.rec_o) & 31) == 0;
 #pragma unroll 1
           for (int c = 0; c < D / 32; ++c) {
@@ -901,7 +901,7 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kRows>::kThreads, RowsTrait
 #pragma unroll
             for (int x = 0; x < 32; ++x) {
               if (l == 0.0f) o[x] = 0.0f;      // (a row that has seen nothing: no product may have written its O)
-              odd = odd + 0.0f * o[x];         // NaN when one is not finite
+              odd[x % 4] = fmaf(0.0f, o[x], odd[x % 4]);
             }
             if (valid) {
               if (last) {
@@ -925,7 +925,7 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kRows>::kThreads, RowsTrait
             else if (a.lse != nullptr) a.lse[out_row] = l == 0.0f ? -INFINITY : (m_log2 + log2f(l)) * kLn2;
           }
           // Rows that are not finite are computed again, one after the other, by the whole warp.
-          unsigned again = __ballot_sync(0xffffffffu, valid && !(odd < INFINITY));
+          unsigned again = __ballot_sync(0xffffffffu, valid && !((odd[0] + odd[1]) + (odd[2] + odd[3]) < INFINITY));
           while (again != 0) {
             const int src = __ffs(again) - 1;
             again &= again - 1;
