@@ -39,8 +39,10 @@ HostPlan plan_rows(const bs_dims &d, int64_t n_rows, int max_new, bool tree) {
   h.p.record_rows = (max_new < h.p.block_tokens ? max_new : h.p.block_tokens) * G;
   const int at_once = h.rows == 32 ? 2 * kSms : kSms;                  // CTAs
   int64_t splits = 1;
-  if (tree && h.items <= kShareItems) {                                      // a wave of CTAs over the units' own tiles
-    if (tiles > 1) h.p.even = at_once;
+  if (tree && h.items * tiles <= at_once) {
+    splits = tiles;                                                   // a CTA a tile
+  } else if (tree && h.items <= kShareItems) {
+    h.p.even = at_once;                                               // a wave of CTAs over the units' own tiles
     splits = tiles;
   } else {
     splits = at_once / h.items;                                       // what one wave has room for
