@@ -41,7 +41,7 @@ HostPlan plan_rows(const bs_dims &d, int64_t n_rows, int max_new, bool tree) {
   int64_t splits = 1;
   if (tree && h.items * tiles <= at_once) {
     splits = tiles;                                                   // a CTA a tile
-  } else if (tree && h.items <= kShareItems) {
+  } else if (tree && h.items <= kShareItems && tiles < (1 << 20)) {
     h.p.even = at_once;                                               // a wave of CTAs over the units' own tiles
     splits = tiles;
   } else {

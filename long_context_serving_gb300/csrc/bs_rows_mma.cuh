@@ -90,11 +90,11 @@ struct ItemWords {
   UnitWords unit;
 };
 __device__ __forceinline__ ItemWords tree_words(const RowsArgs &a, const RowsPlan &p, int item) {
-  const int u = item / p.n_blocks;
+  const int u = p.n_blocks == 1 ? item : item / p.n_blocks;
   return ItemWords{seq_words<true>(a, u / a.dims.n_kv_heads), unit_words<true>(a, u)};
 }
 __device__ __forceinline__ int tree_item(const RowsArgs &a, const RowsPlan &p, int item, const ItemWords &w, RowsItem &it) {
-  const int u = item / p.n_blocks, block = item - u * p.n_blocks;
+  const int u = p.n_blocks == 1 ? item : item / p.n_blocks, block = item - u * p.n_blocks;
   it.b = u / a.dims.n_kv_heads;
   it.h = u - it.b * a.dims.n_kv_heads;
   it.i0 = it.i1 = 0;
@@ -135,12 +135,16 @@ __device__ __forceinline__ void tree_share(const RowsArgs &a, const RowsPlan &p,
     total += n[q];
   }
   total = __reduce_add_sync(0xffffffffu, total);
-  int per = max(1, (total + p.even - 1) / p.even);
+  int per = max(1, (total + p.even - 1) / p.even), pieces[kLaneItems];
   for (;; per += max(1, per / 16)) {
+    const float inv = __frcp_rn(static_cast<float>(per));
     int ctas = 0;
 #pragma unroll
-    for (int q = 0; q < kLaneItems; ++q)
-      if (q < used) ctas += (n[q] + per - 1) / per;
+    for (int q = 0; q < kLaneItems; ++q) {
+      // (the quotient is at least 1 / (2 per) from an integer, its error below that for n < 2^21)
+      pieces[q] = __float2int_rz((static_cast<float>(n[q] + per - 1) + 0.5f) * inv);
+      ctas += pieces[q];
+    }
     if (static_cast<int>(__reduce_add_sync(0xffffffffu, ctas)) <= p.even) break;   // (items are no more than CTAs)
   }
   int before = 0;
@@ -148,7 +152,7 @@ __device__ __forceinline__ void tree_share(const RowsArgs &a, const RowsPlan &p,
 #pragma unroll
   for (int q = 0; q < kLaneItems; ++q) {
     if (q >= used) break;
-    const int mine = (n[q] + per - 1) / per;
+    const int mine = pieces[q];
     int sum = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
