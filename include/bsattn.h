@@ -648,9 +648,11 @@ bs_status bs_rope_append(const bs_dims *dims, const bs_rope *rope, const void *q
  * n_q_heads * head_dim. out bf16 [n_rows][n_q_heads][head_dim], 16-byte aligned; lse fp32
  * [n_rows][n_q_heads], or NULL. Of cfg: cls, sink_tokens and local_tokens.
  * Weights are rounded to bf16 (relative to a running maximum, at most 2^-9 each) before they
- * meet V; logits, maxima, sums and outputs are fp32 until out's own rounding. A row that is
- * not finite after that is computed again in fp32 throughout, without its unseen keys, so
- * that an infinity or a NaN of a key it does not see cannot reach it.
+ * meet V; logits, maxima, sums and outputs are fp32 until out's own rounding (values of V up to
+ * 2^90, whose weighted sums stay finite on the way). An infinity or a NaN of a key that a row
+ * does not see does not reach it: where some rows of a block of tokens see such a value and
+ * others do not, the others are computed again without it, one by one. A row is not finite in
+ * a column in which it sees a V that is not, and in any if one of its logits is not.
  * max_new_tokens (host): an upper bound on seq_lens[b] - tok_begin[b]. It and n_rows size the
  * grid and choose the splits of long rows, and so the order of sums; a row's result does not
  * depend on what other sequences hold.

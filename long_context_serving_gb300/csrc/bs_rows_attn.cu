@@ -95,11 +95,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) rows_merge_kernel(const __gr
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
   float l = 0.0f, acc[E] = {};
-  auto add = [&](bool again) -> bool {        // false: a sum is not finite
-    l = 0.0f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-    if (m == -INFINITY) return true;
+  if (m != -INFINITY) {
     for (int s0 = 0; s0 < n; s0 += kAtOnce) {
       float w = 0.0f, part = 0.0f;            // lane s: weight and sum of record s0 + s
       if (lane < kAtOnce && s0 + lane < n) {
@@ -107,7 +103,7 @@ __global__ void __launch_bounds__(kMergeWarps * 32) rows_merge_kernel(const __gr
         w = x.x == -INFINITY ? 0.0f : exp2f(x.x - m);
         part = x.y;
       }
-      if (s0 > 0 || again) load(s0);
+      if (s0 > 0) load(s0);
 #pragma unroll
       for (int s = 0; s < kAtOnce; ++s) {
         const float ws = __shfl_sync(0xffffffffu, w, s);
@@ -116,14 +112,6 @@ __global__ void __launch_bounds__(kMergeWarps * 32) rows_merge_kernel(const __gr
         for (int e = 0; e < E; ++e) acc[e] = fmaf(o[s][e], ws, acc[e]);
       }
     }
-    float odd = fabsf(l);
-#pragma unroll
-    for (int e = 0; e < E; ++e) odd = odd + 0.0f * acc[e];
-    return __all_sync(0xffffffffu, odd < INFINITY);
-  };
-  if (!add(false)) {                          // (sums of the largest values of bf16: 2^24 below)
-    m += 24.0f;
-    add(true);
   }
   const int64_t out_row = (static_cast<int64_t>(head.z) + row / G) * a.dims.n_q_heads + h * G + row % G;
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;

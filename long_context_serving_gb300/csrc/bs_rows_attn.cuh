@@ -169,15 +169,16 @@ __device__ __forceinline__ bool sees(const Keys &k, const Group &g, int c, int i
 }
 
 // ---------------------------------------------------------------------------------------
-// One row by one warp, in fp32: lane l holds elements [l * D / 32, ...) of q and of the output.
-// x = q . K / sqrt(d) in log2 units, a running maximum m, sum l and unnormalised output o. A key
-// that the row does not see is not looked at. Weights are relative to 2^24 times the largest, so
-// that sums of the largest values of bf16 stay finite (they are why a row comes here, as much as
-// infinities are); m counts that factor.
+// Columns of one row by one warp, in fp32: lane l holds elements [l * D / 32, ...) of q and of the
+// output. `bad` (a bit an element) are columns that are not finite in a product that had an unseen
+// key's infinity or NaN in it. A key that the row does not see is not looked at; one that it does see
+// and that is not finite itself explains its columns (a logit, all of them), whose bits are cleared.
+// From the last key back, for what is not finite tends to be near and the search ends when nothing is
+// left to explain. For the columns that stay: o, unnormalised, relative to 2^m (log2 units).
 // ---------------------------------------------------------------------------------------
 template <int D, bool kTree>
-__device__ __noinline__ void row_attend(const RowsArgs &a, const SeqRows &r, const Keys &k, int h, int i, int gq, int g_lo,
-                                        int g_hi, float &m, float &l, float (&o)[D / 32]) {
+__device__ __noinline__ void row_columns(const RowsArgs &a, const SeqRows &r, const Keys &k, int h, int i, int gq, int g_lo,
+                                         int g_hi, uint32_t &bad, float &m, float (&o)[D / 32]) {
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31;
   const int G = a.dims.n_q_heads / a.dims.n_kv_heads;
@@ -191,7 +192,6 @@ __device__ __noinline__ void row_attend(const RowsArgs &a, const SeqRows &r, con
   }
   const uint64_t mask = kTree ? a.drafts.visible[r.row0 + i] : 0;
   m = -INFINITY;
-  l = 0.0f;
   const int dt = a.dims.kv_dtype;
   auto value = [&](const void *pool, int64_t at) -> float {
     if (dt == BS_BF16) return __bfloat162float(static_cast<const __nv_bfloat16 *>(pool)[at]);
@@ -201,13 +201,14 @@ __device__ __noinline__ void row_attend(const RowsArgs &a, const SeqRows &r, con
     codes_to_f32<false>(c, f);
     return f[0];
   };
-  for (int gi = g_lo; gi < g_hi; ++gi) {
+  for (int gi = g_hi - 1; gi >= g_lo; --gi) {
+    if (!__any_sync(0xffffffffu, bad != 0)) return;
     const Group g = key_group<kTree>(a, k, gi);
     if (g.page == -2) continue;
     const bool draft = g.page == -1;
     const bool quant = !draft && is_quant(dt);
     const float ks = quant ? a.kv.k_scale[g.page] : 1.0f, vs = quant ? a.kv.v_scale[g.page] : 1.0f;
-    for (int c = 0; c < kPage; ++c) {
+    for (int c = kPage - 1; c >= 0; --c) {
       if (!sees<kTree>(k, g, c, i, mask)) continue;
       const int64_t at = draft ? (r.row0 + g.base + c) * a.drafts.row_stride + static_cast<int64_t>(h) * D + lane * E
                                : (static_cast<int64_t>(g.page) * kPage + c) * D + lane * E;
@@ -218,13 +219,16 @@ __device__ __noinline__ void row_attend(const RowsArgs &a, const SeqRows &r, con
 #pragma unroll
       for (int s = 16; s > 0; s >>= 1) x += __shfl_xor_sync(0xffffffffu, x, s);
       x = x * ks * sc;
-      const float top = fmaxf(m, x + 24.0f);   // (a NaN stays out of the maximum and enters the sum)
-      const float keep = m == -INFINITY ? 0.0f : exp2f(m - top), w = top == -INFINITY ? 0.0f : exp2f(x - top);
+      if (!(fabsf(x) < INFINITY)) {
+        bad = 0;
+        return;
+      }
+      const float top = fmaxf(m, x), keep = m == -INFINITY ? 0.0f : exp2f(m - top), w = exp2f(x - top);
       m = top;
-      l = fmaf(l, keep, w);
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         const float v = draft ? __bfloat162float(static_cast<const __nv_bfloat16 *>(a.drafts.v_new)[at + e]) : value(a.kv.v_pool, at + e) * vs;
+        if (!(fabsf(v) < INFINITY)) bad &= ~(1u << e);
         o[e] = fmaf(o[e], keep, w * v);
       }
     }

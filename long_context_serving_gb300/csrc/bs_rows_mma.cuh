@@ -15,16 +15,16 @@
 // starts while the last are made and the rest of it and S do not wait for much. O is brought to a new maximum only when that has grown by more than 2^8
 // (weights of at most 256 in between; the final division takes it back), at the start of a
 // tile, when the products in flight are done: O's rescaling through registers is rare and needs no
-// warps of its own. What the second half's maximum adds, which is taken once its weights are on their
-// way, waits for the next tile (a weight too large for its type meanwhile makes the row one of those
-// that are computed again).
+// warps of its own. The second half of a tile is measured against the same reference, and only where
+// it passes that by 2^30 is everything brought to its maximum at once.
 // Precision: products of bf16 in fp32; weights enter as bf16 (2^-9 of themselves), which is the
 // operand type of V; their sum is taken before that rounding. Page scales: K's multiplies logits
 // in fp32; V's is m * 2^e, 2^e goes into the bf16 values (exact), m into the weights, so that
 // neither a tiny nor a large scale leaves the type's range on its own.
-// A key that no row may see has no place in a product: 0 times an infinity is a NaN. Slots past
-// the cache's end are zeroed, pages that are not there are left out, and a row whose sums are not
-// finite is computed again by row_attend.
+// A key that a row does not see still stands in its products, with a weight of 0, and 0 times an
+// infinity is a NaN. Slots past the cache's end are zeroed and pages that are not there left out; where
+// a group that rows see differently holds a value that is not finite, the block is marked, and its
+// rows' columns that are not finite are computed again without unseen keys (row_columns).
 #pragma once
 
 #include "bs_attn_launch.cuh"
@@ -69,6 +69,12 @@ __device__ __forceinline__ void store_sector(void *to, const uint32_t *w, bool a
     reinterpret_cast<uint4 *>(to)[0] = make_uint4(w[0], w[1], w[2], w[3]);
     reinterpret_cast<uint4 *>(to)[1] = make_uint4(w[4], w[5], w[6], w[7]);
   }
+}
+
+// Is one of eight bf16 infinite or NaN?
+__device__ __forceinline__ bool any_odd_bf16(uint4 w) {
+  auto top = [](uint32_t x) { return __vcmpgeu2(x & 0x7fff7fffu, 0x7f807f80u); };
+  return (top(w.x) | top(w.y) | top(w.z) | top(w.w)) != 0;
 }
 
 // What a CTA works on.
@@ -296,6 +302,7 @@ struct RowsShared {
   uint64_t q_full, s_full[2], p_full[2][2], o_full[2], never;   // (p_full: [row tile][part])
   uint32_t tmem;
   int failed;                 // a wait ran out
+  int marked;                 // a group that rows see differently has a V that is not finite
 };
 
 // kRows: rows of a CTA, 256 (two row tiles), 128 or 32. With 32 (single tokens, small trees) one row
@@ -412,6 +419,7 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kRows>::kThreads, RowsTrait
       }
       mbar_init(&sh.never, 1);
       sh.failed = 0;
+      sh.marked = 0;
       fence_mbar_init();
       fence_proxy_async_smem();
     }
@@ -566,6 +574,7 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kRows>::kThreads, RowsTrait
           ok = wait(&sh.raw_full[raw], item / kRaw & 1) && wait(&sh.empty[slot], (item / kSlots & 1) ^ 1);
           if (!ok) break;
           const TileInfo &info = sh.info[(j - t_lo) % kInfos];
+          bool odd = false;
           uint4 codes[kMine][kPieces];                       // (all on their way before the first store)
 #pragma unroll
           for (int i = 0; i < kMine; ++i)
@@ -589,6 +598,7 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kRows>::kThreads, RowsTrait
                   lo = ld_stream16(at);
                   hi = ld_stream16(at + 8);
                 }
+                odd |= kv == 1 && (any_odd_bf16(lo) || any_odd_bf16(hi));
                 put(rows, c, lo, hi);
               }
               continue;
@@ -604,11 +614,19 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kRows>::kThreads, RowsTrait
               codes_to_bf16<kKv == 2>(w.w, kv == 1, two_e, hi.z, hi.w);
               put(rows, c, lo, hi);
             }
-            if (base + kPage > k.T)                      // zeros behind the last token
+            if (flags & 1u)                              // a group that rows see differently
 #pragma unroll 1
-              for (int c = 0; c < kPieces; ++c)
-                if (base + c * kRowStep + row >= k.T) put(rows, c, make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u));
+              for (int c = 0; c < kPieces; ++c) {
+                if (base + c * kRowStep + row >= k.T) {
+                  put(rows, c, make_uint4(0u, 0u, 0u, 0u), make_uint4(0u, 0u, 0u, 0u));   // (zeros behind the last token)
+                } else if (kKv == 1 && kv == 1) {        // E4M3's NaN: all seven bits
+                  const uint4 w = *reinterpret_cast<const uint4 *>(raw_ring + raw * Tr::kRawBytes + gi * (kPage * D) + (c * kRowStep + row) * D + col);
+                  auto nan = [](uint32_t x) { return __vcmpeq4(x & 0x7f7f7f7fu, 0x7f7f7f7fu); };
+                  odd |= (nan(w.x) | nan(w.y) | nan(w.z) | nan(w.w)) != 0;
+                }
+              }
           }
+          if (__any_sync(0xffffffffu, odd)) *const_cast<volatile int *>(&sh.marked) = 1;
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
@@ -657,20 +675,29 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kRows>::kThreads, RowsTrait
         ok = wait(&sh.full[j % kInfos], j / kInfos & 1);      // V, and K of the next tile
         if (!ok) break;
         if constexpr (!Tr::kQuant) {
-          // rows of V past the cache's end or the drafts' are not zero by themselves
-          uint32_t marked = flags & ~(flags >> 8) & 0xffu;
-          if (marked != 0) {
-            while (marked != 0) {
-              const int i = __ffs(marked) - 1;
-              marked &= marked - 1;
+          // Groups that rows see differently: rows of V past the cache's end or the drafts' become zero
+          // (they hold anything), the others are looked at.
+          uint32_t differ = flags & ~(flags >> 8) & 0xffu;
+          if (differ != 0) {
+            bool odd = false;
+            while (differ != 0) {
+              const int i = __ffs(differ) - 1;
+              differ &= differ - 1;
               const int end = (kTree && (flags >> (16 + i) & 1u)) ? it.k.n_draft : it.k.T;
-              const int kept = end - info.base[i];
-              if (kept >= kPage) continue;
+              const int kept = min(end - info.base[i], kPage);
               unsigned char *at = ring + v_slot * Tr::kSlotBytes + i * (kPage * 128);
-              for (int c = lane; c < (kPage - kept) * 8 * Tr::kHalves; c += 32)
-                *reinterpret_cast<uint4 *>(at + (c % Tr::kHalves) * Tr::kHalfBytes + kept * 128 + c / Tr::kHalves * 16) = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 2
+              for (int c = lane; c < kPage * 8 * Tr::kHalves; c += 32) {
+                uint4 *piece = reinterpret_cast<uint4 *>(at + (c % Tr::kHalves) * Tr::kHalfBytes + c / Tr::kHalves * 16);
+                if (c / (8 * Tr::kHalves) < kept) odd |= any_odd_bf16(*piece);
+                else *piece = make_uint4(0u, 0u, 0u, 0u);
+              }
             }
             fence_proxy_async_smem();
+            if (__any_sync(0xffffffffu, odd)) {
+              *const_cast<volatile int *>(&sh.marked) = 1;
+              __threadfence_block();
+            }
             __syncwarp();
           }
         }
@@ -838,25 +865,10 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kRows>::kThreads, RowsTrait
             tmem_wait_ld<64>(first);
             if constexpr (kAhead) read(1, ahead);
             const float mx = fmaxf(max_of(0, first), pend);
-            bool late = false;
-            if (m == -INFINITY) {            // (nothing seen before: O's row is zero)
-              m = mx;
-              late = valid && m == -INFINITY;
-            }
-            if (__any_sync(0xffffffffu, late)) {      // a row's first keys are in the second half
-              if constexpr (!kAhead) read(1, first);
-              tmem_wait_ld<64>(second);
-              const float then = max_of(1, second);
-              if (m == -INFINITY) m = then;
-              if constexpr (!kAhead) {
-                read(0, first);
-                tmem_wait_ld<64>(first);
-              }
-            }
-            const bool grow = valid && (mx - m) * sc > 8.0f;
-            if (__any_sync(0xffffffffu, grow)) {
-              const float to = grow ? mx : m;
-              const float f = grow ? exp2_approx((m - to) * sc) : 1.0f;
+            if (m == -INFINITY) m = mx;      // (nothing seen before: O's row is zero)
+            // O's row, and l with it, relative to a new reference.
+            auto rescale = [&](float to) {
+              const float f = to == m ? 1.0f : exp2_approx((m - to) * sc);
               m = to;
               l *= f;
               if (j > 0) {
@@ -871,16 +883,41 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kRows>::kThreads, RowsTrait
                   tmem_st16(o_at + c * 16, w);
                 }
               }
-            }
+              return f;
+            };
+            const bool grow = valid && (mx - m) * sc > 8.0f;
+            if (__any_sync(0xffffffffu, grow)) rescale(grow ? mx : m);
             weigh(0, first);
             weigh(1, first + 32);
             if constexpr (!kAhead) read(1, first);
             tmem_wait_ld<64>(second);
+            pend = max_of(1, second);
+            if (m == -INFINITY) m = pend;    // (the first half's weights are zero too)
+            const bool far = valid && (pend - m) * sc > 30.0f;
+            if (__any_sync(0xffffffffu, far)) {
+              // the first half's weights are in tensor memory already
+              const float f = rescale(far ? pend : m);
+              sum[0] = __fmul2_rn(sum[0], make_float2(f, f));
+              sum[1] = __fmul2_rn(sum[1], make_float2(f, f));
+              tmem_wait_st();
+#pragma unroll 1
+              for (int c = 0; c < 2; ++c) {
+                float p16[16];
+                tmem_ld16(s_at + c * 16, p16);
+                tmem_wait_ld<16>(p16);
+                uint32_t w[16];
+#pragma unroll
+                for (int x = 0; x < 16; ++x) {
+                  const uint32_t u = __float_as_uint(p16[x]);
+                  w[x] = pack_bf16(bf16lo(u) * f, bf16hi(u) * f);
+                }
+                tmem_st16(s_at + c * 16, w);
+              }
+            }
             weigh(2, second);
             hand_over(0);
             weigh(3, second + 32);
             hand_over(1);
-            pend = max_of(1, second);
             l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
           } else if (lane == 0) {
             mbar_arrive(&sh.p_full[t][0]);
@@ -928,24 +965,33 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kRows>::kThreads, RowsTrait
             if (!last) p.rec_ml[rec] = make_float2(m_log2, l);
             else if (a.lse != nullptr) a.lse[out_row] = l == 0.0f ? -INFINITY : (m_log2 + log2f(l)) * kLn2;
           }
-          // Rows that are not finite are computed again, one after the other, by the whole warp.
-          unsigned again = __ballot_sync(0xffffffffu, valid && !((odd[0] + odd[1]) + (odd[2] + odd[3]) < INFINITY));
-          while (again != 0) {
-            const int src = __ffs(again) - 1;
-            again &= again - 1;
-            const int ri = __shfl_sync(0xffffffffu, i, src), rg = __shfl_sync(0xffffffffu, gq, src);
-            const int64_t r_out = __shfl_sync(0xffffffffu, out_row, src), r_rec = __shfl_sync(0xffffffffu, rec, src);
-            float rm, rl, ro[D / 32];
-            row_attend<D, kTree>(a, it.r, k, it.h, ri, rg, t_lo * kTileGroups, min(t_hi * kTileGroups, k.n_groups), rm, rl, ro);
-            __syncwarp();                      // (after what the row's own lane has written)
+          // A marked block: columns that are not finite, row by row, by the whole warp. (Sums of weights
+          // have no unseen key in them: where they are not finite, neither is the row.)
+          if (*const_cast<volatile int *>(&sh.marked) != 0) {
+            const bool sums = fabsf(l) < INFINITY;
+            unsigned again = __ballot_sync(0xffffffffu, valid && sums && !((odd[0] + odd[1]) + (odd[2] + odd[3]) < INFINITY));
+            __syncwarp();                      // (the lanes' rows are written)
+            while (again != 0) {
+              const int src = __ffs(again) - 1;
+              again &= again - 1;
+              const int ri = __shfl_sync(0xffffffffu, i, src), rg = __shfl_sync(0xffffffffu, gq, src);
+              const int64_t r_out = __shfl_sync(0xffffffffu, out_row, src), r_rec = __shfl_sync(0xffffffffu, rec, src);
+              const float r_m = __shfl_sync(0xffffffffu, m_log2, src), r_inv = __shfl_sync(0xffffffffu, inv, src);
+              __nv_bfloat16 *to = a.out + r_out * D + lane * (D / 32);
+              float *to_rec = p.rec_o + r_rec * D + lane * (D / 32);
+              uint32_t bad = 0;
 #pragma unroll
-            for (int e = 0; e < D / 32; ++e) {
-              if (last) a.out[r_out * D + lane * (D / 32) + e] = __float2bfloat16_rn(rl == 0.0f ? 0.0f : ro[e] / rl);
-              else p.rec_o[r_rec * D + lane * (D / 32) + e] = ro[e];
-            }
-            if (lane == 0) {
-              if (!last) p.rec_ml[r_rec] = make_float2(rm, rl);
-              else if (a.lse != nullptr) a.lse[r_out] = rl == 0.0f ? -INFINITY : (rm + log2f(rl)) * kLn2;
+              for (int e = 0; e < D / 32; ++e)
+                if (!(fabsf(last ? __bfloat162float(to[e]) : to_rec[e]) < INFINITY)) bad |= 1u << e;
+              float rm, ro[D / 32];
+              row_columns<D, kTree>(a, it.r, k, it.h, ri, rg, t_lo * kTileGroups, min(t_hi * kTileGroups, k.n_groups), bad, rm, ro);
+#pragma unroll
+              for (int e = 0; e < D / 32; ++e)
+                if (bad >> e & 1u) {
+                  const float x = ro[e] * exp2f(rm - r_m);
+                  if (last) to[e] = __float2bfloat16_rn(x * r_inv);
+                  else to_rec[e] = x;
+                }
             }
           }
         }

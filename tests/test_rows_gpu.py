@@ -361,16 +361,63 @@ def test_prefill_unseen_keys_do_not_matter(what):
 
 
 def test_prefill_large_values():
-    """Values whose weighted sums pass fp32 on the way, but not as results, come out."""
-    c = R.Cache(1, 1, 2, 64, [140], "bf16")
-    for lp in range(9):
-        c.v[c.table_np[0, lp], :, :] = 3.0e38
-    p = Prefill(c, [140])
+    """Values up to 2^90 and their sums stay finite, also where a later half of a tile passes the first
+    by far more than weights are let grow."""
+    c = R.Cache(1, 1, 2, 64, [400], "bf16")
+    x = float(torch.tensor(1.2e27).bfloat16())
+    c.v[:] = x
+    p = Prefill(c, [300])
     p.run()
     assert _sync_status(c) == 0
-    out = p.out[p.row0[0]:p.row0[0] + 140].double()
-    want = float(torch.tensor(3.0e38).bfloat16())
-    assert ((out - want).abs() <= 2 * R.HALF_BF16 * want).all()
+    out = p.out[p.row0[0]:p.row0[0] + 300].double()
+    assert ((out - x).abs() <= 2 * R.HALF_BF16 * x).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "int8"])
+@pytest.mark.parametrize("at", [5, 70, 100, 130, 200, 258])
+def test_prefill_logits_that_jump(kind, at):
+    """One key whose logit stands hundreds above the others', in either half of the first tiles and in
+    later ones: the reference follows it, and rows before it are as ever."""
+    c = R.Cache(1, 1, 4, 64, [300], kind, seed=at)
+    p = Prefill(c, [300])
+    lp, slot = c.table_np[0, at // 16], at % 16
+    q = p.q_np[p.row0[0]:p.row0[0] + 300].astype(np.float64)
+    key = q[:, 0].mean(0)
+    key = key / np.linalg.norm(key) * 4000.0
+    if kind == "bf16":
+        key = R.bf16(key)
+        c.k[lp, slot] = torch.as_tensor(key).bfloat16().cuda()
+        c.K[0][at] = key
+    else:                                         # the page's scale serves all its keys
+        code = Q.round_half_even(key / np.abs(key).max() * 127, "int8")
+        s = np.float32(np.abs(key).max() / 127)
+        f = np.float64(s) / np.float64(float(c.ks[lp]))
+        n = min(16, 300 - at // 16 * 16)
+        for t in range(n):
+            c.K[0][at // 16 * 16 + t] = c.K[0][at // 16 * 16 + t] * f
+        c.ks[lp] = float(s)
+        c.k.view(torch.uint8)[lp, slot] = torch.as_tensor(code).cuda()
+        c.K[0][at] = Q.decode(code, "int8") * np.float64(s)
+    p.run()
+    assert _sync_status(c) == 0
+    p.check(rows=80)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_prefill_cache_of_nan(kind):
+    """A cache that holds nothing else gives NaN, and soon: no row is searched to its end."""
+    c = R.Cache(1, 2, 4, 128, [6000], kind)
+    c.v.view(torch.uint8).fill_(0x7F if kind == "e4m3" else 0xFF)
+    p = Prefill(c, [3000])
+    p.run()
+    assert _sync_status(c) == 0
+    e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    e0.record()
+    p.run()
+    e1.record()
+    assert _sync_status(c) == 0
+    assert torch.isnan(p.out[p.row0[0]:p.row0[0] + 3000].float()).all()
+    assert e0.elapsed_time(e1) < 1000
 
 
 @pytest.mark.parametrize("kind", ["e4m3", "int8"])
