@@ -299,7 +299,7 @@ struct RowsShared {
   uint64_t empty[12];         // a slot's products are done
   uint64_t raw_full[8], raw_empty[8];
   uint64_t k0_full, full[kInfos];   // K of the first tile; V of a tile and K of the next one, have landed
-  uint64_t q_full, s_full[2], p_full[2][2], o_full[2], never;   // (p_full: [row tile][part])
+  uint64_t q_full, s_full[2], p_full[2][2], o_full[2], looked, never;   // (p_full: [row tile][part])
   uint32_t tmem;
   int failed;                 // a wait ran out
   int marked;                 // a group that rows see differently has a V that is not finite
@@ -333,6 +333,8 @@ struct RowsTraits {
   static constexpr int kWriters = !kQuant ? 1 : kRows == 32 ? 4 : 8;       // warps that fill a slot
   // Product warp, two copy warps, (8-bit) conversion warps, one on each scheduler, row warps from a
   // multiple of four.
+  // (bf16, 128 and 256 rows: the warp that is left over looks for values that are not finite.)
+  static constexpr bool kLooker = !kQuant && kRows != 32;
   static constexpr int kProduct = kRows == 32 ? 1 : 0, kCopy = kProduct + 1, kConvert = 4;
   static constexpr int kFirstRow = kRows == 32 ? 0 : kQuant ? 4 + kWriters : 4;
   static constexpr int kThreads = 32 * (kRows == 32 ? (kQuant ? 8 : 4) : kFirstRow + kRowWarps);
@@ -402,7 +404,7 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kRows>::kThreads, RowsTrait
     tmem_alloc(&sh.tmem, Tr::kColumns);
     if (lane == 0) {
       for (int i = 0; i < kSlots; ++i) {
-        mbar_init(&sh.empty[i], 1);
+        mbar_init(&sh.empty[i], Tr::kLooker ? 2 : 1);
       }
       mbar_init(&sh.k0_full, Tr::kWriters);
       for (int i = 0; i < kInfos; ++i) mbar_init(&sh.full[i], 2 * Tr::kWriters);
@@ -417,6 +419,7 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kRows>::kThreads, RowsTrait
         mbar_init(&sh.p_full[t][1], Tr::kTileWarps);
         mbar_init(&sh.o_full[t], 1);
       }
+      mbar_init(&sh.looked, 1);
       mbar_init(&sh.never, 1);
       sh.failed = 0;
       sh.marked = 0;
@@ -455,6 +458,27 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kRows>::kThreads, RowsTrait
     if (__all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, a.st, p.wait_ns))) return true;
     *const_cast<volatile int *>(&sh.failed) = 1;
     return false;
+  };
+
+  // Rows of group i of a tile that are tokens or drafts (bf16).
+  auto kept_rows = [&](const TileInfo &info, int i) -> int {
+    const int end = (kTree && (info.flags >> (16 + i) & 1u)) ? it.k.n_draft : it.k.T;
+    return min(end - info.base[i], kPage);
+  };
+  // Marks the block if a V of a group that rows see differently is not finite (bf16; a whole warp).
+  auto look = [&](const TileInfo &info, int slot) {
+    bool odd = false;
+    for (uint32_t left = info.flags & ~(info.flags >> 8) & 0xffu; left != 0; left &= left - 1) {
+      const int i = __ffs(left) - 1, kept = kept_rows(info, i);
+      const unsigned char *at = ring + slot * Tr::kSlotBytes + i * (kPage * 128);
+#pragma unroll 2
+      for (int c = lane; c < kept * 8 * Tr::kHalves; c += 32)
+        odd |= any_odd_bf16(*reinterpret_cast<const uint4 *>(at + (c % Tr::kHalves) * Tr::kHalfBytes + c / Tr::kHalves * 16));
+    }
+    if (__any_sync(0xffffffffu, odd)) {
+      *const_cast<volatile int *>(&sh.marked) = 1;
+      __threadfence_block();
+    }
   };
 
   if (t_lo < t_hi) {
@@ -675,29 +699,17 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kRows>::kThreads, RowsTrait
         ok = wait(&sh.full[j % kInfos], j / kInfos & 1);      // V, and K of the next tile
         if (!ok) break;
         if constexpr (!Tr::kQuant) {
-          // Groups that rows see differently: rows of V past the cache's end or the drafts' become zero
-          // (they hold anything), the others are looked at.
+          // rows of V past the cache's end or the drafts' hold anything: they become zero
           uint32_t differ = flags & ~(flags >> 8) & 0xffu;
           if (differ != 0) {
-            bool odd = false;
-            while (differ != 0) {
-              const int i = __ffs(differ) - 1;
-              differ &= differ - 1;
-              const int end = (kTree && (flags >> (16 + i) & 1u)) ? it.k.n_draft : it.k.T;
-              const int kept = min(end - info.base[i], kPage);
+            for (uint32_t left = differ; left != 0; left &= left - 1) {
+              const int i = __ffs(left) - 1, kept = kept_rows(info, i);
               unsigned char *at = ring + v_slot * Tr::kSlotBytes + i * (kPage * 128);
-#pragma unroll 2
-              for (int c = lane; c < kPage * 8 * Tr::kHalves; c += 32) {
-                uint4 *piece = reinterpret_cast<uint4 *>(at + (c % Tr::kHalves) * Tr::kHalfBytes + c / Tr::kHalves * 16);
-                if (c / (8 * Tr::kHalves) < kept) odd |= any_odd_bf16(*piece);
-                else *piece = make_uint4(0u, 0u, 0u, 0u);
-              }
+              for (int c = kept * 8 * Tr::kHalves + lane; c < kPage * 8 * Tr::kHalves; c += 32)
+                *reinterpret_cast<uint4 *>(at + (c % Tr::kHalves) * Tr::kHalfBytes + c / Tr::kHalves * 16) = make_uint4(0u, 0u, 0u, 0u);
             }
             fence_proxy_async_smem();
-            if (__any_sync(0xffffffffu, odd)) {
-              *const_cast<volatile int *>(&sh.marked) = 1;
-              __threadfence_block();
-            }
+            if constexpr (!Tr::kLooker) look(info, v_slot);
             __syncwarp();
           }
         }
@@ -739,6 +751,24 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kRows>::kThreads, RowsTrait
           }
         }
       }
+    } else if (Tr::kLooker && warp == 3) {
+      // ---- looks at V tiles beside the products; a slot is free when both are done with it ---------
+      const int n = t_hi - t_lo;
+      bool ok = wait(&sh.k0_full, 0);
+      if (ok && lane == 0) mbar_arrive(&sh.empty[0]);
+      for (int j = 0; j < n && ok; ++j) {
+        ok = wait(&sh.full[j % kInfos], j / kInfos & 1);
+        if (!ok) break;
+        const int v_slot = (2 * j + 1) % kSlots;
+        const TileInfo &info = sh.info[j % kInfos];
+        if ((info.flags & ~(info.flags >> 8) & 0xffu) != 0) look(info, v_slot);
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&sh.empty[v_slot]);
+          if (j + 1 < n) mbar_arrive(&sh.empty[(2 * j + 2) % kSlots]);
+        }
+      }
+      if (ok && lane == 0) mbar_arrive(&sh.looked);
     } else if (warp >= Tr::kFirstRow && warp < Tr::kFirstRow + Tr::kRowWarps) {
       // ---- row warps -----------------------------------------------------------------------------
       const int t = (warp - Tr::kFirstRow) / Tr::kTileWarps;
@@ -967,7 +997,7 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kRows>::kThreads, RowsTrait
           }
           // A marked block: columns that are not finite, row by row, by the whole warp. (Sums of weights
           // have no unseen key in them: where they are not finite, neither is the row.)
-          if (*const_cast<volatile int *>(&sh.marked) != 0) {
+          if ((!Tr::kLooker || wait(&sh.looked, 0)) && *const_cast<volatile int *>(&sh.marked) != 0) {
             const bool sums = fabsf(l) < INFINITY;
             unsigned again = __ballot_sync(0xffffffffu, valid && sums && !((odd[0] + odd[1]) + (odd[2] + odd[3]) < INFINITY));
             __syncwarp();                      // (the lanes' rows are written)
