@@ -40,13 +40,22 @@ HostPlan plan_rows(const bs_dims &d, int64_t n_rows, int max_new, bool tree) {
   const int at_once = h.rows == 32 ? 2 * kSms : kSms;                  // CTAs
   int64_t splits = 1;
   if (tree && h.items * tiles <= at_once) {
-    splits = tiles;                                                   // a CTA a tile
+    splits = tiles;             // a CTA a tile: no more than a wave whatever the selections are
   } else if (tree && h.items <= kShareItems && tiles < (1 << 20)) {
-    h.p.even = at_once;                                               // a wave of CTAs over the units' own tiles
+    // One wave over the units' own tiles (128K trees of uneven units: 58 us, an even number of splits
+    // 65; working it out takes a CTA 1 to 2 us, which the case above does without: 10.2 us for 12.7).
+    h.p.even = at_once;
     splits = tiles;
   } else {
-    splits = at_once / h.items;                                       // what one wave has room for
-    if (h.rows < 256 && tiles > 32 && splits < (tiles + 23) / 24) splits = (tiles + 23) / 24;   // pieces of about 24 tiles
+    // What one wave has room for. Fewer rows than a tensor core's worth are bound by memory, and by
+    // how evenly CTAs get their keys: pieces of about 24 tiles (32 sequences of 2K to 16K tokens: 165
+    // us; 48 tiles 174, 12 tiles 167, whole sequences 229), while that is no more than eight waves of CTAs, which leave at once
+    // where a sequence is shorter. Two row tiles are bound by their products, and split no further.
+    splits = at_once / h.items;
+    if (h.rows < 256 && tiles > 32) {
+      const int64_t pieces = (tiles + 23) / 24, room = 8 * at_once / h.items;
+      if (splits < (pieces < room ? pieces : room)) splits = pieces < room ? pieces : room;
+    }
   }
   if (splits > tiles) splits = tiles;
   const int64_t row_bytes = static_cast<int64_t>(h.p.record_rows) * d.head_dim * 4;
