@@ -7,7 +7,7 @@
 // while its warp walks the row's heads, four (d = 128) or eight (d = 64) at a time. Few rows are
 // split over several warps each.
 // Loads of the next heads fly beside this turn's work, a row's first ones beside its angles. Bound by
-// HBM in prompts (26K rows of 28 + 8 heads, bf16: 97 us, 5.5 TB/s, with norms 99; fp32 6.25 TB/s), by one
+// HBM in prompts (29K rows of 28 + 8 heads, bf16: 97 us, 5.5 TB/s, with norms 99; fp32 6.25 TB/s), by one
 // chain of loads in decode steps (64 rows with norms, 3.1 us in a graph).
 // Angles: position * inv_freq in turns, inv_freq / 2 pi held as two floats (high and low part,
 // from one fp64 product a frequency and block), the product's rounding error taken back by an

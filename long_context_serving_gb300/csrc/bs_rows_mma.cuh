@@ -22,8 +22,9 @@
 // from shared memory just what that delivers meanwhile (128 bytes a cycle); two row tiles are what
 // tensor memory holds (512 columns: S and O of each, weights over S).
 // Bounds, measured: with two row tiles, S's and O's products (2,048 cycles a key tile) against a
-// tile's chain of 330 (S ready) + 1,500 to 1,700 (softmax) + 900 cycles: half of a 16K prompt, 8 heads of
-// 4 queries, half of them streaming, 650 to 665 us, 1.47 PFLOP/s, tensor pipe 62 % busy. 8-bit caches
+// tile's chain of 330 (S ready) + 1,640 to 1,800 (softmax) + 900 cycles, by clock stamps in an
+// instrumented copy of an earlier step: half of a 16K prompt, 8 heads of 4 queries, half of them
+// streaming, 644 to 684 us over several machines, 1.42 to 1.51 PFLOP/s. 8-bit caches
 // wait for conversion and shared memory (windows of four ragged chunks 180 us, bf16 134). With few
 // rows HBM: 32 sequences' single tokens over 2K to 16K tokens 164 us, 5.95 TB/s; E4M3 223 us, conversion.
 // Small trees: launch, lookup, copy, products, records and merge one after another, 10.7 us for eight
