@@ -5,6 +5,7 @@ tokens into the paged pool; every step of the decode path is a libbsattn call.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 import numpy as np
@@ -21,6 +22,13 @@ def _kv_tensor(arr: np.ndarray, dtype: str, device) -> torch.Tensor:
     if dtype == "bf16":
         return torch.from_numpy(np.ascontiguousarray(arr).view(np.int16)).to(device).view(torch.bfloat16)
     return torch.from_numpy(np.ascontiguousarray(arr, dtype=np.float32)).to(device)
+
+
+def _on(stream):
+    """torch's own work on `stream` too (a Stream, a raw handle, or None: the current one)."""
+    if stream is None:
+        return contextlib.nullcontext()
+    return torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream))))
 
 
 class PagedLayer:
@@ -241,54 +249,97 @@ class PagedLayer:
         self.advance()
 
     # -- prompts and drafts --------------------------------------------------------
+    # What these calls allocate and upload belongs to the stream they run on, workspaces too: calls on
+    # two streams share nothing, and memory given back is reused behind the kernels that read it.
     def prefill_attend(self, q: torch.Tensor, lo, hi, stream=None):
         """Tokens [lo[b], hi[b]) of every sequence, already in the cache, attend it: q bf16
         [rows][Hq][d], the sequences' rows one behind another. Streaming heads look at their
-        sink and window, the others at everything. Returns out (like q) and lse."""
-        lo, hi = np.asarray(lo, np.int64), np.asarray(hi, np.int64)
+        sink and window, the others at everything. Returns out (packed) and lse."""
+        self._check_q(q)
+        lo, hi = self._per_sequence("lo", lo), self._per_sequence("hi", hi)
         n = hi - lo
-        i32 = lambda a: torch.as_tensor(np.ascontiguousarray(a, dtype=np.int32), device=self.device)  # noqa: E731
-        out = torch.zeros_like(q)
-        lse = torch.zeros(q.shape[:2], dtype=torch.float32, device=self.device)
-        self._rows_ws = self._rows_workspace(B.prefill_workspace_size(self.dims, q.shape[0], max(1, int(n.max()))))
-        self._rows_in = i32(hi), i32(lo), i32(np.cumsum(n) - n)
-        B.prefill_attn(self.dims, q, q.stride(0), q.shape[0], self.kv_at(self._rows_in[0]), self.cfg, self._rows_in[1],
-                       self._rows_in[2], max(1, int(n.max())), out, lse, self._rows_ws, self.status, stream)
+        most = max(1, int(n.max()))
+        with _on(stream):
+            out, lse = self._rows_out(q)
+            lens, begin, first = self._i32(hi), self._i32(lo), self._i32(np.cumsum(n) - n)
+            ws = self._rows_workspace(B.prefill_workspace_size(self.dims, q.shape[0], most))
+            B.prefill_attn(self.dims, q, q.stride(0), q.shape[0], self.kv_at(lens), self.cfg, begin, first, most, out, lse,
+                           ws, self.status, stream)
         return out, lse
 
     def draft_attend(self, q: torch.Tensor, k_new, v_new, n_draft, visible, lens, stream=None):
         """Trees of drafts, n_draft[b] of them for sequence b, attend the blocks of the last selection
-        (the one that became the previous) and the drafts that `visible` names; lens[b] tokens are in
-        the cache. k_new, v_new: rows of all KV heads. Returns out (like q) and lse."""
-        n = np.asarray(n_draft, np.int64)
-        i32 = lambda a: torch.as_tensor(np.ascontiguousarray(a, dtype=np.int32), device=self.device)  # noqa: E731
-        out = torch.zeros_like(q)
-        lse = torch.zeros(q.shape[:2], dtype=torch.float32, device=self.device)
+        (the one that became the previous) and the drafts that `visible` (int64, a row's mask) names;
+        lens[b] tokens are in the cache. k_new, v_new: rows of all KV heads, bf16. Returns out (packed)
+        and lse."""
+        self._check_q(q)
+        rows = q.shape[0]
+        self._check_new(k_new, v_new, rows, torch.bfloat16)
+        if visible.dtype != torch.int64 or not visible.is_contiguous() or visible.numel() < rows or visible.device.type != self.device.type:
+            raise ValueError("visible is int64, contiguous, a mask for every row, on the layer's device")
+        n, lens = self._per_sequence("n_draft", n_draft), self._per_sequence("lens", lens)
         most = max(1, int(n.max()))
-        self._rows_ws = self._rows_workspace(B.tree_workspace_size(self.dims, most))
-        self._rows_in = i32(lens), i32(np.cumsum(n) - n), i32(n)
-        drafts = B.Drafts(k_new=k_new.data_ptr(), v_new=v_new.data_ptr(), row_stride=k_new.stride(0), n_rows=q.shape[0],
-                          row_begin=self._rows_in[1].data_ptr(), n_draft=self._rows_in[2].data_ptr(),
-                          visible=visible.data_ptr(), max_draft=most)
         last = 1 - self.cur
-        B.tree_decode_attn(self.dims, q, q.stride(0), self.kv_at(self._rows_in[0]), self.cfg, self.sel[last], self.cnt[last],
-                           drafts, out, lse, self._rows_ws, self.status, stream)
+        with _on(stream):
+            out, lse = self._rows_out(q)
+            at, first, count = self._i32(lens), self._i32(np.cumsum(n) - n), self._i32(n)
+            drafts = B.Drafts(k_new=k_new.data_ptr(), v_new=v_new.data_ptr(), row_stride=k_new.stride(0), n_rows=rows,
+                              row_begin=first.data_ptr(), n_draft=count.data_ptr(), visible=visible.data_ptr(), max_draft=most)
+            ws = self._rows_workspace(B.tree_workspace_size(self.dims, most))
+            B.tree_decode_attn(self.dims, q, q.stride(0), self.kv_at(at), self.cfg, self.sel[last], self.cnt[last], drafts,
+                               out, lse, ws, self.status, stream)
         return out, lse
 
     def commit_drafts(self, k_new, v_new, n_draft, path, lens, stream=None) -> None:
         """The accepted drafts of each sequence, path[b] (node numbers, -1 behind the last), enter the
         cache behind its lens[b] tokens."""
-        n, path, lens = np.asarray(n_draft, np.int64), np.asarray(path, np.int64), np.asarray(lens, np.int64)
-        i32 = lambda a: torch.as_tensor(np.ascontiguousarray(a, dtype=np.int32), device=self.device)  # noqa: E731
+        n, lens = self._per_sequence("n_draft", n_draft), self._per_sequence("lens", lens)
+        path = np.asarray(path, np.int64)
+        if path.ndim != 2 or path.shape[0] != self.wl.B:
+            raise ValueError("path is [batch][nodes]")
+        live = path >= 0
+        if (live[:, 1:] & ~live[:, :-1]).any() or (path >= np.maximum(n, 0)[:, None]).any():
+            raise ValueError("a path names its own sequence's drafts, and -1 only behind the last")
+        rows = int(n.sum())
+        self._check_new(k_new, v_new, rows, torch.float32 if self.dims.q_dtype == B.BS_FP32 else torch.bfloat16)
         pools = self.pools if self.kv8 else B.Pools(k_pool=self.k_pool.data_ptr(), v_pool=self.v_pool.data_ptr())
-        self._rows_in = i32(lens + (path >= 0).sum(1)), i32(lens), i32(np.cumsum(n) - n), i32(path)
-        B.tree_commit(self.dims, pools, self.page_table, *self._rows_in, path.shape[1], k_new, v_new, k_new.stride(0),
-                      int(n.sum()), self.status, stream)
+        with _on(stream):
+            to, begin, first, nodes = self._i32(lens + live.sum(1)), self._i32(lens), self._i32(np.cumsum(n) - n), self._i32(path)
+            B.tree_commit(self.dims, pools, self.page_table, to, begin, first, nodes, path.shape[1], k_new, v_new,
+                          k_new.stride(0), rows, self.status, stream)
 
-    def _rows_workspace(self, size: int):
-        have = getattr(self, "_rows_ws", None)
-        return have if have is not None and have.numel() >= max(size, 16) else \
-            torch.empty(max(size, 16), dtype=torch.uint8, device=self.device)
+    def _i32(self, a) -> torch.Tensor:
+        return torch.as_tensor(np.ascontiguousarray(a, dtype=np.int32), device=self.device)
+
+    def _per_sequence(self, name: str, a) -> np.ndarray:
+        a = np.asarray(a, np.int64)
+        if a.shape != (self.wl.B,):
+            raise ValueError(f"{name} has one number a sequence ({self.wl.B}), not shape {a.shape}")
+        return a
+
+    def _check_q(self, q: torch.Tensor) -> None:
+        wl = self.wl
+        if q.dtype != torch.bfloat16 or q.ndim != 3 or tuple(q.shape[1:]) != (wl.Hq, wl.d) or q.stride(2) != 1 or \
+                (wl.Hq > 1 and q.stride(1) != wl.d) or q.device.type != self.device.type:
+            raise ValueError(f"q is bf16 [rows][{wl.Hq}][{wl.d}] on the layer's device, a row's heads one behind another")
+
+    def _check_new(self, k_new: torch.Tensor, v_new: torch.Tensor, rows: int, dtype) -> None:
+        width = self.wl.Hkv * self.wl.d
+        for x in (k_new, v_new):
+            flat = x.ndim == 2 and x.shape[1] == width and x.stride(1) == 1
+            heads = x.ndim == 3 and tuple(x.shape[1:]) == (self.wl.Hkv, self.wl.d) and x.stride(2) == 1 and \
+                (self.wl.Hkv == 1 or x.stride(1) == self.wl.d)
+            if not (flat or heads) or x.dtype != dtype or x.shape[0] < rows or x.stride(0) != k_new.stride(0) or \
+                    x.device.type != self.device.type:
+                raise ValueError(f"k_new and v_new are {dtype} rows of {width} elements, {rows} of them at least, of one "
+                                 "stride, on the layer's device")
+
+    def _rows_out(self, q: torch.Tensor):
+        return (torch.zeros(tuple(q.shape), dtype=q.dtype, device=self.device),
+                torch.zeros(tuple(q.shape[:2]), dtype=torch.float32, device=self.device))
+
+    def _rows_workspace(self, size: int) -> torch.Tensor:
+        return torch.empty(max(size, 16), dtype=torch.uint8, device=self.device)
 
     def advance(self) -> None:
         """The current selection becomes the previous one."""
