@@ -516,7 +516,8 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kRows>::kThreads, RowsTrait
           x.ks = a.kv.k_scale[g.page];
           x.vs = a.kv.v_scale[g.page];
         }
-        const uint32_t f = group_flags<kTree>(k, g, it.i0, it.i1);
+        uint32_t f = group_flags<kTree>(k, g, it.i0, it.i1);
+        if (Tr::kQuant && x.ks != x.ks) f |= 1u;     // (a NaN scale of K: the row warps put it into the logits)
         x.differ = __ballot_sync(0xffffffffu, f & 1u);
         x.absent = __ballot_sync(0xffffffffu, f & 0x100u);
         x.drafts = __ballot_sync(0xffffffffu, f & 0x10000u);
@@ -650,6 +651,7 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kRows>::kThreads, RowsTrait
               codes_to_bf16<kKv == 2>(w.w, kv == 1, two_e, hi.z, hi.w);
               put(rows, c, lo, hi);
             }
+            if ((flags & 1u) && kv == 1) odd |= !(fabsf(info.vs[gi]) < INFINITY);
             if (flags & 1u)                              // a group that rows see differently
 #pragma unroll 1
               for (int c = 0; c < kPieces; ++c) {
@@ -828,6 +830,7 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kRows>::kThreads, RowsTrait
                 float x[32];
                 tmem_ld32(s_at + c32 * 32, x);
                 uint32_t seen = 0;             // a bit a key
+                float nan_or_1[2] = {1.0f, 1.0f};
 #pragma unroll
                 for (int y = 0; y < 2; ++y) {
                   const int gi = c32 * 2 + y;
@@ -850,11 +853,12 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kRows>::kThreads, RowsTrait
                     }
                   }
                   seen |= (bits & 0xffffu) << (16 * y);
+                  if (Tr::kQuant && info.ks[gi] != info.ks[gi]) nan_or_1[y] = info.ks[gi];   // (the weights' bound below drops it)
                 }
                 tmem_wait_ld<32>(x);
                 uint32_t w[32];
 #pragma unroll
-                for (int c = 0; c < 32; ++c) w[c] = seen >> c & 1u ? __float_as_uint(x[c]) : 0xff800000u;
+                for (int c = 0; c < 32; ++c) w[c] = seen >> c & 1u ? __float_as_uint(Tr::kQuant ? x[c] * nan_or_1[c / 16] : x[c]) : 0xff800000u;
                 tmem_st16(s_at + c32 * 32, w);
                 tmem_st16(s_at + c32 * 32 + 16, w + 16);
               }
