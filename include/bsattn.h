@@ -652,7 +652,8 @@ bs_status bs_rope_append(const bs_dims *dims, const bs_rope *rope, const void *q
  * 2^90, whose weighted sums stay finite on the way). An infinity or a NaN of a key that a row
  * does not see does not reach it: where some rows of a block of tokens see such a value and
  * others do not, the others are computed again without it, one by one. A row is not finite in
- * a column in which it sees a V that is not, and in any if one of its logits is not.
+ * a column in which it sees a V that is not (a page's scale counts), and in any if one of its
+ * logits is NaN or +inf; a key with a logit of -inf weighs nothing.
  * max_new_tokens (host): an upper bound on seq_lens[b] - tok_begin[b]. It and n_rows size the
  * grid and choose the splits of long rows, and so the order of sums; a row's result does not
  * depend on what other sequences hold.

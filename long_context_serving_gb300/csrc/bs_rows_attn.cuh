@@ -172,7 +172,8 @@ __device__ __forceinline__ bool sees(const Keys &k, const Group &g, int c, int i
 // Columns of one row by one warp, in fp32: lane l holds elements [l * D / 32, ...) of q and of the
 // output. `bad` (a bit an element) are columns that are not finite in a product that had an unseen
 // key's infinity or NaN in it. A key that the row does not see is not looked at; one that it does see
-// and that is not finite itself explains its columns (a logit, all of them), whose bits are cleared.
+// and that is not finite itself explains its columns (a logit of NaN or +inf, all of them), whose bits are
+// cleared; one of -inf weighs nothing.
 // From the last key back, for what is not finite tends to be near and the search ends when nothing is
 // left to explain. For the columns that stay: o, unnormalised, relative to 2^m (log2 units).
 // ---------------------------------------------------------------------------------------
@@ -219,11 +220,11 @@ __device__ __noinline__ void row_columns(const RowsArgs &a, const SeqRows &r, co
 #pragma unroll
       for (int s = 16; s > 0; s >>= 1) x += __shfl_xor_sync(0xffffffffu, x, s);
       x = x * ks * sc;
-      if (!(fabsf(x) < INFINITY)) {
+      if (!(x < INFINITY)) {
         bad = 0;
         return;
       }
-      const float top = fmaxf(m, x), keep = m == -INFINITY ? 0.0f : exp2f(m - top), w = exp2f(x - top);
+      const float top = fmaxf(m, x), keep = m == -INFINITY ? 0.0f : exp2f(m - top), w = x == -INFINITY ? 0.0f : exp2f(x - top);
       m = top;
 #pragma unroll
       for (int e = 0; e < E; ++e) {

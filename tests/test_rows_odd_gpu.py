@@ -57,3 +57,29 @@ def test_k_scales_that_are_nan(kind, page, rows):
             continue
         want = R.attend_row(p.q_np[p.row0[0] + i, g].astype(np.float64), c.K[0][:pos + 1], c.V[0][:pos + 1])
         R.check_row(row, z, want, (i, g))
+
+
+@pytest.mark.parametrize("rows", [6, 40, 150])
+def test_a_logit_of_minus_infinity_weighs_nothing(rows):
+    """Beside it a V that only the last row sees is NaN: the other rows, computed again without it, still
+    take the key of weight zero for one."""
+    T = 195
+    c = R.Cache(1, 1, 4, 64, [T], "bf16")
+    p = Prefill(c, [rows])
+    p.q_np[..., 3] = 1.0
+    p.q.view(p.rows, 4, 64)[..., 3] = 1.0
+    low = 140                                            # in the last key's tile, whatever the split
+    c.k[int(c.table_np[0, low // 16]), low % 16, 3] = float("-inf")
+    c.v[int(c.table_np[0, (T - 1) // 16]), (T - 1) % 16] = float("nan")
+    p.run()
+    assert _sync_status(c) == 0
+    out = p.out.double().cpu().numpy()
+    for i, g in itertools.product(range(rows), range(4)):
+        pos, row = T - rows + i, out[p.row0[0] + i, g]
+        if pos == T - 1:
+            assert np.isnan(row).all()
+            continue
+        s = np.arange(T) <= pos
+        s[low] = False
+        want = R.attend_row(p.q_np[p.row0[0] + i, g].astype(np.float64), c.K[0][s], c.V[0][s])
+        R.check_row(row, float(p.lse[p.row0[0] + i, g]), want, (i, g))
