@@ -647,8 +647,8 @@ bs_status bs_rope_append(const bs_dims *dims, const bs_rope *rope, const void *q
  * q: n_rows rows of q_stride elements, 16-byte aligned, q_stride a multiple of 8 and at least
  * n_q_heads * head_dim. out bf16 [n_rows][n_q_heads][head_dim], 16-byte aligned; lse fp32
  * [n_rows][n_q_heads], or NULL. Of cfg: cls, sink_tokens and local_tokens.
- * Weights are rounded to bf16 (relative to a running maximum, at most 2^-9 each) before they
- * meet V; logits, maxima, sums and outputs are fp32 until out's own rounding (values of V up to
+ * Weights (with an 8-bit cache times the mantissa of V's scale) are rounded to bf16, off by at most
+ * 2^-8 of themselves each, before they meet V; logits, maxima, sums and outputs are fp32 until out's own rounding (values of V up to
  * 2^90, whose weighted sums stay finite on the way). An infinity or a NaN of a key that a row
  * does not see does not reach it: where some rows of a block of tokens see such a value and
  * others do not, the others are computed again without it, one by one. A row is not finite in

@@ -26,7 +26,7 @@
 // instrumented copy of an earlier step: half of a 16K prompt, 8 heads of 4 queries, half of them
 // streaming, 644 to 684 us over several machines, 1.42 to 1.51 PFLOP/s. 8-bit caches
 // wait for conversion and shared memory (windows of four ragged chunks 180 us, bf16 134). With few
-// rows HBM: 32 sequences' single tokens over 2K to 16K tokens 164 us, 5.95 TB/s; E4M3 223 us, conversion.
+// rows HBM: 32 sequences' single tokens over 2K to 16K tokens 164 us, 5.95 TB/s; E4M3 221 us, conversion.
 // Small trees: launch, lookup, copy, products, records and merge one after another, 10.7 us for eight
 // drafts over 32K tokens.
 // Precision: products of bf16 in fp32; weights enter as bf16 (2^-9 of themselves), which is the
@@ -301,7 +301,8 @@ struct TileInfo {
   int base[kTileGroups];      // first key of each group
   uint32_t flags;             // bits 0..7: rows differ in what they see of the group, or its end is
                               // past the cache's; 8..15: it is not there; 16..23: it is of drafts
-  float ks[kTileGroups], vs[kTileGroups];   // 8-bit caches: K's scale, mantissa of V's
+  float2 ks[kTileGroups];     // 8-bit caches: K's scale; log2 of the mantissa of V's, in the logits' units
+  float vs[kTileGroups];                    // that mantissa
   float ve[kTileGroups];                    // and its power of two
 };
 
@@ -503,7 +504,7 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kRows>::kThreads, RowsTrait
       // three loads one behind another, mostly from memory.
       struct Lookup {
         Group g;
-        float ks, vs;
+        float ks, vs, ve, lv;                // as in TileInfo
         uint32_t differ, absent, drafts;     // of the 32 groups, as in TileInfo::flags
       };
       auto look_up = [&](int j) -> Group {
@@ -511,10 +512,13 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kRows>::kThreads, RowsTrait
         return i < min(k.n_groups, t_hi * kTileGroups) ? key_group<kTree>(a, k, i) : Group{0, -2};
       };
       auto complete = [&](const Group &g) -> Lookup {
-        Lookup x{g, 1.0f, 1.0f, 0u, 0u, 0u};
+        Lookup x{g, 1.0f, 1.0f, 1.0f, 0.0f, 0u, 0u, 0u};
         if (Tr::kQuant && kv == 0 && g.page >= 0) {
           x.ks = a.kv.k_scale[g.page];
-          x.vs = a.kv.v_scale[g.page];
+          x.ve = split_scale(a.kv.v_scale[g.page], x.vs);
+          // (a reference only: an error of this makes the largest weight 1 + 2^-21)
+          constexpr float kUnits = (D == 128 ? 11.3137085f : 8.0f) * kLn2;
+          x.lv = x.vs > 0.0f && x.vs < INFINITY ? __log2f(x.vs) * kUnits : 0.0f;
         }
         uint32_t f = group_flags<kTree>(k, g, it.i0, it.i1);
         if (Tr::kQuant && x.ks != x.ks) f |= 1u;     // (a NaN scale of K: the row warps put it into the logits)
@@ -549,10 +553,9 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kRows>::kThreads, RowsTrait
           if (lane >= s && lane < s + kTileGroups) {
             info.base[lane - s] = now.g.base;
             if constexpr (Tr::kQuant) {
-              float m;
-              info.ve[lane - s] = split_scale(now.vs, m);
-              info.ks[lane - s] = now.ks;
-              info.vs[lane - s] = m;
+              info.ve[lane - s] = now.ve;
+              info.ks[lane - s] = make_float2(now.ks, now.lv);
+              info.vs[lane - s] = now.vs;
             }
           }
           if (lane == 0) info.flags = flags;
@@ -853,7 +856,7 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kRows>::kThreads, RowsTrait
                     }
                   }
                   seen |= (bits & 0xffffu) << (16 * y);
-                  if (Tr::kQuant && info.ks[gi] != info.ks[gi]) nan_or_1[y] = info.ks[gi];   // (the weights' bound below drops it)
+                  if (Tr::kQuant && info.ks[gi].x != info.ks[gi].x) nan_or_1[y] = info.ks[gi].x;   // (the weights' bound below drops it)
                 }
                 tmem_wait_ld<32>(x);
                 uint32_t w[32];
@@ -876,7 +879,10 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kRows>::kThreads, RowsTrait
 #pragma unroll
               for (int gi = 0; gi < 4; ++gi) {
                 float of = largest(x + gi * 16);
-                if (Tr::kQuant && of != -INFINITY) of *= info.ks[half * 4 + gi];
+                // (8-bit: of weight times V's mantissa, which is what is rounded to bf16. The reference then
+                // makes the largest of them 1, which rounds to itself: in a model of it rows of 3 to 17 keys
+                // are 1.8 to 1.9e-3 off for 2.3 to 2.4e-3 with the logits' maximum. Costs 0.2 to 0.7 %.)
+                if (Tr::kQuant && of != -INFINITY) of = fmaf(of, info.ks[half * 4 + gi].x, info.ks[half * 4 + gi].y);
                 mx = fmaxf(mx, of);
               }
               return mx;
@@ -890,7 +896,7 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kRows>::kThreads, RowsTrait
               for (int x = 0; x < 16; ++x) {
                 const int gi = c32 * 2 + x / 8;
                 // (a K scale of 0 must not make a NaN of -inf)
-                const float to_log2 = Tr::kQuant ? fmaxf(info.ks[gi] * sc, 1.17549435e-38f) : sc;
+                const float to_log2 = Tr::kQuant ? fmaxf(info.ks[gi].x * sc, 1.17549435e-38f) : sc;
                 const float2 y = __ffma2_rn(make_float2(x32[2 * x], x32[2 * x + 1]), make_float2(to_log2, to_log2), m2);
                 float2 e = make_float2(exp2_approx(y.x), exp2_approx(y.y));
                 sum[x & 1] = __fadd2_rn(sum[x & 1], e);

@@ -83,3 +83,21 @@ def test_a_logit_of_minus_infinity_weighs_nothing(rows):
         s[low] = False
         want = R.attend_row(p.q_np[p.row0[0] + i, g].astype(np.float64), c.K[0][s], c.V[0][s])
         R.check_row(row, float(p.lse[p.row0[0] + i, g]), want, (i, g))
+
+
+@pytest.mark.parametrize("rows", [6, 40, 150])
+@pytest.mark.parametrize("kind", ["e4m3", "int8"])
+def test_a_row_of_one_key_is_its_value_rounded_once(kind, rows):
+    """The first token sees itself alone. Its weight, taken with the V scale's mantissa, is the reference:
+    1 up to the fp32 steps of a logit of a few units and of exp2 (under 2^-18 together), so 1 in bf16, and
+    the quotient is V within 2^-17 before the one rounding to bf16, half a step of 2^-8 of it."""
+    for seed in range(8):
+        c = R.Cache(1, 4, 4, 64, [rows], kind, seed=seed)
+        p = Prefill(c, [rows])
+        p.run()
+        assert _sync_status(c) == 0
+        out = p.out.double().cpu().numpy()[p.row0[0]]
+        for u, g in itertools.product(range(4), range(4)):
+            v = np.asarray(c.V[u][0], np.float64)
+            err = np.abs(out[u * 4 + g] - v)
+            assert (err <= (R.HALF_BF16 + 2.0 ** -16) * np.abs(v)).all(), (seed, u, g, (err / np.maximum(np.abs(v), 1e-30)).max())
