@@ -29,7 +29,7 @@
 // rows HBM: 32 sequences' single tokens over 2K to 16K tokens 164 us, 5.95 TB/s; E4M3 221 us, conversion.
 // Small trees: launch, lookup, copy, products, records and merge one after another, 10.7 us for eight
 // drafts over 32K tokens.
-// Precision: products of bf16 in fp32; weights enter as bf16 (2^-9 of themselves), which is the
+// Precision: products of bf16 in fp32; weights enter as bf16 (off by up to 2^-8 of themselves), which is the
 // operand type of V; their sum is taken before that rounding. Page scales: K's multiplies logits
 // in fp32; V's is m * 2^e, 2^e goes into the bf16 values (exact), m into the weights, so that
 // neither a tiny nor a large scale leaves the type's range on its own.
