@@ -100,11 +100,16 @@ __global__ void __launch_bounds__(kMergeWarps * 32) rows_merge_kernel(const __gr
   };
   load(0);
   float m = -INFINITY;
-  for (int s = lane; s < n; s += 32) m = fmaxf(m, p.rec_ml[rec + s * step].x);
+  bool nan = false;                                        // (a record of NaN logits alone has no maximum)
+  for (int s = lane; s < n; s += 32) {
+    const float2 x = p.rec_ml[rec + s * step];
+    m = fmaxf(m, x.x);
+    nan |= x.y != x.y;
+  }
 #pragma unroll
   for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
   float l = 0.0f, acc[E] = {};
-  if (m != -INFINITY) {
+  if (m != -INFINITY || __any_sync(0xffffffffu, nan)) {
     for (int s0 = 0; s0 < n; s0 += kAtOnce) {
       float w = 0.0f, part = 0.0f;            // lane s: weight and sum of record s0 + s
       if (lane < kAtOnce && s0 + lane < n) {
