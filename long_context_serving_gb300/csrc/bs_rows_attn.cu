@@ -99,11 +99,13 @@ __global__ void __launch_bounds__(kMergeWarps * 32) rows_merge_kernel(const __gr
       for (int e = 0; e < E; ++e) o[s][e] = s0 + s < n ? p.rec_o[(rec + (s0 + s) * step) * D + lane * E + e] : 0.0f;
   };
   load(0);
+  // A record's sum in log2 units; what is merged are means, weighed by sums of at most 1.
+  auto size_of = [](float2 x) -> float { return x.y == 0.0f ? -INFINITY : x.x + log2f(x.y); };
   float m = -INFINITY;
   bool nan = false;                                        // (a record of NaN logits alone has no maximum)
   for (int s = lane; s < n; s += 32) {
     const float2 x = p.rec_ml[rec + s * step];
-    m = fmaxf(m, x.x);
+    m = fmaxf(m, size_of(x));
     nan |= x.y != x.y;
   }
 #pragma unroll
@@ -111,17 +113,16 @@ __global__ void __launch_bounds__(kMergeWarps * 32) rows_merge_kernel(const __gr
   float l = 0.0f, acc[E] = {};
   if (m != -INFINITY || __any_sync(0xffffffffu, nan)) {
     for (int s0 = 0; s0 < n; s0 += kAtOnce) {
-      float w = 0.0f, part = 0.0f;            // lane s: weight and sum of record s0 + s
+      float w = 0.0f;                         // lane s: weight of record s0 + s
       if (lane < kAtOnce && s0 + lane < n) {
         const float2 x = p.rec_ml[rec + (s0 + lane) * step];
-        w = x.x == -INFINITY ? 0.0f : exp2f(x.x - m);
-        part = x.y;
+        w = x.y == 0.0f ? 0.0f : x.y * exp2f(x.x - m);
       }
       if (s0 > 0) load(s0);
 #pragma unroll
       for (int s = 0; s < kAtOnce; ++s) {
         const float ws = __shfl_sync(0xffffffffu, w, s);
-        l = fmaf(__shfl_sync(0xffffffffu, part, s), ws, l);
+        l += ws;
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] = fmaf(o[s][e], ws, acc[e]);
       }

@@ -13,11 +13,12 @@
 // S of the next key tile is issued behind O's update, so with two tiles one's products run beside
 // the other's softmax; weights are handed over in two parts, 96 keys and 32, so that O's update
 // starts while the last are made and the rest of it and S do not wait for much. O is brought to a
-// new maximum only when that has grown by more than 2^8 (weights of at most 256 in between; the final
-// division takes it back), at the start of a tile, when the products in flight are done: O's rescaling
-// through registers is rare and needs no warps of its own. The second half of a tile is measured
-// against the same reference, and only where it passes that by 2^30 is everything brought to its
-// maximum at once.
+// new maximum only when that has grown by more than 2^8 (the final division takes it back), at the
+// start of a tile, when the products in flight are done: O's rescaling through registers is rare and
+// needs no warps of its own. The second half of a tile is measured against the same reference, and
+// only where it passes that by 2^30 is everything brought to its maximum at once. So 64 weights are
+// 2^30 at most, until the next tile's start brings them to 2^8 too: with V up to 2^90 sums stay below
+// 2^127. Records of split rows are divided by their own sums, so that as many as there are can be added.
 // Tiles are 128 rows for the tensor cores' full rate and 128 keys because a product of 128 x 128 takes
 // from shared memory just what that delivers meanwhile (128 bytes a cycle); two row tiles are what
 // tensor memory holds (512 columns: S and O of each, weights over S).
@@ -60,8 +61,8 @@ struct RowsPlan {
   int splits;         // CTAs a block's keys are split over, at most (1: records unused)
   int even;           // > 0: that many CTAs share all items' key tiles (tree_share)
   int record_rows;    // rows of a block, at most
-  float *rec_o;       // [CTA][record_rows][D]: unnormalised outputs
-  float2 *rec_ml;     // [CTA][record_rows]: maximum (log2 units), sum
+  float *rec_o;       // [CTA][record_rows][D]: outputs over the CTA's keys
+  float2 *rec_ml;     // [CTA][record_rows]: reference (log2 units), sum of the weights relative to it
   int4 *heads;        // [item]: CTAs that took part, the first of them, first row, rows
   uint64_t wait_ns;
 };
@@ -995,12 +996,13 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kRows>::kThreads, RowsTrait
             for (int x = 0; x < 32; ++x) {
               if (l == 0.0f) o[x] = 0.0f;      // (a row that has seen nothing: no product may have written its O)
               odd[x % 4] = fmaf(0.0f, o[x], odd[x % 4]);
+              o[x] *= inv;
             }
             if (valid) {
               if (last) {
                 uint32_t w[16];
 #pragma unroll
-                for (int x = 0; x < 16; ++x) w[x] = pack_bf16(o[2 * x] * inv, o[2 * x + 1] * inv);
+                for (int x = 0; x < 16; ++x) w[x] = pack_bf16(o[2 * x], o[2 * x + 1]);
                 __nv_bfloat16 *to = a.out + out_row * D + c * 32;
                 store_sector(to, w, aligned);
                 store_sector(to + 16, w + 8, aligned);
@@ -1040,8 +1042,8 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kRows>::kThreads, RowsTrait
 #pragma unroll
               for (int e = 0; e < D / 32; ++e)
                 if (bad >> e & 1u) {
-                  const float x = ro[e] * exp2f(rm - r_m);
-                  if (last) to[e] = __float2bfloat16_rn(x * r_inv);
+                  const float x = ro[e] * exp2f(rm - r_m) * r_inv;
+                  if (last) to[e] = __float2bfloat16_rn(x);
                   else to_rec[e] = x;
                 }
             }

@@ -1,4 +1,5 @@
-"""Prompt and tree attention where rows are split: rows of NaN through the merge."""
+"""Prompt and tree attention where rows are split: rows of NaN through the merge,
+values at the end of the range in many pieces."""
 import numpy as np
 import pytest
 import torch
@@ -82,3 +83,33 @@ def test_keys_of_nan_are_rows_of_nan(call, form, n, kind):
     if c.B > 1:
         next_ = slice(int(x.row0[1]), int(x.row0[1]) + n)
         assert torch.isfinite(x.out[next_].float()).all() and torch.isfinite(x.lse[next_]).all()
+
+
+def _fill_keys(c, value):
+    """K[t] = value(t) in its first element, 0 in the others (bf16 caches)."""
+    for u, T in ((u, int(c.lens[u // c.Hkv])) for u in range(c.B * c.Hkv)):
+        t = torch.arange(T, device="cuda")
+        at = torch.as_tensor(c.table_np[u].astype(np.int64), device="cuda")[t // 16]
+        c.k[at, t % 16] = 0.0
+        x = np.array([value(i) for i in range(T)])
+        c.k[at, t % 16, 0] = torch.as_tensor(x, device="cuda").bfloat16()
+        c.K[u] = np.zeros((T, c.d))
+        c.K[u][:, 0] = x
+
+
+@pytest.mark.parametrize("call,form,n", [c for c in CASES if c[2] != 20])
+def test_the_largest_values_in_many_pieces(call, form, n):
+    """V of 2^90 where the second half of every key tile passes the first by 2^28.9: a piece's sums are
+    relative to its first half's maximum, and as many of them as there are stay finite together. Every
+    weighted mean is 2^90, a number of bf16, up to the weights' rounding."""
+    c, x = _prefill("bf16", form, n) if call == "prefill" else _tree("bf16", form, n, masks=lambda i, rng: 0)
+    _fill_keys(c, lambda t: 20.0 if t % 128 >= 64 else 0.0)
+    c.v[:] = 2.0 ** 90
+    x.q[:] = 0.0
+    for h in range(c.Hkv * c.G):
+        x.q[:, h * c.d] = 8.0                     # a logit of 8 K / sqrt(64) = K: 20 log2(e) = 28.85
+    x.run()
+    assert _sync_status(c) == 0
+    for b in range(c.B):
+        out = x.out[x.row0[b]:x.row0[b] + n].double()
+        assert ((out - 2.0 ** 90).abs() <= 2 * R.HALF_BF16 * 2.0 ** 90).all(), out.max()
