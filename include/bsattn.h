@@ -648,7 +648,8 @@ bs_status bs_rope_append(const bs_dims *dims, const bs_rope *rope, const void *q
  * n_q_heads * head_dim. out bf16 [n_rows][n_q_heads][head_dim], 16-byte aligned; lse fp32
  * [n_rows][n_q_heads], or NULL. Of cfg: cls, sink_tokens and local_tokens.
  * Weights (with an 8-bit cache times the mantissa of V's scale) are rounded to bf16, off by at most
- * 2^-8 of themselves each, before they meet V; logits, maxima, sums and outputs are fp32 until out's own rounding (values of V up to
+ * 2^-8 of themselves each, before they meet V, and out is divided by their sum as rounded; lse has the
+ * sum before. Logits, maxima, sums and outputs are fp32 until out's own rounding (values of V up to
  * 2^90, whose weighted sums stay finite on the way). An infinity or a NaN of a key that a row
  * does not see does not reach it: where some rows of a block of tokens see such a value and
  * others do not, the others are computed again without it, one by one. A row is not finite in

@@ -31,9 +31,13 @@
 // Small trees: launch, lookup, copy, products, records and merge one after another, 10.7 us for eight
 // drafts over 32K tokens.
 // Precision: products of bf16 in fp32; weights enter as bf16 (off by up to 2^-8 of themselves), which is the
-// operand type of V; their sum is taken before that rounding. Page scales: K's multiplies logits
-// in fp32; V's is m * 2^e, 2^e goes into the bf16 values (exact), m into the weights, so that
-// neither a tiny nor a large scale leaves the type's range on its own.
+// operand type of V. A row is divided by the sum of its weights as they entered, so that the rounding of
+// one that dominates falls out (against a plain form in fp32 with bf16 outputs trees are 1.9e-3 apart for 2.5e-3
+// when divided by the sum before rounding, single tokens 1.7 for 2.3e-3); the other sum is lse's. It costs 4 to 5 %
+// of prompts (half a 16K prompt 671 for 640 us, E4M3 1066 for 1016), 0 to 6 % of trees, 0 to 2 % of single tokens. (Weights
+// in two parts, twice the products of P and V, took 5 to 17 % more of trees, 7 and 28 % of single tokens over bf16 and E4M3.)
+// Page scales: K's multiplies logits in fp32; V's is m * 2^e, 2^e goes into the bf16 values (exact), m
+// into the weights, by their exponent, so that neither a tiny nor a large scale leaves the type's range on its own.
 // A key that a row does not see still stands in its products, with a weight of 0, and 0 times an
 // infinity is a NaN. Slots past the cache's end are zeroed and pages that are not there left out; where
 // a group that rows see differently holds a value that is not finite, the block is marked, and its
@@ -82,6 +86,14 @@ __device__ __forceinline__ void store_sector(void *to, const uint32_t *w, bool a
     reinterpret_cast<uint4 *>(to)[0] = make_uint4(w[0], w[1], w[2], w[3]);
     reinterpret_cast<uint4 *>(to)[1] = make_uint4(w[4], w[5], w[6], w[7]);
   }
+}
+
+// sum + the two bf16 of w, by additions of mixed types (with shifts and masks instead, half a 16K prompt took
+// 723 us for 671). Volatile, so that they stay behind the store of what they add.
+__device__ __forceinline__ void add_bf16x2(float2 &sum, uint32_t w) {
+  asm volatile("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tadd.rn.f32.bf16 %0, lo, %0;\n\tadd.rn.f32.bf16 %1, hi, %1;\n\t}"
+      : "+f"(sum.x), "+f"(sum.y)
+      : "r"(w));
 }
 
 // Is one of eight bf16 infinite or NaN?
@@ -303,8 +315,8 @@ struct TileInfo {
   uint32_t flags;             // bits 0..7: rows differ in what they see of the group, or its end is
                               // past the cache's; 8..15: it is not there; 16..23: it is of drafts
   float2 ks[kTileGroups];     // 8-bit caches: K's scale; log2 of the mantissa of V's, in the logits' units
-  float vs[kTileGroups];                    // that mantissa
-  float ve[kTileGroups];                    // and its power of two
+  float inv_vs[kTileGroups];  // 1 / that mantissa
+  float ve[kTileGroups];      // its power of two
 };
 
 struct RowsShared {
@@ -389,16 +401,16 @@ __device__ __forceinline__ void codes_to_bf16(uint32_t w, bool scaled, float two
   hi = pack_bf16(b.x, b.y);
 }
 
-// A scale as m * 2^e, 2^e returned; m in [1, 2), smaller for a subnormal scale, and what there is
-// for 0, infinity and NaN.
+// A scale as m * 2^e, 2^e with its sign returned; m in [1, 2), smaller for a subnormal scale. 0, infinity
+// and NaN are returned as they are, with m = 1.
 __device__ __forceinline__ float split_scale(float s, float &m) {
   const uint32_t bits = __float_as_uint(s), e = (bits >> 23) & 0xffu;
   if (e == 0xffu || s == 0.0f) {
-    m = s;
-    return 1.0f;
+    m = 1.0f;
+    return s;
   }
-  m = e == 0 ? s * 8.507059173023462e37f : __uint_as_float((bits & 0x807fffffu) | 0x3f800000u);   // (2^126)
-  return __uint_as_float((e == 0 ? 1u : e) << 23);
+  m = e == 0 ? fabsf(s) * 8.507059173023462e37f : __uint_as_float((bits & 0x7fffffu) | 0x3f800000u);   // (2^126)
+  return __uint_as_float((bits & 0x80000000u) | (e == 0 ? 1u : e) << 23);
 }
 
 template <int D, int kKv, int kRows, bool kTree>
@@ -505,7 +517,7 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kRows>::kThreads, RowsTrait
       // three loads one behind another, mostly from memory.
       struct Lookup {
         Group g;
-        float ks, vs, ve, lv;                // as in TileInfo
+        float ks, inv_vs, ve, lv;            // as in TileInfo
         uint32_t differ, absent, drafts;     // of the 32 groups, as in TileInfo::flags
       };
       auto look_up = [&](int j) -> Group {
@@ -516,10 +528,12 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kRows>::kThreads, RowsTrait
         Lookup x{g, 1.0f, 1.0f, 1.0f, 0.0f, 0u, 0u, 0u};
         if (Tr::kQuant && kv == 0 && g.page >= 0) {
           x.ks = a.kv.k_scale[g.page];
-          x.ve = split_scale(a.kv.v_scale[g.page], x.vs);
-          // (a reference only: an error of this makes the largest weight 1 + 2^-21)
+          float vs;
+          x.ve = split_scale(a.kv.v_scale[g.page], vs);
+          // (an error of the logarithm, 2^-21 of the weights, is one of V's scale)
           constexpr float kUnits = (D == 128 ? 11.3137085f : 8.0f) * kLn2;
-          x.lv = x.vs > 0.0f && x.vs < INFINITY ? __log2f(x.vs) * kUnits : 0.0f;
+          x.lv = __log2f(vs) * kUnits;
+          x.inv_vs = __fdividef(1.0f, vs);
         }
         uint32_t f = group_flags<kTree>(k, g, it.i0, it.i1);
         if (Tr::kQuant && x.ks != x.ks) f |= 1u;     // (a NaN scale of K: the row warps put it into the logits)
@@ -556,7 +570,7 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kRows>::kThreads, RowsTrait
             if constexpr (Tr::kQuant) {
               info.ve[lane - s] = now.ve;
               info.ks[lane - s] = make_float2(now.ks, now.lv);
-              info.vs[lane - s] = now.vs;
+              info.inv_vs[lane - s] = now.inv_vs;
             }
           }
           if (lane == 0) info.flags = flags;
@@ -655,7 +669,7 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kRows>::kThreads, RowsTrait
               codes_to_bf16<kKv == 2>(w.w, kv == 1, two_e, hi.z, hi.w);
               put(rows, c, lo, hi);
             }
-            if ((flags & 1u) && kv == 1) odd |= !(fabsf(info.vs[gi]) < INFINITY);
+            if ((flags & 1u) && kv == 1) odd |= !(fabsf(info.ve[gi]) < INFINITY);
             if (flags & 1u)                              // a group that rows see differently
 #pragma unroll 1
               for (int c = 0; c < kPieces; ++c) {
@@ -806,6 +820,7 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kRows>::kThreads, RowsTrait
           if (k.n_draft < 64) mask &= (1ull << k.n_draft) - 1;
         }
         float m = -INFINITY, l = 0.0f;       // reference in the logits' units (times sc: log2), sum
+        float used = 0.0f;                   // sum of the weights as they enter the products
         float pend = -INFINITY;              // maximum of the last second half
         const int n = t_hi - t_lo;
         bool ok = true;
@@ -825,7 +840,7 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kRows>::kThreads, RowsTrait
               for (int c = 0; c < 4; ++c) top[c] = fmaxf(fmaxf(x[c], x[4 + c]), fmaxf(x[8 + c], x[12 + c]));
               return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
             };
-            float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+            float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)}, rounded = make_float2(0.0f, 0.0f);   // this tile's l, used
             if ((flags & 0xffffu) != 0) {
               // Logits of keys that the row does not see become -inf, in tensor memory: most tiles have
               // none, and their code keeps its registers.
@@ -880,34 +895,47 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kRows>::kThreads, RowsTrait
 #pragma unroll
               for (int gi = 0; gi < 4; ++gi) {
                 float of = largest(x + gi * 16);
-                // (8-bit: of weight times V's mantissa, which is what is rounded to bf16. The reference then
-                // makes the largest of them 1, which rounds to itself: in a model of it rows of 3 to 17 keys
-                // are 1.8 to 1.9e-3 off for 2.3 to 2.4e-3 with the logits' maximum. Costs 0.2 to 0.7 %.)
+                // (8-bit: of weight times V's mantissa, which is what is rounded to bf16. A reference that is
+                // the row's maximum then makes the largest of them 1, which rounds to itself: in a model rows
+                // of 3 to 200 keys are 1.8 to 2.0e-3 off for 1.8 to 2.2e-3 with the logits' maximum. Costs 0.2 to 0.7 %.)
                 if (Tr::kQuant && of != -INFINITY) of = fmaf(of, info.ks[half * 4 + gi].x, info.ks[half * 4 + gi].y);
                 mx = fmaxf(mx, of);
               }
               return mx;
             };
-            // Weights of keys [32 c32, + 32), over the first logits.
+            // Weights of keys [32 c32, + 32), over the first logits (8-bit: times V's mantissa, through
+            // the exponent; both sums are of weights without it).
             auto weigh = [&](int c32, const float *x32) {
               const float base_m = m == -INFINITY ? 0.0f : -m * sc;
-              const float2 m2 = make_float2(base_m, base_m);
               uint32_t w[16];
 #pragma unroll
-              for (int x = 0; x < 16; ++x) {
-                const int gi = c32 * 2 + x / 8;
+              for (int y = 0; y < 2; ++y) {
+                const int gi = c32 * 2 + y;
                 // (a K scale of 0 must not make a NaN of -inf)
                 const float to_log2 = Tr::kQuant ? fmaxf(info.ks[gi].x * sc, 1.17549435e-38f) : sc;
-                const float2 y = __ffma2_rn(make_float2(x32[2 * x], x32[2 * x + 1]), make_float2(to_log2, to_log2), m2);
-                float2 e = make_float2(exp2_approx(y.x), exp2_approx(y.y));
-                sum[x & 1] = __fadd2_rn(sum[x & 1], e);
-                if constexpr (Tr::kQuant) {
-                  const float vs = info.vs[gi];
-                  e = __fmul2_rn(e, make_float2(vs, vs));
+                const float from = Tr::kQuant ? fmaf(info.ks[gi].y, sc, base_m) : base_m;
+                float2 exact = make_float2(0.0f, 0.0f);                // of the group (8-bit)
+#pragma unroll
+                for (int x = 8 * y; x < 8 * y + 8; ++x) {
+                  const float2 z = __ffma2_rn(make_float2(x32[2 * x], x32[2 * x + 1]), make_float2(to_log2, to_log2), make_float2(from, from));
+                  const float2 e = make_float2(exp2_approx(z.x), exp2_approx(z.y));
+                  if constexpr (Tr::kQuant) exact = __fadd2_rn(exact, e);
+                  else sum[x & 1] = __fadd2_rn(sum[x & 1], e);
+                  w[x] = pack_bf16(e.x, e.y);
                 }
-                w[x] = pack_bf16(e.x, e.y);
+                if constexpr (Tr::kQuant) sum[0] = __ffma2_rn(exact, make_float2(info.inv_vs[gi], info.inv_vs[gi]), sum[0]);
               }
               tmem_st16(s_at + c32 * 16, w);
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {
+                float2 taken = make_float2(0.0f, 0.0f);
+#pragma unroll
+                for (int x = 8 * y; x < 8 * y + 8; ++x) {
+                  if constexpr (Tr::kQuant) add_bf16x2(taken, w[x]);
+                  else add_bf16x2(rounded, w[x]);
+                }
+                if constexpr (Tr::kQuant) rounded = __ffma2_rn(taken, make_float2(info.inv_vs[c32 * 2 + y], info.inv_vs[c32 * 2 + y]), rounded);
+              }
             };
             auto hand_over = [&](int part) {
               tmem_wait_st();
@@ -924,6 +952,7 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kRows>::kThreads, RowsTrait
               const float f = to == m ? 1.0f : exp2_approx((m - to) * sc);
               m = to;
               l *= f;
+              used *= f;
               if (j > 0) {
 #pragma unroll 1
                 for (int c = 0; c < D / 16; ++c) {
@@ -952,6 +981,7 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kRows>::kThreads, RowsTrait
               const float f = rescale(far ? pend : m);
               sum[0] = __fmul2_rn(sum[0], make_float2(f, f));
               sum[1] = __fmul2_rn(sum[1], make_float2(f, f));
+              rounded = __fmul2_rn(rounded, make_float2(f, f));
               tmem_wait_st();
 #pragma unroll 1
               for (int c = 0; c < 2; ++c) {
@@ -972,6 +1002,7 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kRows>::kThreads, RowsTrait
             weigh(3, second + 32);
             hand_over(1);
             l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+            used += rounded.x + rounded.y;
           } else if (lane == 0) {
             mbar_arrive(&sh.p_full[t][0]);
             mbar_arrive(&sh.p_full[t][1]);
@@ -984,7 +1015,7 @@ __global__ void __launch_bounds__(RowsTraits<D, kKv, kRows>::kThreads, RowsTrait
           const bool last = it.n_splits == 1;
           const int64_t out_row = (it.r.row0 + i) * a.dims.n_q_heads + it.h * G + gq;
           const int64_t rec = static_cast<int64_t>(blockIdx.x) * p.record_rows + (t * p.tokens * G + row);
-          const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+          const float inv = l == 0.0f ? 0.0f : 1.0f / used;
           float odd[4] = {fabsf(l), 0.0f, 0.0f, 0.0f};     // NaN or infinite when the row's sums are
           const bool aligned = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0, rec_aligned = (reinterpret_cast<uintptr_t>(p.rec_o) & 31) == 0;
 #pragma unroll 1

@@ -1,9 +1,12 @@
 """Prompt and tree attention where rows are split: rows of NaN through the merge,
-values at the end of the range in many pieces."""
+values at the end of the range in many pieces; a key that dominates."""
+import itertools
+
 import numpy as np
 import pytest
 import torch
 
+import _quant as Q
 import _rows as R
 from long_context_serving_gb300 import bsattn as B
 from test_rows_gpu import Prefill, Tree, _sync_status
@@ -113,3 +116,63 @@ def test_the_largest_values_in_many_pieces(call, form, n):
     for b in range(c.B):
         out = x.out[x.row0[b]:x.row0[b] + n].double()
         assert ((out - 2.0 ** 90).abs() <= 2 * R.HALF_BF16 * 2.0 ** 90).all(), out.max()
+
+
+def _two_keys(c, u, a, b, rng):
+    """Unit u with keys of which a has the logit 0 and b one of 4.375 for a query of sqrt(d) in the first
+    place, all others far below; V zero but for b. c.K and c.V, float64, follow."""
+    T = int(c.lens[u // c.Hkv])
+    row = c.table_np[u][:-(-T // 16)]
+    pages = torch.as_tensor(row.astype(np.int64), device="cuda")
+    K, V = np.zeros((T, c.d)), np.zeros((T, c.d))
+    if c.kind == "bf16":
+        K[:, 0], K[a, 0], K[b, 0] = -60.0, 0.0, 4.375
+        V[b] = R.bf16(rng.uniform(1, 2, c.d))
+        for pool, x in ((c.k, K), (c.v, V)):
+            pool[pages] = torch.as_tensor(np.pad(x, ((0, 16 * len(row) - T), (0, 0)))).cuda().bfloat16().view(-1, 16, c.d)
+    else:
+        low, one, scale = (0xFE, 0x50, 4.375 / 8) if c.kind == "e4m3" else (0x81, 64, 4.375 / 64)    # -448 and 8; -127 and 64
+        kc, vc = np.zeros((16 * len(row), c.d), np.uint8), np.zeros((16 * len(row), c.d), np.uint8)
+        kc[:, 0], kc[a, 0], kc[b, 0] = low, 0, one
+        vc[b] = rng.integers(1, 120, c.d)
+        for pool, x in ((c.k, kc), (c.v, vc)):
+            pool.view(torch.uint8)[pages] = torch.as_tensor(x.reshape(-1, 16, c.d)).cuda()
+        c.ks[pages], c.vs[pages] = scale, 1.375
+        K, V = Q.decode(kc[:T], c.kind) * scale, Q.decode(vc[:T], c.kind) * 1.375
+    c.K[u], c.V[u] = K, V
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "int8"])
+@pytest.mark.parametrize("call,form,n", CASES)
+def test_a_key_that_dominates_comes_back(call, form, n, kind):
+    """A first key sets the reference; a later one, in the second half of its tile or in another, weighs
+    2^6.3 times as much, a number that bf16 does not hold. Its share p of the row is over 0.9: both parts of the
+    quotient take the same rounded weight, so that its half step, 2^-8 of it at most, leaves 1 - p of
+    itself, and the other weights as much; logits are within 2^-16 (1 + their terms) in both
+    parts, the result is rounded once, half a step of its own binade."""
+    if call == "prefill" and form == "whole":
+        c = R.Cache(2, 1, 4, 64, [128, 128], kind)
+        x = Prefill(c, [n, n])
+    else:
+        c, x = _prefill(kind, form, n) if call == "prefill" else _tree(kind, form, n, masks=lambda i, rng: 0)
+    H, T = c.Hkv * c.G, int(min(c.lens))
+    qs = R.bf16(np.random.default_rng(3).uniform(7.5, 8.5, (x.rows, H)))
+    x.q[:] = 0.0
+    x.q.view(x.rows, H, c.d)[..., 0] = torch.as_tensor(qs).cuda().bfloat16()
+    for at in sorted({min(66, T - 1), (T - n - 1 if call == "prefill" else T - 1)}):
+        for u in range(c.B * c.Hkv):
+            _two_keys(c, u, 7, at, np.random.default_rng(u))
+        x.run()
+        assert _sync_status(c) == 0
+        out = x.out.double().cpu().numpy()
+        for b, h, i, g in itertools.product(range(c.B), range(c.Hkv), range(n), range(c.G)):
+            u, row = b * c.Hkv + h, int(x.row0[b]) + i
+            seen = int(c.lens[b]) - (n - i - 1 if call == "prefill" else 0)
+            w = np.exp(c.K[u][:seen, 0] * float(qs[row, h * c.G + g]) / np.sqrt(c.d))
+            p = w[at] / w.sum()
+            assert p > 0.9
+            want = p * c.V[u][at]
+            half = 2.0 ** (np.floor(np.log2(np.maximum(np.abs(want), 1e-30))) - 8)
+            tol = half + np.abs(want) * (2 * R.HALF_BF16 * (1 - p) + 2.0 ** -15 * (1 + 5))
+            err = np.abs(out[row, h * c.G + g] - want)
+            assert (err <= tol).all(), (b, h, i, g, at, float((err / half).max()))
