@@ -722,7 +722,9 @@ size_t bs_tree_workspace_size(const bs_dims *dims, int32_t max_draft);
  * the accepted tokens already, so that one path and one pair of lengths serve every layer.
  * Errors as for bs_quant_append; a sequence with more tokens than path_stride
  * (BS_ERR_CAPACITY) or a path entry whose row is outside [0, n_rows) (BS_ERR_DEVICE_BOUNDS) is
- * skipped. One launch; bitwise reproducible. */
+ * skipped. Sub-block means are not touched: call bs_build_block_summaries with the same lengths
+ * before the next step, which renews the one of its own token only. One launch; bitwise
+ * reproducible. */
 bs_status bs_tree_commit(const bs_dims *dims, const bs_pools *pools, const int32_t *page_table,
                          const int32_t *seq_lens, const int32_t *tok_begin, const int32_t *row_begin,
                          const int32_t *path, int32_t path_stride, const void *k_new, const void *v_new,

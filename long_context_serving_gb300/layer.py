@@ -292,7 +292,7 @@ class PagedLayer:
 
     def commit_drafts(self, k_new, v_new, n_draft, path, lens, stream=None) -> None:
         """The accepted drafts of each sequence, path[b] (node numbers, -1 behind the last), enter the
-        cache behind its lens[b] tokens."""
+        cache behind its lens[b] tokens, and the means that the next step scores with follow."""
         n, lens = self._per_sequence("n_draft", n_draft), self._per_sequence("lens", lens)
         path = np.asarray(path, np.int64)
         if path.ndim != 2 or path.shape[0] != self.wl.B:
@@ -307,6 +307,8 @@ class PagedLayer:
             to, begin, first, nodes = self._i32(lens + live.sum(1)), self._i32(lens), self._i32(np.cumsum(n) - n), self._i32(path)
             B.tree_commit(self.dims, pools, self.page_table, to, begin, first, nodes, path.shape[1], k_new, v_new,
                           k_new.stride(0), rows, self.status, stream)
+            # (a step renews the sub-block of its own token only)
+            B.build_block_summaries(self.dims, self.kv_at(to), self.cfg, begin, path.shape[1], self.summaries, self.status, stream)
 
     def _i32(self, a) -> torch.Tensor:
         return torch.as_tensor(np.ascontiguousarray(a, dtype=np.int32), device=self.device)
