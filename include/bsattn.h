@@ -595,7 +595,9 @@ bs_status bs_pages_copy(const bs_dims *dims, const bs_pools *pools, const bs_pag
  * Rows. New tokens of all sequences are packed rows; those of sequence b start at row
  * row_begin[b]. A row holds the heads of one token; row_stride (elements) lets q, k and v
  * be columns of one fused projection's output. Rows that belong to no sequence are
- * neither read for a result nor written.
+ * neither read for a result nor written. A call with n_rows = 0 does nothing (a commit reports
+ * sequences that name rows all the same), and the arrays that have a place a row may be NULL (in
+ * bs_quant_append too).
  * ------------------------------------------------------------------------------ */
 
 /* Norm and rotation of queries and keys (host struct; device pointers). Pair i, i <

@@ -353,12 +353,12 @@ bs_status commit_rows(const AppendArgs &a, cudaStream_t cs) {
   return launch_ex(kernel, grid, kAppendThreads, 0, cs, 0, true, a) == cudaSuccess ? BS_OK : BS_ERR_CUDA;
 }
 
-// Host checks that both appends share (after those of the dims).
+// Host checks that both appends share (after those of the dims). Arrays of no rows have no address.
 bs_status check_append(const bs_dims *dims, const bs_pools *pools, const void *page_table, const void *seq_lens,
                        const void *tok_begin, const void *row_begin, const void *k_new, const void *v_new,
                        int64_t row_stride, int64_t n_rows, const void *dev_status) {
-  if (!pools || !pools->k_pool || !pools->v_pool || !page_table || !seq_lens || !tok_begin || !row_begin || !k_new ||
-      !v_new || !dev_status)
+  if (!pools || !pools->k_pool || !pools->v_pool || !page_table || !seq_lens || !tok_begin || !row_begin || !dev_status ||
+      (n_rows != 0 && (!k_new || !v_new)))
     return BS_ERR_INVALID_ARG;
   if (is_quant(dims->kv_dtype) && (!pools->k_scale || !pools->v_scale)) return BS_ERR_INVALID_ARG;
   if (n_rows < 0 || row_stride < static_cast<int64_t>(dims->n_kv_heads) * dims->head_dim) return BS_ERR_INVALID_ARG;

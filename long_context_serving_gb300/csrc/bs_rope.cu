@@ -228,11 +228,13 @@ extern "C" bs_status bs_rope_append(const bs_dims *dims, const bs_rope *rope, co
   using namespace bsi;
   bs_status s = check_dims(dims);
   if (s != BS_OK) return s;
-  if (!rope || !rope->inv_freq || !q || !k || !positions || !q_out || !dev_status) return BS_ERR_INVALID_ARG;
+  if (n_rows < 0 || n_rows > (int64_t(1) << 40)) return BS_ERR_INVALID_ARG;
+  const bool some = n_rows > 0;      // (arrays of no rows have no address)
+  if (!rope || !rope->inv_freq || !dev_status || (some && (!q || !k || !positions || !q_out))) return BS_ERR_INVALID_ARG;
   if (pools != nullptr) {
     if (is_quant(dims->kv_dtype)) return BS_ERR_INVALID_ARG;
-    if (!pools->k_pool || !pools->v_pool || !page_table || !row_seq || !v) return BS_ERR_INVALID_ARG;
-  } else if (!k_out) {
+    if (!pools->k_pool || !pools->v_pool || !page_table || (some && (!row_seq || !v))) return BS_ERR_INVALID_ARG;
+  } else if (some && !k_out) {
     return BS_ERR_INVALID_ARG;
   }
   if (rope->rot_dim < 16 || rope->rot_dim > dims->head_dim || rope->rot_dim % 16 != 0) return BS_ERR_SHAPE;
@@ -240,7 +242,6 @@ extern "C" bs_status bs_rope_append(const bs_dims *dims, const bs_rope *rope, co
   // (written so that NaN fails too)
   if (!(rope->eps >= 0.0f && rope->eps <= 3.4e38f) || !(rope->magnitude >= -3.4e38f && rope->magnitude <= 3.4e38f))
     return BS_ERR_INVALID_ARG;
-  if (n_rows < 0 || n_rows > (int64_t(1) << 40)) return BS_ERR_INVALID_ARG;
   if (row_stride < static_cast<int64_t>(dims->n_q_heads) * dims->head_dim) return BS_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k) || (pools && (!aligned16(v) || !aligned16(pools->k_pool) || !aligned16(pools->v_pool))) ||
       !aligned16(q_out) || (k_out && !aligned16(k_out)) || row_stride % (dims->q_dtype == BS_FP32 ? 4 : 8) != 0 ||

@@ -177,12 +177,12 @@ bs_status launch_rows(RowsArgs &a, void *workspace, size_t workspace_bytes, cuda
   return launch_ex(merge, grid, kMergeWarps * 32, 0, cs, 0, true, a, h.p) == cudaSuccess ? BS_OK : BS_ERR_CUDA;
 }
 
-// Host checks that both calls share (after those of the dims).
-bs_status check_rows(const bs_dims *dims, const void *q, int64_t q_stride, const bs_kv *kv, const void *cfg,
+// Host checks that both calls share (after those of the dims). Arrays of no rows have no address.
+bs_status check_rows(const bs_dims *dims, const void *q, int64_t q_stride, int64_t n_rows, const bs_kv *kv, const void *cfg,
                      const void *out, const void *dev_status) {
   if (dims->q_dtype != BS_BF16 || dims->kv_dtype == BS_FP32) return BS_ERR_INVALID_ARG;
-  if (!q || !kv || !kv->k_pool || !kv->v_pool || !kv->page_table || !kv->seq_lens || !cfg || !out || !dev_status)
-    return BS_ERR_INVALID_ARG;
+  if (n_rows < 0 || (n_rows > 0 && (!q || !out))) return BS_ERR_INVALID_ARG;
+  if (!kv || !kv->k_pool || !kv->v_pool || !kv->page_table || !kv->seq_lens || !cfg || !dev_status) return BS_ERR_INVALID_ARG;
   if (is_quant(dims->kv_dtype) && (!kv->k_scale || !kv->v_scale)) return BS_ERR_INVALID_ARG;
   if (q_stride < static_cast<int64_t>(dims->n_q_heads) * dims->head_dim) return BS_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(out) || !aligned16(kv->k_pool) || !aligned16(kv->v_pool) || q_stride % 8 != 0)
@@ -213,10 +213,10 @@ extern "C" bs_status bs_prefill_attn(const bs_dims *dims, const void *q, int64_t
   using namespace bsi;
   bs_status s = check_dims(dims);
   if (s != BS_OK) return s;
-  s = check_rows(dims, q, q_stride, kv, cfg, out, dev_status);
+  s = check_rows(dims, q, q_stride, n_rows, kv, cfg, out, dev_status);
   if (s != BS_OK) return s;
   if (!cfg->cls || !cfg->sink_tokens || !cfg->local_tokens || !tok_begin || !row_begin) return BS_ERR_INVALID_ARG;
-  if (n_rows < 0 || max_new_tokens < 1) return BS_ERR_INVALID_ARG;
+  if (max_new_tokens < 1) return BS_ERR_INVALID_ARG;
   if (n_rows > INT32_MAX) return BS_ERR_CAPACITY;
   if (n_rows == 0) return BS_OK;
   RowsArgs a{};
@@ -244,12 +244,12 @@ extern "C" bs_status bs_tree_decode_attn(const bs_dims *dims, const void *q, int
   using namespace bsi;
   bs_status s = check_dims(dims);
   if (s != BS_OK) return s;
-  s = check_rows(dims, q, q_stride, kv, cfg, out, dev_status);
+  if (!drafts) return BS_ERR_INVALID_ARG;
+  s = check_rows(dims, q, q_stride, drafts->n_rows, kv, cfg, out, dev_status);
   if (s != BS_OK) return s;
-  if (!cfg->block_tokens || !sel_idx || !sel_cnt || !drafts || !drafts->k_new || !drafts->v_new || !drafts->row_begin ||
-      !drafts->n_draft || !drafts->visible)
-    return BS_ERR_INVALID_ARG;
-  if (drafts->max_draft < 1 || drafts->max_draft > BS_MAX_DRAFT || drafts->n_rows < 0) return BS_ERR_INVALID_ARG;
+  if (!cfg->block_tokens || !sel_idx || !sel_cnt || !drafts->row_begin || !drafts->n_draft) return BS_ERR_INVALID_ARG;
+  if (drafts->n_rows > 0 && (!drafts->k_new || !drafts->v_new || !drafts->visible)) return BS_ERR_INVALID_ARG;
+  if (drafts->max_draft < 1 || drafts->max_draft > BS_MAX_DRAFT) return BS_ERR_INVALID_ARG;
   if (drafts->row_stride < static_cast<int64_t>(dims->n_kv_heads) * dims->head_dim) return BS_ERR_INVALID_ARG;
   if (!aligned16(drafts->k_new) || !aligned16(drafts->v_new) || drafts->row_stride % 8 != 0 ||
       reinterpret_cast<uintptr_t>(drafts->visible) % 8 != 0)

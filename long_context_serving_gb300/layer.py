@@ -301,6 +301,8 @@ class PagedLayer:
         if (live[:, 1:] & ~live[:, :-1]).any() or (path >= np.maximum(n, 0)[:, None]).any():
             raise ValueError("a path names its own sequence's drafts, and -1 only behind the last")
         rows = int(n.sum())
+        if not live.any():
+            return
         self._check_new(k_new, v_new, rows, torch.float32 if self.dims.q_dtype == B.BS_FP32 else torch.bfloat16)
         pools = self.pools if self.kv8 else B.Pools(k_pool=self.k_pool.data_ptr(), v_pool=self.v_pool.data_ptr())
         with _on(stream):

@@ -89,3 +89,38 @@ def test_the_step_behind_a_commit_scores_what_was_committed(kv8):
     for name in ("scores", "out", "lse", "summaries"):
         assert torch.equal(getattr(a, name).view(torch.int32), getattr(b, name).view(torch.int32)), name
     assert torch.equal(a.sel[0], b.sel[0]) and torch.equal(a.cnt[0], b.cnt[0])
+
+
+@pytest.mark.parametrize("kv8", [None, "int8"])
+def test_appends_of_no_rows(kv8):
+    """No row and no accepted draft is nothing to do; an accepted draft without a row is reported."""
+    wl = make_workload(2, seed=3, T=100)
+    layer = PagedLayer(wl, kv8=kv8)
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    before = layer.k_pool.view(torch.uint8).clone()
+    empty = torch.empty(0, wl.Hkv * wl.d, dtype=torch.bfloat16, device="cuda")
+    pools = layer.pools if kv8 else B.Pools(k_pool=layer.k_pool.data_ptr(), v_pool=layer.v_pool.data_ptr())
+    for accepted, status in ((0, 0), (1, B.BS_ERR_DEVICE_BOUNDS)):
+        B.tree_commit(layer.dims, pools, layer.page_table, i32(50 + accepted), i32(50), i32(0), i32(0, 0), 2, empty, empty,
+                      wl.Hkv * wl.d, 0, layer.status)
+        assert layer.read_status() == status
+        if kv8:
+            layer.status.zero_()
+            B.quant_append(layer.dims, pools, layer.page_table, i32(50 + accepted), i32(50), i32(0), empty, empty, wl.Hkv * wl.d, 0, 1,
+                           layer.status)
+            assert layer.read_status() == status
+    assert torch.equal(before, layer.k_pool.view(torch.uint8))
+
+
+def test_attention_of_no_rows():
+    """Empty tensors, which have no address, give empty results."""
+    wl = make_workload(2, seed=3, T=100)
+    layer = PagedLayer(wl)
+    q = torch.empty(0, wl.Hq, wl.d, dtype=torch.bfloat16, device="cuda")
+    kv = torch.empty(0, wl.Hkv * wl.d, dtype=torch.bfloat16, device="cuda")
+    assert q.data_ptr() == 0
+    for out, lse in (layer.prefill_attend(q, [99], [99]),
+                     layer.draft_attend(q, kv, kv, [0], torch.empty(0, dtype=torch.int64, device="cuda"), [99])):
+        assert out.shape == (0, wl.Hq, wl.d) and lse.shape == (0, wl.Hq)
+    layer.commit_drafts(kv, kv, [0], [[-1]], [99])
+    assert layer.read_status() == 0
