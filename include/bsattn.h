@@ -617,7 +617,8 @@ typedef struct {
  *   x' = x * rsqrt(mean(x^2) + eps) * weight (x where the weight is NULL);
  *   (a, b) of each pair -> m (a cos - b sin), m (b cos + a sin), m = magnitude;
  * rounded once, to q_dtype in q_out and k_out, to kv_dtype in the cache. The angle keeps
- * its fraction of a turn to 2^-24 whatever the position (below 2^24).
+ * its fraction of a turn to 2^-24 whatever the position (below 2^24) where |inv_freq| is at most 1,
+ * to 2^-23 up to 32.
  * q rows: n_q_heads * head_dim elements at q + r * row_stride; k and v rows likewise with
  * n_kv_heads. positions int32 [n_rows], 0 .. 2^24 - 1. row_seq int32 [n_rows]: the row's
  * sequence, < 0 for a padding row, which is skipped; NULL (only without pools): no

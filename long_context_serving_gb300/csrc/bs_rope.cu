@@ -9,10 +9,11 @@
 // Loads of the next heads fly beside this turn's work, a row's first ones beside its angles. Bound by
 // HBM in prompts (29K rows of 28 + 8 heads, bf16: 97 us, 5.5 TB/s, with norms 99; fp32 6.25 TB/s), by one
 // chain of loads in decode steps (64 rows with norms, 3.1 us in a graph).
-// Angles: position * inv_freq in turns, inv_freq / 2 pi held as two floats (high and low part,
-// from one fp64 product a frequency and block), the product's rounding error taken back by an
-// fma: the fraction of a turn is right to 2^-24 at any position below 2^24, without fp64 in the
-// loop (fp64 runs at 1/64 of fp32's rate here).
+// Angles: position * inv_freq in turns, inv_freq / 2 pi, less its whole turns, held as two floats (high
+// and low part, from one fp64 product a frequency and block), the product's rounding error taken back by
+// an fma: the fraction of a turn is right to 2^-24 at any position below 2^24 for frequencies of up to
+// a radian (parts of 1/4 a turn: roundings of 2^-25, 2^-27 and less), to 2^-23 up to 32 radians (parts of 1/2 a turn
+// and fp64's own 2^-52 of the angle), without fp64 in the loop (fp64 runs at 1/64 of fp32's rate here).
 #include "bs_attn_launch.cuh"
 #include "bs_rows.cuh"
 
@@ -49,7 +50,8 @@ __global__ void __launch_bounds__(kRopeThreads, Q32 ? 2 : 3) rope_kernel(const _
   asm volatile("griddepcontrol.wait;" ::: "memory");      // everything before this call has finished
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x < rot / 2) {
-    const double f = a.rope.inv_freq[threadIdx.x] * 0.15915494309189533577;   // 1 / (2 pi)
+    const double turn = a.rope.inv_freq[threadIdx.x] * 0.15915494309189533577;   // 1 / (2 pi)
+    const double f = turn - rint(turn);           // (positions are whole: whole turns fall out)
     const float hi = static_cast<float>(f);
     turns[threadIdx.x] = make_float2(hi, static_cast<float>(f - hi));
   }

@@ -1,5 +1,6 @@
 """Prompt and tree attention where rows are split: rows of NaN through the merge,
-values at the end of the range in many pieces; a key that dominates."""
+values at the end of the range in many pieces; a key that dominates; and rotation by
+more than a turn a position."""
 import itertools
 
 import numpy as np
@@ -8,6 +9,7 @@ import torch
 
 import _quant as Q
 import _rows as R
+from _rows import i32
 from long_context_serving_gb300 import bsattn as B
 from test_rows_gpu import Prefill, Tree, _sync_status
 
@@ -176,3 +178,28 @@ def test_a_key_that_dominates_comes_back(call, form, n, kind):
             tol = half + np.abs(want) * (2 * R.HALF_BF16 * (1 - p) + 2.0 ** -15 * (1 + 5))
             err = np.abs(out[row, h * c.G + g] - want)
             assert (err <= tol).all(), (b, h, i, g, at, float((err / half).max()))
+
+
+@pytest.mark.parametrize("inter", [False, True])
+def test_rotation_by_more_than_a_turn_a_position(inter):
+    """Frequencies up to 32 radians a position at positions near 2^24: the angle's fraction of a turn is
+    right to 2^-23 (2^-24 up to one radian), sine and cosine in fp32 to 2^-22."""
+    d, rows = 64, 4096
+    freq = np.zeros(d // 2)
+    freq[:8] = [1.0, 0.77, 2 * np.pi, 3.3, 10.7, 25.1327, 31.9, 32.0]
+    c = R.Cache(1, 1, 1, d, [16], "bf16", q_dtype=B.BS_FP32)
+    pos = np.random.default_rng(1).integers(1 << 23, 1 << 24, rows)
+    x = torch.zeros(rows, 3, d, device="cuda")
+    x[:, :, 0 if inter else 0:(16 if inter else 8):2 if inter else 1] = 1.0       # the first of each pair
+    q, k = torch.empty(rows, 1, d, device="cuda"), torch.empty(rows, 1, d, device="cuda")
+    f_t = torch.as_tensor(freq, device="cuda")
+    rope = B.Rope(inv_freq=f_t.data_ptr(), rot_dim=d, interleaved=int(inter), magnitude=1.0, eps=0.0)
+    B.rope_append(c.dims, rope, x, x[:, 1], x[:, 2], 3 * d, rows, i32(pos), None, None, None, q, k, c.status)
+    assert _sync_status(c) == 0
+    got = q[:, 0].double().cpu().numpy()
+    a, b = (got[:, 0:16:2], got[:, 1:16:2]) if inter else (got[:, :8], got[:, d // 2:d // 2 + 8])
+    wide = np.longdouble
+    turns = pos[:, None].astype(wide) * freq[:8].astype(wide) * wide("0.15915494309189533576888376337251436")
+    angle = (2 * np.pi * (turns - np.rint(turns))).astype(np.float64)
+    tol = 2 * np.pi * np.where(freq[:8] <= 1, 2.0 ** -24, 2.0 ** -23) + 2.0 ** -22
+    assert (np.abs(a - np.cos(angle)) <= tol).all() and (np.abs(b - np.sin(angle)) <= tol).all()
