@@ -675,7 +675,11 @@ bs_status bs_prefill_attn(const bs_dims *dims, const void *q, int64_t q_stride, 
                           int32_t max_new_tokens, void *out, float *lse, void *workspace, size_t workspace_bytes,
                           int32_t *dev_status, bs_stream_t stream);
 
-/* Bytes of workspace bs_prefill_attn needs (0 on bad arguments, or when it needs none). */
+/* Bytes of workspace bs_prefill_attn needs on the current device (0 on bad arguments, or when it
+ * needs none). Not monotonic: only calls whose rows leave CTAs without work split them, so that a
+ * long prompt may need none where a single token needs some. A loop that keeps one workspace sizes it
+ * for every shape that it calls with, each with its own n_rows and max_new_tokens, and takes the
+ * largest; no call needs more than 66 MiB and 16 bytes for each KV head of a block of rows. */
 size_t bs_prefill_workspace_size(const bs_dims *dims, int64_t n_rows, int32_t max_new_tokens);
 
 /* Largest tree of drafts of one sequence. */

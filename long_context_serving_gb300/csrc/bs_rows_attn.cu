@@ -6,10 +6,9 @@ namespace bsi {
 namespace {
 
 // ---------------------------------------------------------------------------------------
-// Plan: from host-known bounds only (n_rows, the most tokens of a sequence, the dims).
+// Plan: from host-known bounds only (n_rows, the most tokens of a sequence, the dims) and the current
+// device's SMs.
 // ---------------------------------------------------------------------------------------
-constexpr int kSms = 152;
-
 struct HostPlan {
   RowsPlan p;
   int rows;                // rows of a CTA: 32, 128 or 256
@@ -37,20 +36,21 @@ HostPlan plan_rows(const bs_dims &d, int64_t n_rows, int max_new, bool tree) {
     tiles = (static_cast<int64_t>(d.max_pages_per_unit) + kTileGroups - 1) / kTileGroups;
   }
   h.p.record_rows = (max_new < h.p.block_tokens ? max_new : h.p.block_tokens) * G;
-  const int at_once = h.rows == 32 ? 2 * kSms : kSms;                  // CTAs
+  const int at_once = attn_target_ctas() / (h.rows == 32 ? 1 : 2);      // CTAs
   int64_t splits = 1;
   if (tree && h.items * tiles <= at_once) {
     splits = tiles;             // a CTA a tile: no more than a wave whatever the selections are
-  } else if (tree && h.items <= kShareItems && tiles < (1 << 20)) {
+  } else if (tree && h.items <= kShareItems && h.items <= at_once && tiles < (1 << 20)) {
     // One wave over the units' own tiles (128K trees of uneven units: 58 us, an even number of splits
     // 65; working it out takes a CTA 1 to 2 us, which the case above does without: 10.2 us for 12.7).
     h.p.even = at_once;
     splits = tiles;
   } else {
     // What one wave has room for. Fewer rows than a tensor core's worth are bound by memory, and by
-    // how evenly CTAs get their keys: pieces of about 24 tiles (32 sequences of 2K to 16K tokens: 165
-    // us; 48 tiles 174, 12 tiles 167, whole sequences 229), while that is no more than eight waves of CTAs, which leave at once
-    // where a sequence is shorter. Two row tiles are bound by their products, and split no further.
+    // how evenly CTAs get their keys: as many pieces as the longest row that the table can hold has
+    // 24 tiles (32 sequences of 2K to 16K tokens, of 16K at most: 165 us; pieces by 48 tiles 174, by 12 tiles
+    // 167, whole sequences 229), while that is no more than eight waves of CTAs. A shorter sequence is cut
+    // into as many, smaller ones, or into its tiles. Two row tiles are bound by their products, and split no further.
     splits = at_once / h.items;
     if (h.rows < 256 && tiles > 32) {
       const int64_t pieces = (tiles + 23) / 24, room = 8 * at_once / h.items;
