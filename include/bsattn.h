@@ -708,6 +708,9 @@ typedef struct {
  * Selections are those of bs_select_topk (for the root's query, say): ascending, at most
  * max_sel_per_unit blocks and max_gather_pages_per_unit pages (BS_ERR_CAPACITY).
  * workspace: bs_tree_workspace_size bytes, under the rules of bs_prefill_attn's.
+ * Where key tiles are split, the points depend on what the whole batch has selected and drafted, and so
+ * does the order of a row's sums: other sequences change its last bits (the same batch gives the same
+ * bits), unlike bs_prefill_attn's.
  * Skipped: a sequence with n_draft outside 0 .. max_draft or T < 0 (BS_ERR_INVALID_ARG), rows outside
  * [0, n_rows) (BS_ERR_DEVICE_BOUNDS) or more pages than a row (BS_ERR_CAPACITY); a unit whose
  * block_tokens is not a positive multiple of 16 (BS_ERR_INVALID_ARG). A block or page out of

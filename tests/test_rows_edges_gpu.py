@@ -1,6 +1,6 @@
 """Prompt and tree attention where rows are split: rows of NaN through the merge,
-values at the end of the range in many pieces; a key that dominates; and rotation by
-more than a turn a position."""
+values at the end of the range in many pieces; a key that dominates; rotation by more
+than a turn a position; long caches; a tree beside others."""
 import itertools
 
 import numpy as np
@@ -203,3 +203,31 @@ def test_rotation_by_more_than_a_turn_a_position(inter):
     angle = (2 * np.pi * (turns - np.rint(turns))).astype(np.float64)
     tol = 2 * np.pi * np.where(freq[:8] <= 1, 2.0 ** -24, 2.0 ** -23) + 2.0 ** -22
     assert (np.abs(a - np.cos(angle)) <= tol).all() and (np.abs(b - np.sin(angle)) <= tol).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("new", [1, 30, 200])
+def test_prompts_behind_a_long_cache(kind, new):
+    """Tens of thousands of tokens before the new ones, dense and windowed heads."""
+    c = R.Cache(1, 2, 4, 128, [40961], kind)
+    p = Prefill(c, [new], cls=[1, 0], sink=70, local=9000)
+    p.run()
+    assert _sync_status(c) == 0
+    p.check(rows=6)
+
+
+def test_a_tree_beside_others():
+    """Other sequences' selections may move a tree's split points, and so the last bits of its sums: with
+    either it is what the formula gives, the same bits again in the same batch."""
+    for other in (60, 5):
+        c = R.Cache(2, 2, 4, 64, [3000, 3000], "bf16", seed=5, max_gather_pages_per_unit=512)
+        t = Tree(c, [12, 12])
+        t.cnt.copy_(i32([188, 188, other, other]))
+        t.sel[2] = t.sel[3] = list(range(other))
+        t.run()
+        assert _sync_status(c) == 0
+        t.check()
+        first = t.out.clone()
+        t.ws.fill_(0xFF)
+        t.run()
+        assert _sync_status(c) == 0 and torch.equal(first, t.out)
