@@ -628,7 +628,8 @@ typedef struct {
  * the V of a row go to slot position % 16 of the page that page_table names for position /
  * 16 in the row's sequence; no two rows may name one slot. k_out may then be NULL. With
  * pools NULL, k_out takes the keys, and v and page_table are not read (8-bit caches: follow
- * with bs_quant_append; drafts: nothing is written to the cache yet).
+ * with bs_quant_append; drafts: nothing is written to the cache yet). Those calls take K and V of one row
+ * stride: where V is columns of a wider row, copy it to rows like k_out's.
  * A row whose position is outside the range is skipped (BS_ERR_INVALID_ARG), and so is one
  * whose row_seq >= batch (BS_ERR_DEVICE_BOUNDS) or whose position lies past the page table's
  * row (BS_ERR_CAPACITY); a page outside the pool: that head's K and V are not written

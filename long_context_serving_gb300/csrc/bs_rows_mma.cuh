@@ -25,10 +25,10 @@
 // Bounds, measured: with two row tiles, S's and O's products (2,048 cycles a key tile) against a
 // tile's chain of 330 (S ready) + 1,640 to 1,800 (softmax) + 900 cycles, by clock stamps in an
 // instrumented copy of an earlier step: half of a 16K prompt, 8 heads of 4 queries, half of them
-// streaming, 644 to 684 us over several machines, 1.42 to 1.51 PFLOP/s. 8-bit caches
-// wait for conversion and shared memory (windows of four ragged chunks 180 us, bf16 134). With few
-// rows HBM: 32 sequences' single tokens over 2K to 16K tokens 164 us, 5.95 TB/s; E4M3 221 us, conversion.
-// Small trees: launch, lookup, copy, products, records and merge one after another, 10.7 us for eight
+// streaming, 670 to 702 us over several machines, 1.38 to 1.45 PFLOP/s. 8-bit caches
+// wait for conversion and shared memory (windows of four ragged chunks 190 us, bf16 128 to 135). With few
+// rows HBM: 32 sequences' single tokens over 2K to 16K tokens 165 us, 5.9 TB/s; E4M3 225 us, conversion.
+// Small trees: launch, lookup, copy, products, records and merge one after another, 10.9 us for eight
 // drafts over 32K tokens.
 // Precision: products of bf16 in fp32; weights enter as bf16 (off by up to 2^-8 of themselves), which is the
 // operand type of V. A row is divided by the sum of its weights as they entered, so that the rounding of
